@@ -17,6 +17,7 @@
 #include <utility>
 
 #include "../../include/mscl.h"
+#include "failure.hpp"
 #include "kernels.hpp"
 #include "port_proxy.hpp"
 
@@ -740,6 +741,12 @@ mscl_status_t noalloc_geometry(int device, int nranks, NoAllocDevice* out) {
 }
 
 }  // namespace
+
+mscl_status_t mscl::record_failure(mscl_status_t s, const char* msg) { return fail(s, msg); }
+
+void mscl::log_text(int level, const char* msg) {
+  if (log_level() >= level) log_line(level, msg);
+}
 
 extern "C" {
 

@@ -1,0 +1,656 @@
+// Host side of the linear layer and of layer norm (include/mscl.h): argument
+// checks, the choice of kernel, tile and split, and the launches of the
+// kernels in linear.hpp and norm.hpp.  Every entry point returns a status
+// code; nothing here aborts or allocates.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/mscl.h"
+#include "failure.hpp"
+#include "linear.hpp"
+#include "norm.hpp"
+
+namespace {
+
+using namespace mscl;
+
+// ------------------------------------------------------------------ checks
+
+mscl_status_t bad(const char* msg) { return record_failure(MSCL_ERR_INVALID_ARGUMENT, msg); }
+
+mscl_status_t failed_hip(hipError_t e, const char* what) {
+  char text[160];
+  snprintf(text, sizeof text, "%s: %s", what, hipGetErrorString(e));
+  return record_failure(MSCL_ERR_HIP, text);
+}
+
+size_t bytes_of(int dtype) { return dtype == MSCL_FLOAT32 ? 4 : 2; }
+bool known_dtype(int d) { return d == MSCL_FLOAT32 || d == MSCL_FLOAT16 || d == MSCL_BFLOAT16; }
+
+// A buffer of a call: its name for messages, where it lies, whether the call
+// writes it, and the buffer that it may be exactly the same as.
+struct Span {
+  const char* name;
+  uintptr_t first, bytes;
+  bool written;
+  const char* may_be;
+};
+
+struct Spans {
+  Span s[12];
+  int n = 0;
+  mscl_status_t status = MSCL_SUCCESS;
+
+  // rows x cols elements of `e` bytes, `stride` elements apart.  A null
+  // pointer is refused if `needed` and the matrix has elements.
+  void add(const char* name, const void* p, size_t rows, size_t cols, size_t stride, size_t e, bool written,
+           bool needed, const char* may_be = nullptr) {
+    if (status != MSCL_SUCCESS) return;
+    char text[160];
+    if (rows == 0 || cols == 0) return;
+    if (!p) {
+      if (!needed) return;
+      snprintf(text, sizeof text, "%s is null", name);
+      status = bad(text);
+      return;
+    }
+    if (rows > 1 && stride < cols) {
+      snprintf(text, sizeof text, "the row stride of %s is shorter than its rows", name);
+      status = bad(text);
+      return;
+    }
+    // 2^62 bytes bound every product below
+    const size_t most = size_t(1) << 62;
+    const size_t reach = rows > 1 ? rows - 1 : 0;
+    if (cols > most / e || (reach && stride > (most / e - cols) / reach)) {
+      snprintf(text, sizeof text, "the size of %s overflows", name);
+      status = bad(text);
+      return;
+    }
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uintptr_t bytes = (reach * stride + cols) * e;
+    if (a % e) {
+      snprintf(text, sizeof text, "%s is not aligned to its elements", name);
+      status = record_failure(MSCL_ERR_MISALIGNED, text);
+      return;
+    }
+    if (UINTPTR_MAX - a < bytes) {
+      snprintf(text, sizeof text, "%s wraps the address space", name);
+      status = bad(text);
+      return;
+    }
+    s[n++] = Span{name, a, bytes, written, may_be};
+  }
+
+  mscl_status_t check() const {
+    mscl_status_t st = status;
+    for (int i = 1; i < n && st == MSCL_SUCCESS; ++i) st = check_last(i);
+    return st;
+  }
+
+  // Span `i` against those before it.
+  mscl_status_t check_last(int i) const {
+    for (int j = 0; j < i; ++j) {
+      if (!s[i].written && !s[j].written) continue;
+      if (s[i].first >= s[j].first + s[j].bytes || s[j].first >= s[i].first + s[i].bytes) continue;
+      const bool same = s[i].first == s[j].first && s[i].bytes == s[j].bytes;
+      const bool allowed = (s[i].may_be && !strcmp(s[i].may_be, s[j].name)) ||
+                           (s[j].may_be && !strcmp(s[j].may_be, s[i].name));
+      if (same && allowed) continue;
+      char text[160];
+      snprintf(text, sizeof text, "%s and %s overlap", s[j].name, s[i].name);
+      return bad(text);
+    }
+    return MSCL_SUCCESS;
+  }
+
+  // The workspace of a call whose other buffers have passed check().
+  mscl_status_t check_workspace(const void* p, size_t have, size_t need) {
+    if (need == 0) return MSCL_SUCCESS;
+    char text[160];
+    if (!p || have < need) {
+      snprintf(text, sizeof text, "workspace of %zu bytes needed, %zu given", need, p ? have : size_t(0));
+      return bad(text);
+    }
+    if (reinterpret_cast<uintptr_t>(p) % 16)
+      return record_failure(MSCL_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+    add("workspace", p, 1, need, 0, 1, true, true);
+    return status != MSCL_SUCCESS ? status : check_last(n - 1);
+  }
+};
+
+// Compute units of the current device, looked up once per device; the
+// library holds code for gfx950 alone.
+mscl_status_t current_device(int* cus) {
+  constexpr int kMost = 64;
+  static std::atomic<int> known[kMost];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return failed_hip(e, "hipGetDevice");
+  if (dev < 0 || dev >= kMost) return bad("device ordinal out of range");
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    hipDeviceProp_t prop;
+    e = hipGetDeviceProperties(&prop, dev);
+    if (e != hipSuccess) return failed_hip(e, "hipGetDeviceProperties");
+    if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+      return record_failure(MSCL_ERR_UNSUPPORTED, "this library is built for gfx950");
+    n = std::max(1, prop.multiProcessorCount);
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *cus = n;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return failed_hip(e, what);
+  log_text(3, what);
+  return MSCL_SUCCESS;
+}
+
+const char* bytes_at(const void* p) { return static_cast<const char*>(p); }
+char* bytes_at(void* p) { return static_cast<char*>(p); }
+uint64_t ceil_div(uint64_t a, uint64_t b) { return a / b + (a % b != 0); }
+uint64_t round_up(uint64_t a, uint64_t b) { return ceil_div(a, b) * b; }
+
+// Grids are 32-bit; sizes beyond them are refused, not cut.
+constexpr uint64_t kMostGroups = 0x7fffffffu;
+
+// Runs fn(codec) for an element type.
+template <class Fn>
+mscl_status_t with_codec(int dtype, Fn&& fn) {
+  switch (dtype) {
+    case MSCL_FLOAT32: return fn(F32{});
+    case MSCL_FLOAT16: return fn(F16{});
+    default: return fn(BF16{});
+  }
+}
+template <class Fn>
+mscl_status_t with_codecs(int dtype, int param_dtype, Fn&& fn) {
+  if (dtype == MSCL_FLOAT32) return fn(F32{}, F32{});
+  if (dtype == MSCL_FLOAT16) return param_dtype == MSCL_FLOAT32 ? fn(F16{}, F32{}) : fn(F16{}, F16{});
+  return param_dtype == MSCL_FLOAT32 ? fn(BF16{}, F32{}) : fn(BF16{}, BF16{});
+}
+
+// ------------------------------------------------------------------ matrix products
+
+constexpr int kCus = 256;  // of an MI355X: the plans must not depend on a device, as workspaces are sized without one
+
+// How one product m x n x k runs.
+struct ProductPlan {
+  int tile = 64;        // 64 or 128: linear_tile's square
+  uint32_t shares = 1;  // of k
+  uint32_t blocks_per_share = 0;
+  size_t bytes = 0;     // partial sums
+  uint64_t partial_stride = 0;
+};
+
+ProductPlan plan_product(uint64_t m, uint64_t n, uint64_t k, int dtype) {
+  ProductPlan p;
+  const uint64_t block = 128 / bytes_of(dtype);
+  const uint64_t blocks = ceil_div(k, block);
+  const uint64_t big = ceil_div(m, 128) * ceil_div(n, 128);
+  p.tile = big >= kCus ? 128 : 64;
+  const uint64_t tiles = ceil_div(m, p.tile) * ceil_div(n, p.tile);
+  uint64_t shares = 1;
+  if (tiles < 2 * kCus && blocks >= 8) shares = std::min({ceil_div(2 * kCus, tiles), blocks / 4, uint64_t(32)});
+  p.blocks_per_share = static_cast<uint32_t>(ceil_div(blocks, shares));
+  if (p.blocks_per_share == 0) p.blocks_per_share = 1;
+  p.shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(blocks, p.blocks_per_share)));
+  p.partial_stride = round_up(n, 8);
+  if (p.shares > 1) p.bytes = p.shares * m * p.partial_stride * 4;
+  return p;
+}
+
+template <class C, bool kAAlong, bool kBAlong>
+mscl_status_t product(const ProductPlan& p, const Operand& a, const Operand& b, uint64_t k, const Epilogue& e0,
+                      char* workspace, hipStream_t stream) {
+  TileArgs t;
+  t.a = a;
+  t.b = b;
+  t.e = e0;
+  t.k = k;
+  t.e.partial = p.shares > 1 ? reinterpret_cast<float*>(workspace) : nullptr;
+  t.e.partial_stride = p.partial_stride;
+  const uint64_t tm = ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
+  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  t.tiles_m = static_cast<uint32_t>(tm);
+  t.tiles_n = static_cast<uint32_t>(tn);
+  t.blocks_per_share = p.blocks_per_share;
+  const dim3 grid(static_cast<uint32_t>(tm * tn), p.shares);
+  if (p.tile == 128)
+    linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
+  else
+    linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
+  mscl_status_t st = launched("linear_tile");
+  if (st != MSCL_SUCCESS || p.shares == 1) return st;
+  const uint64_t groups = ceil_div(ceil_div(e0.n, C::V) * e0.m, 256);
+  if (groups > kMostGroups) return bad("the matrices have too many tiles");
+  linear_join<C><<<static_cast<uint32_t>(groups), 256, 0, stream>>>(t.e, static_cast<int>(p.shares));
+  return launched("linear_join");
+}
+
+mscl_status_t check_linear(const mscl_linear_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  if (!known_dtype(c->dtype)) return bad("unknown dtype");
+  if (c->activation < MSCL_ACT_NONE || c->activation > MSCL_ACT_SILU) return bad("unknown activation");
+  const size_t e = bytes_of(c->dtype);
+  s.add("x", c->x, c->rows, c->in_features, c->x_stride, e, false, c->out_features != 0);
+  s.add("w", c->w, c->out_features, c->in_features, c->w_stride, e, false, c->rows != 0);
+  s.add("bias", c->bias, 1, c->out_features, 0, e, false, false);
+  s.add("residual", c->residual, c->rows, c->out_features, c->residual_stride, e, false, false);
+  s.add("y", c->y, c->rows, c->out_features, c->y_stride, e, true, true, "residual");
+  s.add("preact", c->preact, c->rows, c->out_features, c->preact_stride, e, true, false);
+  return s.check();
+}
+
+ProductPlan plan_linear(const mscl_linear_t& c) { return plan_product(c.rows, c.out_features, c.in_features, c.dtype); }
+
+// Parts of a backward call's workspace, each from a 256-byte boundary.
+struct BackwardPlan {
+  ProductPlan dx, dw;
+  bool slope = false;  // dz is computed into the workspace
+  uint64_t dz_stride = 0;
+  uint32_t groups = 0, rows_per_group = 0;  // of the bias gradient's partial sums
+  size_t dz_at = 0, sums_at = 0, partial_at = 0, bytes = 0;
+};
+
+// Row groups of a pass that sums columns: enough workgroups for the device,
+// but at least 16 rows each, so that the partial sums stay a small part of
+// the traffic.
+void plan_groups(uint64_t rows, uint64_t column_blocks, uint32_t* groups, uint32_t* rows_per_group) {
+  uint64_t want = std::max<uint64_t>(1, ceil_div(4 * kCus, std::max<uint64_t>(1, column_blocks)));
+  uint64_t per = std::max<uint64_t>(16, ceil_div(rows, want));
+  per = std::max(per, ceil_div(rows, 65535));
+  *rows_per_group = static_cast<uint32_t>(std::min<uint64_t>(per, 0xffffffffu));
+  *groups = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(rows, *rows_per_group)));
+}
+
+BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
+  BackwardPlan p;
+  const size_t e = bytes_of(c.dtype);
+  p.slope = c.activation != MSCL_ACT_NONE && (c.dx || c.dw);
+  size_t at = 0;
+  if (p.slope) {
+    p.dz_stride = round_up(c.out_features, 64);
+    p.dz_at = at;
+    at = round_up(at + c.rows * p.dz_stride * e, 256);
+  }
+  if (c.dbias) {
+    plan_groups(c.rows, ceil_div(c.out_features, 64 * (16 / e)), &p.groups, &p.rows_per_group);
+    p.sums_at = at;
+    at = round_up(at + size_t(p.groups) * c.out_features * 4, 256);
+  }
+  p.partial_at = at;
+  size_t partial = 0;
+  if (c.dx) {
+    p.dx = plan_product(c.rows, c.in_features, c.out_features, c.dtype);
+    partial = std::max(partial, p.dx.bytes);
+  }
+  if (c.dw) {
+    p.dw = plan_product(c.out_features, c.in_features, c.rows, c.dtype);
+    partial = std::max(partial, p.dw.bytes);
+  }
+  p.bytes = at + partial;
+  return p;
+}
+
+mscl_status_t check_linear_backward(const mscl_linear_backward_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  if (!known_dtype(c->dtype)) return bad("unknown dtype");
+  if (c->activation < MSCL_ACT_NONE || c->activation > MSCL_ACT_SILU) return bad("unknown activation");
+  const size_t e = bytes_of(c->dtype);
+  const bool some = c->dx || c->dw || c->dbias;
+  s.add("dy", c->dy, c->rows, c->out_features, c->dy_stride, e, false, some);
+  if (c->dw) s.add("x", c->x, c->rows, c->in_features, c->x_stride, e, false, c->out_features != 0);
+  if (c->dx) s.add("w", c->w, c->out_features, c->in_features, c->w_stride, e, false, c->rows != 0);
+  if (c->activation != MSCL_ACT_NONE)
+    s.add("preact", c->preact, c->rows, c->out_features, c->preact_stride, e, false, some);
+  s.add("dx", c->dx, c->rows, c->in_features, c->dx_stride, e, true, false);
+  s.add("dw", c->dw, c->out_features, c->in_features, c->dw_stride, e, true, false);
+  s.add("dbias", c->dbias, 1, c->out_features, 0, e, true, false);
+  return s.check();
+}
+
+// ------------------------------------------------------------------ layer norm
+
+mscl_status_t check_params(int dtype, int param_dtype, size_t width) {
+  if (!known_dtype(dtype) || !known_dtype(param_dtype)) return bad("unknown dtype");
+  if (param_dtype != dtype && param_dtype != MSCL_FLOAT32) return bad("param_dtype must be dtype or MSCL_FLOAT32");
+  if (width == 0) return bad("width must be at least 1");
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t check_layer_norm(const mscl_layer_norm_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  mscl_status_t st = check_params(c->dtype, c->param_dtype, c->width);
+  if (st != MSCL_SUCCESS) return st;
+  if (!(c->eps >= 0.0)) return bad("eps must be at least 0");
+  const size_t e = bytes_of(c->dtype), pe = bytes_of(c->param_dtype);
+  s.add("x", c->x, c->rows, c->width, c->x_stride, e, false, true);
+  s.add("weight", c->weight, 1, c->width, 0, pe, false, false);
+  s.add("bias", c->bias, 1, c->width, 0, pe, false, false);
+  s.add("y", c->y, c->rows, c->width, c->y_stride, e, true, true, "x");
+  s.add("mean", c->mean, 1, c->rows, 0, 4, true, false);
+  s.add("rstd", c->rstd, 1, c->rows, 0, 4, true, false);
+  return s.check();
+}
+
+mscl_status_t check_layer_norm_backward(const mscl_layer_norm_backward_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  mscl_status_t st = check_params(c->dtype, c->param_dtype, c->width);
+  if (st != MSCL_SUCCESS) return st;
+  const size_t e = bytes_of(c->dtype), pe = bytes_of(c->param_dtype);
+  const bool some = c->dx || c->dweight || c->dbias;
+  s.add("dy", c->dy, c->rows, c->width, c->dy_stride, e, false, some);
+  s.add("x", c->x, c->rows, c->width, c->x_stride, e, false, some);
+  s.add("mean", c->mean, 1, c->rows, 0, 4, false, some);
+  s.add("rstd", c->rstd, 1, c->rows, 0, 4, false, some);
+  s.add("weight", c->weight, 1, c->width, 0, pe, false, false);
+  s.add("dx", c->dx, c->rows, c->width, c->dx_stride, e, true, false, "dy");
+  s.add("dweight", c->dweight, 1, c->width, 0, pe, true, false);
+  s.add("dbias", c->dbias, 1, c->width, 0, pe, true, false);
+  return s.check();
+}
+
+struct NormBackPlan {
+  bool sums = false;
+  uint32_t groups = 0, rows_per_group = 0;
+  uint64_t sums_stride = 0;
+  size_t bytes = 0;
+};
+
+NormBackPlan plan_layer_norm_backward(const mscl_layer_norm_backward_t& c) {
+  NormBackPlan p;
+  p.sums = c.dweight || c.dbias;
+  if (!p.sums) return p;
+  plan_groups(c.rows, ceil_div(c.width, 64 * (16 / bytes_of(c.dtype))), &p.groups, &p.rows_per_group);
+  p.sums_stride = round_up(c.width, 4);
+  p.bytes = size_t(p.groups) * 2 * p.sums_stride * 4;
+  return p;
+}
+
+// A row's 16-byte vectors -> threads and vectors per thread that hold it.
+template <class C, class P>
+void launch_norm(const NormArgs& a, hipStream_t s) {
+  const uint64_t vecs = ceil_div(a.width, C::V);
+  const uint32_t rows = static_cast<uint32_t>(a.rows), quads = static_cast<uint32_t>(ceil_div(a.rows, 4));
+  if (vecs <= 64)
+    norm_rows<C, P, 64, 1><<<quads, 256, 0, s>>>(a);
+  else if (vecs <= 128)
+    norm_rows<C, P, 64, 2><<<quads, 256, 0, s>>>(a);
+  else if (vecs <= 256)
+    norm_rows<C, P, 256, 1><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 512)
+    norm_rows<C, P, 256, 2><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 1024)
+    norm_rows<C, P, 256, 4><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 2048)
+    norm_rows<C, P, 1024, 2><<<rows, 1024, 0, s>>>(a);
+  else if (vecs <= 4096)
+    norm_rows<C, P, 1024, 4><<<rows, 1024, 0, s>>>(a);
+  else
+    norm_rows_wide<C, P><<<rows, 1024, 0, s>>>(a);
+}
+
+template <class C, class P>
+void launch_norm_back(const NormBackArgs& a, hipStream_t s) {
+  const uint64_t vecs = ceil_div(a.width, C::V);
+  const uint32_t rows = static_cast<uint32_t>(a.rows), quads = static_cast<uint32_t>(ceil_div(a.rows, 4));
+  if (vecs <= 64)
+    norm_back_rows<C, P, 64, 1><<<quads, 256, 0, s>>>(a);
+  else if (vecs <= 128)
+    norm_back_rows<C, P, 64, 2><<<quads, 256, 0, s>>>(a);
+  else if (vecs <= 256)
+    norm_back_rows<C, P, 256, 1><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 512)
+    norm_back_rows<C, P, 256, 2><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 1024)
+    norm_back_rows<C, P, 256, 4><<<rows, 256, 0, s>>>(a);
+  else if (vecs <= 2048)
+    norm_back_rows<C, P, 1024, 2><<<rows, 1024, 0, s>>>(a);
+  else
+    norm_back_rows_wide<C, P><<<rows, 1024, 0, s>>>(a);
+}
+
+mscl_status_t join_columns(int param_dtype, const float* sums, uint64_t stride, uint64_t width, uint32_t groups,
+                           void* first, void* second, uint32_t kinds, hipStream_t stream) {
+  JoinArgs j;
+  j.sums = sums;
+  j.out[0] = bytes_at(first);
+  j.out[1] = bytes_at(second);
+  j.stride = stride;
+  j.width = width;
+  j.groups = groups;
+  j.kinds = kinds;
+  const uint64_t blocks = ceil_div(width, 32);
+  if (blocks > kMostGroups) return bad("the rows are too wide");
+  return with_codec(param_dtype, [&](auto p) {
+    column_join<decltype(p)><<<dim3(static_cast<uint32_t>(blocks), kinds), 256, 0, stream>>>(j);
+    return launched("column_join");
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+mscl_status_t mscl_linear_workspace(const mscl_linear_t* call, size_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  Spans spans;
+  const mscl_status_t st = check_linear(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  *bytes = call->rows && call->out_features ? plan_linear(*call).bytes : 0;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t mscl_linear(const mscl_linear_t* call, void* workspace, size_t workspace_bytes, void* stream) {
+  Spans spans;
+  mscl_status_t st = check_linear(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_linear_t& c = *call;
+  if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
+  const ProductPlan p = plan_linear(c);
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  Epilogue e;
+  memset(&e, 0, sizeof e);
+  e.bias = bytes_at(c.bias);
+  e.residual = bytes_at(c.residual);
+  e.residual_stride = c.residual_stride;
+  e.y = bytes_at(c.y);
+  e.y_stride = c.y_stride;
+  e.z = bytes_at(c.preact);
+  e.z_stride = c.preact_stride;
+  e.m = c.rows;
+  e.n = c.out_features;
+  e.act = c.activation;
+  const Operand a{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
+  const Operand b{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
+  return with_codec(c.dtype, [&](auto t) {
+    return product<decltype(t), true, true>(p, a, b, c.in_features, e, bytes_at(workspace),
+                                            static_cast<hipStream_t>(stream));
+  });
+}
+
+mscl_status_t mscl_linear_backward_workspace(const mscl_linear_backward_t* call, size_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  Spans spans;
+  const mscl_status_t st = check_linear_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  *bytes = plan_linear_backward(*call).bytes;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  Spans spans;
+  mscl_status_t st = check_linear_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_linear_backward_t& c = *call;
+  const BackwardPlan p = plan_linear_backward(c);
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  const bool dx = c.dx && c.rows && c.in_features;
+  const bool dw = c.dw && c.out_features && c.in_features;
+  const bool db = c.dbias && c.out_features;
+  if (!dx && !dw && !db) return MSCL_SUCCESS;
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = bytes_at(workspace);
+  Operand dz{bytes_at(c.dy), c.dy_stride, c.rows, c.out_features};
+  if (db || (p.slope && (dx || dw))) {
+    SlopeArgs a;
+    memset(&a, 0, sizeof a);
+    a.dy = bytes_at(c.dy);
+    a.dy_stride = c.dy_stride;
+    a.z = c.activation != MSCL_ACT_NONE ? bytes_at(c.preact) : nullptr;
+    a.z_stride = c.preact_stride;
+    a.act = c.activation;
+    a.rows = c.rows;
+    a.cols = c.out_features;
+    if (p.slope) {
+      a.dz = ws + p.dz_at;
+      a.dz_stride = p.dz_stride;
+    }
+    uint32_t groups = p.groups;
+    a.rows_per_group = p.rows_per_group;
+    if (db) {
+      a.sums = reinterpret_cast<float*>(ws + p.sums_at);
+      a.sums_stride = c.out_features;
+    } else {
+      plan_groups(c.rows, ceil_div(c.out_features, 64 * (16 / bytes_of(c.dtype))), &groups, &a.rows_per_group);
+    }
+    const uint64_t blocks = ceil_div(c.out_features, 64 * (16 / bytes_of(c.dtype)));
+    if (blocks > kMostGroups) return bad("the matrices have too many tiles");
+    if (blocks) {
+      st = with_codec(c.dtype, [&](auto t) {
+        linear_slope<decltype(t)><<<dim3(static_cast<uint32_t>(blocks), groups), 256, 0, s>>>(a);
+        return launched("linear_slope");
+      });
+      if (st != MSCL_SUCCESS) return st;
+    }
+    if (db) {
+      st = join_columns(c.dtype, a.sums, a.sums_stride, c.out_features, groups, c.dbias, nullptr, 1, s);
+      if (st != MSCL_SUCCESS) return st;
+    }
+    if (p.slope) dz = Operand{ws + p.dz_at, p.dz_stride, c.rows, c.out_features};
+  }
+  Epilogue e;
+  if (dx) {
+    memset(&e, 0, sizeof e);
+    e.y = bytes_at(c.dx);
+    e.y_stride = c.dx_stride;
+    e.m = c.rows;
+    e.n = c.in_features;
+    const Operand b{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
+    st = with_codec(c.dtype, [&](auto t) {
+      return product<decltype(t), true, false>(p.dx, dz, b, c.out_features, e, ws + p.partial_at, s);
+    });
+    if (st != MSCL_SUCCESS) return st;
+  }
+  if (dw) {
+    memset(&e, 0, sizeof e);
+    e.y = bytes_at(c.dw);
+    e.y_stride = c.dw_stride;
+    e.m = c.out_features;
+    e.n = c.in_features;
+    const Operand b{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
+    st = with_codec(c.dtype, [&](auto t) {
+      return product<decltype(t), false, false>(p.dw, dz, b, c.rows, e, ws + p.partial_at, s);
+    });
+  }
+  return st;
+}
+
+mscl_status_t mscl_layer_norm(const mscl_layer_norm_t* call, void* stream) {
+  Spans spans;
+  mscl_status_t st = check_layer_norm(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_layer_norm_t& c = *call;
+  if (c.rows == 0) return MSCL_SUCCESS;
+  if (c.rows > kMostGroups) return bad("too many rows");
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  NormArgs a;
+  a.x = bytes_at(c.x);
+  a.x_stride = c.x_stride;
+  a.w = bytes_at(c.weight);
+  a.b = bytes_at(c.bias);
+  a.y = bytes_at(c.y);
+  a.y_stride = c.y_stride;
+  a.mean = c.mean;
+  a.rstd = c.rstd;
+  a.rows = c.rows;
+  a.width = c.width;
+  a.eps = static_cast<float>(c.eps);
+  return with_codecs(c.dtype, c.param_dtype, [&](auto t, auto p) {
+    launch_norm<decltype(t), decltype(p)>(a, static_cast<hipStream_t>(stream));
+    return launched("norm_rows");
+  });
+}
+
+mscl_status_t mscl_layer_norm_backward_workspace(const mscl_layer_norm_backward_t* call, size_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  Spans spans;
+  const mscl_status_t st = check_layer_norm_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  *bytes = plan_layer_norm_backward(*call).bytes;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t mscl_layer_norm_backward(const mscl_layer_norm_backward_t* call, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  Spans spans;
+  mscl_status_t st = check_layer_norm_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_layer_norm_backward_t& c = *call;
+  const NormBackPlan p = plan_layer_norm_backward(c);
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  if (c.rows > kMostGroups) return bad("too many rows");
+  if (!p.sums && (!c.dx || c.rows == 0)) return MSCL_SUCCESS;
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  NormBackArgs a;
+  a.dy = bytes_at(c.dy);
+  a.dy_stride = c.dy_stride;
+  a.x = bytes_at(c.x);
+  a.x_stride = c.x_stride;
+  a.mean = c.mean;
+  a.rstd = c.rstd;
+  a.w = bytes_at(c.weight);
+  a.dx = bytes_at(c.dx);
+  a.dx_stride = c.dx_stride;
+  a.sums = reinterpret_cast<float*>(workspace);
+  a.sums_stride = p.sums_stride;
+  a.rows = c.rows;
+  a.width = c.width;
+  a.rows_per_group = p.rows_per_group;
+  if (p.sums) {  // before dx, which may be written over dy
+    const uint64_t blocks = ceil_div(c.width, 64 * (16 / bytes_of(c.dtype)));
+    if (blocks > kMostGroups) return bad("the rows are too wide");
+    st = with_codec(c.dtype, [&](auto t) {
+      norm_back_columns<decltype(t)><<<dim3(static_cast<uint32_t>(blocks), p.groups), 256, 0, s>>>(a);
+      return launched("norm_back_columns");
+    });
+    if (st != MSCL_SUCCESS) return st;
+    st = join_columns(c.param_dtype, a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2, s);
+    if (st != MSCL_SUCCESS) return st;
+  }
+  if (!c.dx || c.rows == 0) return MSCL_SUCCESS;
+  return with_codecs(c.dtype, c.param_dtype, [&](auto t, auto q) {
+    launch_norm_back<decltype(t), decltype(q)>(a, s);
+    return launched("norm_back_rows");
+  });
+}
+
+}  // extern "C"

@@ -1,19 +1,20 @@
 """Thin ctypes binding over libmscl.so (C ABI in include/mscl.h).
 
-Argument marshalling only: every step of the AllReduce runs in the HIP
-library.  Names mirror the C entry points without the ``mscl_`` prefix.
+Argument marshalling only: every step of the AllReduce, of the linear layer
+and of layer norm runs in the HIP library.  Names mirror the C entry points without the ``mscl_`` prefix.
 There is no fallback: if the library is missing, loading raises.
 
 Pointers are plain integers (device addresses, e.g. ``tensor.data_ptr()``),
 streams are ``hipStream_t`` values as integers (``torch.cuda.Stream.cuda_stream``;
-0 = default stream).  ``allreduce_tensors`` is a convenience wrapper that
-takes torch tensors and the current torch stream.
+0 = default stream).  ``allreduce_tensors`` and the operators' ``*_tensors``
+are convenience wrappers that take torch tensors and the current torch stream.
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmscl.so")
@@ -39,13 +40,26 @@ ALGO_CODES = {"auto": ALGO_AUTO, "one_shot": ALGO_ONE_SHOT, "two_shot": ALGO_TWO
               "two_shot_fused": ALGO_TWO_SHOT_FUSED, "two_shot_port": ALGO_TWO_SHOT_PORT,
               "two_shot_fused_nobarrier": ALGO_TWO_SHOT_FUSED_NOBARRIER, "two_shot_pertile": ALGO_TWO_SHOT_PERTILE}
 
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATION_CODES = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+                    "silu": ACT_SILU}
+
 # every function include/mscl.h declares
 EXPORTS = (
     "mscl_version", "mscl_status_string", "mscl_last_error_string", "mscl_channel_create",
     "mscl_channel_destroy", "mscl_channel_check", "mscl_channel_reset", "mscl_allreduce",
     "mscl_select_algo", "mscl_channel_plan", "mscl_channel_set_fault_controls", "mscl_channel_set_checks",
     "mscl_reduce_scatter", "mscl_allgather", "mscl_channel_selftest", "mscl_allreduce_noalloc",
+    "mscl_linear", "mscl_linear_workspace", "mscl_linear_backward", "mscl_linear_backward_workspace",
+    "mscl_layer_norm", "mscl_layer_norm_backward", "mscl_layer_norm_backward_workspace",
 )
+
+# the argument records of include/mscl.h, field by field: pointers and sizes
+# ("N": 8 bytes), then the codes ("i")
+LINEAR = struct.Struct("14Nii")
+LINEAR_BACKWARD = struct.Struct("16Nii")
+LAYER_NORM = struct.Struct("10Ndii")
+LAYER_NORM_BACKWARD = struct.Struct("13Nii")
 
 
 class MsclError(RuntimeError):
@@ -110,6 +124,13 @@ def load(path: str = LIB_PATH):
     lib.mscl_channel_set_fault_controls.argtypes = [vp, ctypes.c_uint64, c_int]
     lib.mscl_channel_set_checks.restype = c_int
     lib.mscl_channel_set_checks.argtypes = [vp, c_int, c_int]
+    for name in ("mscl_linear", "mscl_linear_backward", "mscl_layer_norm_backward"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [ctypes.c_char_p, vp, c_size, vp]
+        getattr(lib, name + "_workspace").restype = c_int
+        getattr(lib, name + "_workspace").argtypes = [ctypes.c_char_p, ctypes.POINTER(c_size)]
+    lib.mscl_layer_norm.restype = c_int
+    lib.mscl_layer_norm.argtypes = [ctypes.c_char_p, vp]
     _lib = lib
     return lib
 
@@ -262,3 +283,275 @@ def allreduce_tensors(inputs, outputs, algo: int = ALGO_AUTO, stream=None) -> No
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         allreduce([t.data_ptr() for t in inputs], [t.data_ptr() for t in outputs], t0.numel(), codes[t0.dtype],
                   len(inputs), algo, handle)
+
+
+# ---------------------------------------------------------------- linear layer and layer norm
+
+def _codes():
+    import torch
+
+    return {torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16}
+
+
+def _same_kind(like, **tensors):
+    """Checks shared by the operators' tensors: element type, device."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}")
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must be of {like.dtype}")
+
+
+def _matrix(name, t, cols):
+    """`t` as rows of `cols` elements that lie next to each other: a view where strides allow one."""
+    if t.dim() == 0 or t.shape[-1] != cols:
+        raise ValueError(f"{name} must have {cols} columns")
+    if t.dim() != 2:
+        t = t.reshape(-1, cols) if cols else t.reshape(t.shape[:-1].numel(), 0)
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t
+
+
+def _vector(name, t, n):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _on_stream(device, stream, tensors, run):
+    """run(stream handle) with `device` current and allocations made for `stream` (default: torch's current one)."""
+    import torch
+
+    if stream is None and device.index == torch.cuda.current_device():
+        return run(torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return run(torch.cuda.current_stream(device).cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+            return run(stream.cuda_stream)
+
+
+def _workspace(query, call, like):
+    """The workspace that a call asks for, as (tensor or None, its bytes)."""
+    import torch
+
+    need = ctypes.c_size_t()
+    _check(query(call, ctypes.byref(need)), query.__name__)
+    if need.value == 0:
+        return None, 0
+    return torch.empty(need.value, dtype=torch.uint8, device=like.device), need.value
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _row_stride(t):
+    return 0 if t is None else t.stride(0)
+
+
+def linear_tensors(x, weight, bias=None, residual=None, activation="none", return_preact=False, stream=None):
+    """mscl_linear on torch tensors: activation(x @ weight.T + bias) + residual.
+
+    x is (..., in), weight (out, in), bias (out), residual (..., out), all of
+    one dtype (float32 / float16 / bfloat16) and device; rows may be strided,
+    elements of a row must be contiguous.  activation is a name of
+    ACTIVATION_CODES.  Returns y (..., out), or (y, preact) with return_preact:
+    what linear_backward_tensors needs where there is an activation.
+    """
+    import torch
+
+    lib = load()
+    dtype = _codes().get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    if weight.dim() != 2:
+        raise ValueError("weight must be a matrix")
+    _same_kind(x, weight=weight, bias=bias, residual=residual)
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    n, k = weight.shape
+    xm, wm = _matrix("x", x, k), _matrix("weight", weight, k)
+    rows = xm.shape[0]
+    if bias is not None:
+        _vector("bias", bias, n)
+    rm = None
+    if residual is not None:
+        if residual.shape != x.shape[:-1] + (n,):
+            raise ValueError(f"residual must be {tuple(x.shape[:-1]) + (n,)}")
+        rm = _matrix("residual", residual, n)
+
+    def run(handle):
+        y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+        z = torch.empty_like(y) if return_preact else None
+        call = LINEAR.pack(xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), _address(bias), _address(rm),
+                           _row_stride(rm), y.data_ptr(), n, _address(z), n, rows, k, n, dtype,
+                           ACTIVATION_CODES[activation])
+        space, size = _workspace(lib.mscl_linear_workspace, call, x)
+        _check(lib.mscl_linear(call, _address(space), size, handle or None), "mscl_linear")
+        if x.dim() != 2:
+            y = y.view(x.shape[:-1] + (n,))
+            z = z.view(y.shape) if return_preact else None
+        return (y, z) if return_preact else y
+
+    return _on_stream(x.device, stream, (x, weight, bias, residual), run)
+
+
+def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_dx=True, need_dw=True, need_db=True,
+                            stream=None):
+    """mscl_linear_backward on torch tensors: (dx, dw, db) of linear_tensors.
+
+    dy is the gradient of y (..., out) (and of the residual), preact what
+    linear_tensors returned with return_preact (needed unless activation is
+    "none").  A gradient that is not needed is None.
+    """
+    import torch
+
+    lib = load()
+    dtype = _codes().get(dy.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {dy.dtype}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    if weight.dim() != 2:
+        raise ValueError("weight must be a matrix")
+    if activation != "none" and preact is None:
+        raise ValueError("an activation's gradient needs preact")
+    if activation == "none":
+        preact = None
+    _same_kind(dy, x=x, weight=weight, preact=preact)
+    if not dy.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    n, k = weight.shape
+    gm, xm, wm = _matrix("dy", dy, n), _matrix("x", x, k), _matrix("weight", weight, k)
+    rows = gm.shape[0]
+    if x.shape[:-1] != dy.shape[:-1]:
+        raise ValueError("dy and x must have the same rows")
+    zm = None
+    if preact is not None:
+        if preact.shape != dy.shape:
+            raise ValueError("preact must have dy's shape")
+        zm = _matrix("preact", preact, n)
+
+    def run(handle):
+        dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device) if need_dx else None
+        dw = torch.empty((n, k), dtype=dy.dtype, device=dy.device) if need_dw else None
+        db = torch.empty((n,), dtype=dy.dtype, device=dy.device) if need_db else None
+        call = LINEAR_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(),
+                                    wm.stride(0), _address(zm), _row_stride(zm), _address(dx), k, _address(dw), k,
+                                    _address(db), rows, k, n, dtype, ACTIVATION_CODES[activation])
+        space, size = _workspace(lib.mscl_linear_backward_workspace, call, dy)
+        _check(lib.mscl_linear_backward(call, _address(space), size, handle or None), "mscl_linear_backward")
+        if need_dx and x.dim() != 2:
+            dx = dx.view(x.shape)
+        return dx, dw, db
+
+    return _on_stream(dy.device, stream, (dy, x, weight, preact), run)
+
+
+def _param_code(like, **tensors):
+    """The parameters' type: that of the rows, or float32; None entries say nothing."""
+    import torch
+
+    kinds = {t.dtype for t in tensors.values() if t is not None}
+    if len(kinds) > 1 or not kinds <= {like.dtype, torch.float32}:
+        raise ValueError(f"parameters must all be of {like.dtype} or all of float32")
+    for name, t in tensors.items():
+        if t is not None:
+            if t.device != like.device:
+                raise ValueError(f"{name} must be on {like.device}")
+            _vector(name, t, like.shape[-1])
+    return kinds.pop() if kinds else like.dtype
+
+
+def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, stream=None):
+    """mscl_layer_norm on torch tensors, over the last dimension of x.
+
+    weight and bias have x's dtype or float32.  Returns y, or (y, mean, rstd)
+    with return_stats: float32 of x's leading shape, what
+    layer_norm_backward_tensors needs.
+    """
+    import torch
+
+    lib = load()
+    codes = _codes()
+    if x.dtype not in codes:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension of at least 1")
+    if not eps >= 0:
+        raise ValueError("eps must be at least 0")
+    width = x.shape[-1]
+    param = codes[_param_code(x, weight=weight, bias=bias)]
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    xm = _matrix("x", x, width)
+    rows = xm.shape[0]
+
+    def run(handle):
+        y = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
+        rstd = torch.empty_like(mean) if return_stats else None
+        call = LAYER_NORM.pack(xm.data_ptr(), xm.stride(0), _address(weight), _address(bias), y.data_ptr(), width,
+                               _address(mean), _address(rstd), rows, width, eps, codes[x.dtype], param)
+        _check(lib.mscl_layer_norm(call, handle or None), "mscl_layer_norm")
+        if x.dim() != 2:
+            y = y.view(x.shape)
+        return (y, mean, rstd) if return_stats else y
+
+    return _on_stream(x.device, stream, (x, weight, bias), run)
+
+
+def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, need_dw=True, need_db=True, stream=None):
+    """mscl_layer_norm_backward on torch tensors: (dx, dw, db) of layer_norm_tensors.
+
+    mean and rstd are what it returned with return_stats.  dw and db have
+    weight's dtype (dy's without a weight).  A gradient that is not needed is
+    None.
+    """
+    import torch
+
+    lib = load()
+    codes = _codes()
+    if dy.dtype not in codes:
+        raise ValueError(f"unsupported dtype {dy.dtype}")
+    if dy.dim() == 0 or dy.shape[-1] == 0:
+        raise ValueError("dy must have a last dimension of at least 1")
+    if x.shape != dy.shape:
+        raise ValueError("dy and x must have the same shape")
+    _same_kind(dy, x=x)
+    width = dy.shape[-1]
+    kind = _param_code(dy, weight=weight)
+    if not dy.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.device != dy.device or t.shape != dy.shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, float32, on {dy.device} and {tuple(dy.shape[:-1])}")
+    gm, xm = _matrix("dy", dy, width), _matrix("x", x, width)
+    rows = gm.shape[0]
+
+    def run(handle):
+        dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device) if need_dx else None
+        dw = torch.empty((width,), dtype=kind, device=dy.device) if need_dw else None
+        db = torch.empty((width,), dtype=kind, device=dy.device) if need_db else None
+        call = LAYER_NORM_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), mean.data_ptr(),
+                                        rstd.data_ptr(), _address(weight), _address(dx), width, _address(dw),
+                                        _address(db), rows, width, codes[dy.dtype], codes[kind])
+        space, size = _workspace(lib.mscl_layer_norm_backward_workspace, call, dy)
+        _check(lib.mscl_layer_norm_backward(call, _address(space), size, handle or None), "mscl_layer_norm_backward")
+        if need_dx and dy.dim() != 2:
+            dx = dx.view(dy.shape)
+        return dx, dw, db
+
+    return _on_stream(dy.device, stream, (dy, x, mean, rstd, weight), run)

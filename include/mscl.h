@@ -447,6 +447,150 @@ mscl_status_t mscl_channel_set_checks(mscl_channel_t channel, int check_protocol
  */
 mscl_status_t mscl_channel_selftest(mscl_channel_t channel, uint32_t rounds, uint64_t* mismatches);
 
+/* ------------------------------------------------------------------------
+ * The operators around the AllReduce of a tensor-parallel layer: the linear
+ * layers before it and the layer norm behind it, forward and backward.  They
+ * run on one rank's matrices on the current device, need no channel set and
+ * may run at the same time as each other on different streams (each call
+ * with its own workspace).  The pages are silent on them.
+ *
+ * Matrices are row major: `*_stride` is the distance between rows in
+ * elements (at least the row's length; ignored for a matrix of one row), so
+ * a block of columns of a larger matrix can be given or written as it lies.
+ * Pointers need the alignment of one element.  All sums, statistics and
+ * activations are binary32 (whatever the element type) and each result is
+ * rounded once, to nearest even; the one rounding inside an operator is
+ * named at mscl_linear_backward.  Sums are added in an order fixed by the
+ * sizes and strides alone (no atomics): the same call gives the same bits.
+ * Infinities and NaN propagate as in the formulas, except that an activation
+ * (and its slope) at -infinity is its limit.
+ *
+ * Every call is asynchronous on `stream` (a hipStream_t of the current
+ * device, NULL for the default stream), allocates nothing, and can be
+ * captured into a graph.  `workspace` is device memory of at least the bytes
+ * that the operator's *_workspace function gives for the same call (16-byte
+ * aligned; NULL when that is 0); it is used until the call has finished on
+ * the stream and holds nothing between calls.  Outputs must not overlap
+ * inputs, each other or the workspace, except where said.
+ * Errors of all of them: INVALID_ARGUMENT (a null pointer that is needed, a
+ * stride shorter than its row, an overlap, an unknown dtype or activation,
+ * sizes that overflow, a workspace that is too small), MISALIGNED,
+ * UNSUPPORTED (not a gfx950 GPU), HIP.
+ */
+typedef enum {
+  MSCL_ACT_NONE = 0,
+  MSCL_ACT_RELU = 1,      /* max(z, 0) */
+  MSCL_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  MSCL_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  MSCL_ACT_SILU = 4       /* z / (1 + e^-z) */
+} mscl_activation_t;
+
+typedef struct {
+  const void* x;        /* [rows][in_features] */
+  size_t x_stride;
+  const void* w;        /* [out_features][in_features] */
+  size_t w_stride;
+  const void* bias;     /* [out_features], or NULL */
+  const void* residual; /* [rows][out_features], or NULL */
+  size_t residual_stride;
+  void* y;              /* [rows][out_features] */
+  size_t y_stride;
+  void* preact;         /* [rows][out_features]: receives x w^T + bias, or NULL */
+  size_t preact_stride;
+  size_t rows, in_features, out_features;
+  int dtype;            /* mscl_dtype_t of every matrix */
+  int activation;       /* mscl_activation_t */
+} mscl_linear_t;
+
+/*
+ * y = activation(x w^T + bias) + residual; the activation is taken of the
+ * unrounded sums, also where `preact` keeps them rounded.  `y` may be
+ * `residual` (same pointer and stride).  rows or out_features 0: nothing to
+ * do; in_features 0: the sums are 0.
+ */
+mscl_status_t mscl_linear(const mscl_linear_t* call, void* workspace, size_t workspace_bytes, void* stream);
+mscl_status_t mscl_linear_workspace(const mscl_linear_t* call, size_t* bytes);
+
+typedef struct {
+  const void* dy;       /* [rows][out_features] */
+  size_t dy_stride;
+  const void* x;        /* [rows][in_features]; needed for dw */
+  size_t x_stride;
+  const void* w;        /* [out_features][in_features]; needed for dx */
+  size_t w_stride;
+  const void* preact;   /* [rows][out_features]: what mscl_linear kept; needed unless activation is NONE */
+  size_t preact_stride;
+  void* dx;             /* [rows][in_features], or NULL */
+  size_t dx_stride;
+  void* dw;             /* [out_features][in_features], or NULL */
+  size_t dw_stride;
+  void* dbias;          /* [out_features], or NULL */
+  size_t rows, in_features, out_features;
+  int dtype;
+  int activation;
+} mscl_linear_backward_t;
+
+/*
+ * With dz = dy activation'(preact):  dx = dz w,  dw = dz^T x,  dbias = the
+ * columns' sums of dz.  The gradient of the residual is dy itself.  Where
+ * there is an activation, dz is rounded to the element type before the two
+ * matrix products, as the matrix units take that type (dbias is summed from
+ * the unrounded values): a binary16 dz above 65504 becomes infinite.  At
+ * preact = 0 the slope of RELU is 0.  rows 0: dw and dbias are 0.
+ */
+mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+mscl_status_t mscl_linear_backward_workspace(const mscl_linear_backward_t* call, size_t* bytes);
+
+typedef struct {
+  const void* x;        /* [rows][width] */
+  size_t x_stride;
+  const void* weight;   /* [width] of param_dtype, or NULL for 1 */
+  const void* bias;     /* [width] of param_dtype, or NULL for 0 */
+  void* y;              /* [rows][width] */
+  size_t y_stride;
+  float* mean;          /* [rows]: receives the rows' means, or NULL */
+  float* rstd;          /* [rows]: receives 1 / sqrt(variance + eps), or NULL */
+  size_t rows, width;
+  double eps;           /* >= 0 */
+  int dtype;
+  int param_dtype;      /* dtype, or MSCL_FLOAT32 */
+} mscl_layer_norm_t;
+
+/*
+ * y = (x - mean) rstd weight + bias over each row, the variance being the
+ * mean of (x - mean)^2.  `y` may be `x` (same pointer and stride).  width must be at
+ * least 1; rows 0: nothing to do.  No workspace.
+ */
+mscl_status_t mscl_layer_norm(const mscl_layer_norm_t* call, void* stream);
+
+typedef struct {
+  const void* dy;       /* [rows][width] */
+  size_t dy_stride;
+  const void* x;        /* [rows][width] */
+  size_t x_stride;
+  const float* mean;    /* [rows], as mscl_layer_norm gave them */
+  const float* rstd;    /* [rows] */
+  const void* weight;   /* [width] of param_dtype, or NULL for 1 */
+  void* dx;             /* [rows][width], or NULL */
+  size_t dx_stride;
+  void* dweight;        /* [width] of param_dtype, or NULL */
+  void* dbias;          /* [width] of param_dtype, or NULL */
+  size_t rows, width;
+  int dtype;
+  int param_dtype;
+} mscl_layer_norm_backward_t;
+
+/*
+ * With h = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean of g - h (mean of g h)) over each row,
+ *   dweight = the columns' sums of dy h,  dbias = the columns' sums of dy.
+ * `dx` may be `dy` (same pointer and stride).  rows 0: dweight and dbias are 0.
+ */
+mscl_status_t mscl_layer_norm_backward(const mscl_layer_norm_backward_t* call, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+mscl_status_t mscl_layer_norm_backward_workspace(const mscl_layer_norm_backward_t* call, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif
