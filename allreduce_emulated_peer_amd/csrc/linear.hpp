@@ -456,6 +456,226 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
   }
 }
 
+// ------------------------------------------------------------------ large products of 16-bit types
+
+// 256 x 256 tiles by 8 waves (2 x 4; a wave has 4 x 2 tiles of 16 x 16 in each
+// quarter of the tile), 64 k at a time, memory to LDS without registers in
+// between.  A block of k lies in LDS as four halves: rows 0..127 and
+// 128..255 of A, and of B, 16 KiB each, in Stage's layout; two blocks fill
+// 128 KiB, so one workgroup runs on a compute unit.
+//
+// A block is multiplied in four phases, a quarter of the tile each:
+//   (A0, B0)  (A0, B1)  (A1, B1)  (A1, B0)
+// While a phase's 16 MFMAs run, its wave reads the next phase's new half into
+// registers (B1, A1, the next block's A0, the next block's B0), and the
+// workgroup starts the copy of the half that the phase before has finished
+// with.  So each half is on its way for seven phases (96 KiB in flight per
+// compute unit), every phase waits for all but the 12 newest copies and for
+// its own reads, and one barrier a phase orders both.
+// The second block of a pair finds its first B half where the block before
+// read it to, so the two B register sets change roles from block to block.
+constexpr int kHalfBytes = 128 * 128;
+constexpr int kBlockBytes = 4 * kHalfBytes;
+constexpr int kBigLds = 2 * kBlockBytes;
+
+struct BigArgs {
+  Operand a, b;
+  Epilogue e;
+  uint64_t k;
+  uint32_t tiles_m, tiles_n;
+};
+
+// 16 bytes a lane from memory to LDS, lane l's to lds + 16 l; past the
+// resource's range zeros arrive.  The wait is the caller's (vmcnt).  The
+// compiler's own form of this instruction makes it wait for every copy under
+// way at the next LDS read.  Nothing else in these kernels uses m0.
+__device__ inline void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t lds, uint32_t voffset, uint32_t soffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voffset),
+               "s"(from), "s"(soffset)
+               : "memory");
+}
+
+// One operand's copies: half h of k block t of a 256-row (or -column) tile.
+// Offsets from the tile's start (kAlong) or the block's first row (kDown) fit
+// 31 bits, which the host has checked.  Rows and chunks that do not exist lie
+// past the resource's range, so zeros take their place: rows past the
+// matrix's end by themselves, and the chunks past k of a kAlong row by an
+// offset out of any range.
+template <class C, bool kAlong>
+struct Copier {
+  static constexpr int e = C::kElemBytes;
+  const char* base;  // of the tile
+  uint64_t left;     // bytes from there to the matrix's end
+  uint32_t stride;   // bytes
+  uint32_t blocks;
+  uint32_t voffset;
+  uint32_t last;     // kAlong: voffset in the last block
+
+  __device__ inline void init(const Operand& o, uint64_t first, uint64_t k, uint32_t blocks_, int wave) {
+    const int lane = threadIdx.x & 63;
+    stride = static_cast<uint32_t>(o.stride * e);
+    blocks = blocks_;
+    const uint64_t at = kAlong ? first * stride : first * e;
+    base = o.base + at;
+    left = (o.rows - 1) * o.stride * e + o.cols * e - at;
+    if constexpr (kAlong) {
+      const int chunk = (lane & 7) ^ (lane >> 3);
+      voffset = (wave * 8 + (lane >> 3)) * stride + chunk * 16;
+      last = static_cast<uint64_t>(blocks - 1) * 64 + chunk * C::V < k ? voffset : kNowhere;
+    } else {
+      const int row = wave * 4 + (lane >> 4);
+      voffset = row * stride + Stage<C, false, 128, 512>::swizzle(row, lane & 15) * 16;
+      last = voffset;
+    }
+  }
+
+  static constexpr uint32_t kNowhere = 0xf0000000u;
+
+  static __device__ inline __amdgpu_buffer_rsrc_t range(const char* from, uint64_t bytes) {
+    const uint32_t n = bytes >> 31 ? 0x7fffffffu : static_cast<uint32_t>(bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, static_cast<int>(n), kRawBufferWord3);
+  }
+
+  __device__ inline void copy(uint32_t lds, int h, uint32_t t, int wave) const {
+    if constexpr (kAlong) {
+      const __amdgpu_buffer_rsrc_t from = range(base, left);
+      const uint32_t v = t + 1 < blocks ? voffset : (t + 1 == blocks ? last : kNowhere);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        copy_to_lds(from, lds + (q * 8 + wave) * 1024, v, (h * 128 + q * 64) * stride + t * 128);
+    } else {
+      const uint64_t at = static_cast<uint64_t>(t) * (64 * stride);
+      const __amdgpu_buffer_rsrc_t from = range(base + at, t < blocks ? left - at : 0);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        copy_to_lds(from, lds + (q * 8 + wave) * 1024, voffset, q * 32 * stride + h * 128 * e);
+    }
+  }
+};
+
+template <class C, bool kAAlong, bool kBAlong>
+__global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
+  using SA = Stage<C, kAAlong, 128, 512>;
+  using SB = Stage<C, kBAlong, 128, 512>;
+  extern __shared__ __align__(16) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+
+  // Workgroup w runs on XCD w % 8: each XCD gets a run of neighbouring tiles,
+  // and runs go down bands of 8 tile rows, so that what is in flight on one
+  // XCD shares operands in its L2.
+  const uint32_t tiles = args.tiles_m * args.tiles_n;
+  uint32_t id = blockIdx.x;
+  {
+    const uint32_t per = tiles / 8, more = tiles % 8, x = id % 8, i = id / 8;
+    id = x * per + (x < more ? x : more) + i;
+  }
+  constexpr uint32_t kBand = 8;
+  const uint32_t band = id / (kBand * args.tiles_n), in_band = id % (kBand * args.tiles_n);
+  const uint32_t high = args.tiles_m - band * kBand < kBand ? args.tiles_m - band * kBand : kBand;
+  const uint64_t m0 = static_cast<uint64_t>(band * kBand + in_band % high) * 256;
+  const uint64_t n0 = static_cast<uint64_t>(in_band / high) * 256;
+
+  Copier<C, kAAlong> ca;
+  Copier<C, kBAlong> cb;
+  const uint32_t blocks = static_cast<uint32_t>((args.k + 63) / 64);
+  ca.init(args.a, m0, args.k, blocks, wave);
+  cb.init(args.b, n0, args.k, blocks, wave);
+
+  // Halves of block t: A0, A1, B0, B1.  Both blocks' A halves come first, so
+  // that one address register and the instruction's offset reach them all.
+  auto region = [](uint32_t t, int which) { return (which >> 1) * (4 * kHalfBytes) + (t & 1) * (2 * kHalfBytes) + (which & 1) * kHalfBytes; };
+
+  f32x4 acc[2][2][4][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) acc[i][j][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 fa[2][2][4], fb[2][2][2];  // [set][step][tile]
+
+  ca.copy(lds0 + region(0, 0), 0, 0, wave);
+  cb.copy(lds0 + region(0, 2), 0, 0, wave);
+  cb.copy(lds0 + region(0, 3), 1, 0, wave);
+  ca.copy(lds0 + region(0, 1), 1, 0, wave);
+  ca.copy(lds0 + region(1, 0), 0, 1, wave);
+  cb.copy(lds0 + region(1, 2), 0, 1, wave);
+  cb.copy(lds0 + region(1, 3), 1, 1, wave);
+  ca.copy(lds0 + region(1, 1), 1, 1, wave);
+  asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) fa[0][s][x] = SA::fragment(lds + region(0, 0), wm * 64 + 16 * x, s);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) fb[0][s][y] = SB::fragment(lds + region(0, 2), wn * 32 + 16 * y, s);
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  ca.copy(lds0 + region(0, 0), 0, 2, wave);
+  asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+
+  // One phase: the products of A set `i` and B set `b` into quarter (i, j);
+  // `read` takes the slots 0..7 and reads a part of the next half in each.
+  auto phase = [&](auto i_, auto j_, auto b_, auto&& read, auto&& copy) {
+    constexpr int i = decltype(i_)::value, j = decltype(j_)::value, b = decltype(b_)::value;
+#pragma unroll
+    for (int slot = 0; slot < 8; ++slot) {
+      const int s = slot >> 2, x = slot & 3;
+      read(slot);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) acc[i][j][x][y] = multiply<C>(fb[b][s][y], fa[i][s][x], acc[i][j][x][y]);
+      if (slot == 3) copy();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    asm volatile("s_waitcnt vmcnt(12) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using Zero = std::integral_constant<int, 0>;
+  using One = std::integral_constant<int, 1>;
+  // One block whose first B half is in set `b`.
+  auto block = [&](uint32_t t, auto b_, auto c_) {
+    constexpr int b = decltype(b_)::value, c = decltype(c_)::value;
+    phase(Zero{}, Zero{}, b_,
+          [&](int slot) {
+            if (slot < 4) fb[c][slot >> 1][slot & 1] = SB::fragment(lds + region(b, 3), wn * 32 + 16 * (slot & 1), slot >> 1);
+          },
+          [&] { cb.copy(lds0 + region(b, 2), 0, t + 2, wave); });
+    phase(Zero{}, One{}, c_,
+          [&](int slot) { fa[1][slot >> 2][slot & 3] = SA::fragment(lds + region(b, 1), wm * 64 + 16 * (slot & 3), slot >> 2); },
+          [&] { cb.copy(lds0 + region(b, 3), 1, t + 2, wave); });
+    phase(One{}, One{}, c_,
+          [&](int slot) { fa[0][slot >> 2][slot & 3] = SA::fragment(lds + region(c, 0), wm * 64 + 16 * (slot & 3), slot >> 2); },
+          [&] { ca.copy(lds0 + region(b, 1), 1, t + 2, wave); });
+    phase(One{}, Zero{}, b_,
+          [&](int slot) {
+            if (slot < 4) fb[c][slot >> 1][slot & 1] = SB::fragment(lds + region(c, 2), wn * 32 + 16 * (slot & 1), slot >> 1);
+          },
+          [&] { ca.copy(lds0 + region(c, 0), 0, t + 3, wave); });
+  };
+  uint32_t t = 0;
+  for (; t + 2 <= blocks; t += 2) {
+    block(t, Zero{}, One{});
+    block(t + 1, One{}, Zero{});
+  }
+  if (t < blocks) block(t, Zero{}, One{});
+  // zeros that copies past the last block still bring must not meet the next
+  // workgroup's LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  with_activation(args.e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        each_group<C>(acc[i][j], m0 + i * 128 + wm * 64, n0 + j * 128 + wn * 32,
+                      [&](uint64_t m, uint64_t n, float* v) { finish<C, decltype(act)::value>(args.e, m, n, v); });
+  });
+}
+
 // Adds the shares of k in their order and finishes the sums.
 template <class C>
 __global__ __launch_bounds__(256) void linear_join(const Epilogue e, int shares) {
@@ -477,6 +697,30 @@ __global__ __launch_bounds__(256) void linear_join(const Epilogue e, int shares)
     }
   }
   with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v); });
+}
+
+// ------------------------------------------------------------------ operands laid out anew
+
+struct PackArgs {
+  const char* from;
+  char* to;
+  uint64_t from_stride, to_stride, rows, cols;
+};
+
+// A copy of a matrix with rows at 16-byte boundaries, each padded with zeros
+// to whole vectors.  linear_big takes only such operands.
+template <class C>
+__global__ __launch_bounds__(256) void linear_pack(const PackArgs a) {
+  constexpr int V = C::V;
+  const uint64_t per_row = (a.cols + V - 1) / V;
+  const uint64_t total = per_row * a.rows;
+  for (uint64_t id = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; id < total;
+       id += static_cast<uint64_t>(gridDim.x) * 256) {
+    const uint64_t row = id / per_row, col = id % per_row * V;
+    const int valid = a.cols - col < V ? static_cast<int>(a.cols - col) : V;
+    *reinterpret_cast<u32x4*>(a.to + (row * a.to_stride + col) * C::kElemBytes) =
+        load_upto<C>(a.from + (row * a.from_stride + col) * C::kElemBytes, valid);
+  }
 }
 
 // ------------------------------------------------------------------ dz and the bias gradient
@@ -528,11 +772,9 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs a) {
       for (int i = 0; i < V; ++i) sum[i] += g[i];
       if (a.dz) {
         char* p = a.dz + (m * a.dz_stride + n) * C::kElemBytes;
-        const u32x4 b = C::pack(g);
-        if (valid == V)
-          store_loose<C>(p, b);
-        else if (valid > 0)
-          store_partial<C>(p, 0, b, valid);
+        // rows of dz are padded to whole vectors, and the padding is 0: that
+        // is what dy and z read as there
+        if (valid > 0) *reinterpret_cast<u32x4*>(p) = C::pack(g);
       }
     }
   });

@@ -185,33 +185,96 @@ constexpr int kCus = 256;  // of an MI355X: the plans must not depend on a devic
 
 // How one product m x n x k runs.
 struct ProductPlan {
-  int tile = 64;        // 64 or 128: linear_tile's square
-  uint32_t shares = 1;  // of k
-  uint32_t blocks_per_share = 0;
-  size_t bytes = 0;     // partial sums
+  int tile = 64;         // 64 or 128: linear_tile's square; 256: linear_big's
+  bool pack_a = false, pack_b = false;  // operands laid out anew for linear_big
+  uint32_t shares = 1;   // of k
+  uint32_t blocks_per_share = 1;
   uint64_t partial_stride = 0;
+  size_t a_bytes = 0, b_bytes = 0, partial_bytes = 0;
+  size_t bytes() const { return a_bytes + b_bytes + partial_bytes; }
 };
 
-ProductPlan plan_product(uint64_t m, uint64_t n, uint64_t k, int dtype) {
+// Whether linear_big can take an operand as it lies: 16-byte chunks that are
+// aligned and whole, and offsets within a tile that fit 31 bits.
+bool lies_well(const Operand& o) {
+  return reinterpret_cast<uintptr_t>(o.base) % 16 == 0 && (o.rows <= 1 || o.stride % 8 == 0) && o.cols % 8 == 0;
+}
+bool within_reach(uint64_t stride, uint64_t cols, bool along) {
+  const uint64_t limit = uint64_t(1) << 30;  // elements of 2 bytes
+  return stride < limit / 256 && (!along || cols < limit - 256 * stride);
+}
+
+uint64_t packed_stride(uint64_t cols) { return round_up(cols, 64); }
+size_t packed_bytes(const Operand& o) { return round_up(o.rows * packed_stride(o.cols) * 2, 256); }
+
+ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool b_along, uint64_t m, uint64_t n,
+                         uint64_t k, int dtype) {
   ProductPlan p;
   const uint64_t block = 128 / bytes_of(dtype);
   const uint64_t blocks = ceil_div(k, block);
-  const uint64_t big = ceil_div(m, 128) * ceil_div(n, 128);
-  p.tile = big >= kCus ? 128 : 64;
+  if (dtype != MSCL_FLOAT32 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus / 2 && blocks >= 4 && blocks < (1u << 24)) {
+    p.pack_a = !lies_well(a);
+    p.pack_b = !lies_well(b);
+    if (within_reach(p.pack_a ? packed_stride(a.cols) : a.stride, a.cols, a_along) &&
+        within_reach(p.pack_b ? packed_stride(b.cols) : b.stride, b.cols, b_along)) {
+      p.tile = 256;
+      if (p.pack_a) p.a_bytes = packed_bytes(a);
+      if (p.pack_b) p.b_bytes = packed_bytes(b);
+      return p;
+    }
+    p.pack_a = p.pack_b = false;
+  }
+  const uint64_t large = ceil_div(m, 128) * ceil_div(n, 128);
+  p.tile = large >= kCus ? 128 : 64;
   const uint64_t tiles = ceil_div(m, p.tile) * ceil_div(n, p.tile);
   uint64_t shares = 1;
   if (tiles < 2 * kCus && blocks >= 8) shares = std::min({ceil_div(2 * kCus, tiles), blocks / 4, uint64_t(32)});
-  p.blocks_per_share = static_cast<uint32_t>(ceil_div(blocks, shares));
-  if (p.blocks_per_share == 0) p.blocks_per_share = 1;
+  p.blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(blocks, shares)));
   p.shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(blocks, p.blocks_per_share)));
   p.partial_stride = round_up(n, 8);
-  if (p.shares > 1) p.bytes = p.shares * m * p.partial_stride * 4;
+  if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
   return p;
 }
 
+template <class C>
+mscl_status_t pack(Operand* o, char* to, hipStream_t stream) {
+  PackArgs a{o->base, to, o->stride, packed_stride(o->cols), o->rows, o->cols};
+  const uint64_t groups = std::min<uint64_t>(ceil_div(ceil_div(o->cols, C::V) * o->rows, 256), 16 * kCus);
+  linear_pack<C><<<static_cast<uint32_t>(groups), 256, 0, stream>>>(a);
+  *o = Operand{to, a.to_stride, o->rows, round_up(o->cols, C::V)};
+  return launched("linear_pack");
+}
+
+// linear_big's LDS is more than a kernel gets unasked.
 template <class C, bool kAAlong, bool kBAlong>
-mscl_status_t product(const ProductPlan& p, const Operand& a, const Operand& b, uint64_t k, const Epilogue& e0,
-                      char* workspace, hipStream_t stream) {
+hipError_t allow_lds() {
+  static std::atomic<bool> done{false};
+  if (done.load(std::memory_order_acquire)) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_big<C, kAAlong, kBAlong>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+  if (e == hipSuccess) done.store(true, std::memory_order_release);
+  return e;
+}
+
+template <class C, bool kAAlong, bool kBAlong>
+mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, const Epilogue& e0, char* workspace,
+                      hipStream_t stream) {
+  const uint64_t tm = ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
+  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  const uint32_t groups = static_cast<uint32_t>(tm * tn);
+  if constexpr (C::kElemBytes == 2) {
+    if (p.tile == 256) {
+      mscl_status_t st = MSCL_SUCCESS;
+      if (p.pack_a) st = pack<C>(&a, workspace, stream);
+      if (st == MSCL_SUCCESS && p.pack_b) st = pack<C>(&b, workspace + p.a_bytes, stream);
+      if (st != MSCL_SUCCESS) return st;
+      const hipError_t err = allow_lds<C, kAAlong, kBAlong>();
+      if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+      BigArgs t{a, b, e0, round_up(k, C::V), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
+      linear_big<C, kAAlong, kBAlong><<<groups, 512, kBigLds, stream>>>(t);
+      return launched("linear_big");
+    }
+  }
   TileArgs t;
   t.a = a;
   t.b = b;
@@ -219,21 +282,19 @@ mscl_status_t product(const ProductPlan& p, const Operand& a, const Operand& b, 
   t.k = k;
   t.e.partial = p.shares > 1 ? reinterpret_cast<float*>(workspace) : nullptr;
   t.e.partial_stride = p.partial_stride;
-  const uint64_t tm = ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
-  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
   t.tiles_m = static_cast<uint32_t>(tm);
   t.tiles_n = static_cast<uint32_t>(tn);
   t.blocks_per_share = p.blocks_per_share;
-  const dim3 grid(static_cast<uint32_t>(tm * tn), p.shares);
+  const dim3 grid(groups, p.shares);
   if (p.tile == 128)
     linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
   else
     linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
   mscl_status_t st = launched("linear_tile");
   if (st != MSCL_SUCCESS || p.shares == 1) return st;
-  const uint64_t groups = ceil_div(ceil_div(e0.n, C::V) * e0.m, 256);
-  if (groups > kMostGroups) return bad("the matrices have too many tiles");
-  linear_join<C><<<static_cast<uint32_t>(groups), 256, 0, stream>>>(t.e, static_cast<int>(p.shares));
+  const uint64_t joins = ceil_div(ceil_div(e0.n, C::V) * e0.m, 256);
+  if (joins > kMostGroups) return bad("the matrices have too many tiles");
+  linear_join<C><<<static_cast<uint32_t>(joins), 256, 0, stream>>>(t.e, static_cast<int>(p.shares));
   return launched("linear_join");
 }
 
@@ -251,13 +312,18 @@ mscl_status_t check_linear(const mscl_linear_t* c, Spans& s) {
   return s.check();
 }
 
-ProductPlan plan_linear(const mscl_linear_t& c) { return plan_product(c.rows, c.out_features, c.in_features, c.dtype); }
+Operand x_of(const mscl_linear_t& c) { return Operand{bytes_at(c.x), c.x_stride, c.rows, c.in_features}; }
+Operand w_of(const mscl_linear_t& c) { return Operand{bytes_at(c.w), c.w_stride, c.out_features, c.in_features}; }
+
+ProductPlan plan_linear(const mscl_linear_t& c) {
+  return plan_product(x_of(c), true, w_of(c), true, c.rows, c.out_features, c.in_features, c.dtype);
+}
 
 // Parts of a backward call's workspace, each from a 256-byte boundary.
 struct BackwardPlan {
   ProductPlan dx, dw;
   bool slope = false;  // dz is computed into the workspace
-  uint64_t dz_stride = 0;
+  Operand dz, x, w;    // dz without its address where it is computed
   uint32_t groups = 0, rows_per_group = 0;  // of the bias gradient's partial sums
   size_t dz_at = 0, sums_at = 0, partial_at = 0, bytes = 0;
 };
@@ -278,10 +344,13 @@ BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
   const size_t e = bytes_of(c.dtype);
   p.slope = c.activation != MSCL_ACT_NONE && (c.dx || c.dw);
   size_t at = 0;
+  p.dz = Operand{bytes_at(c.dy), c.dy_stride, c.rows, c.out_features};
+  p.x = Operand{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
+  p.w = Operand{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
   if (p.slope) {
-    p.dz_stride = round_up(c.out_features, 64);
+    p.dz = Operand{nullptr, packed_stride(c.out_features), c.rows, round_up(c.out_features, 16 / e)};
     p.dz_at = at;
-    at = round_up(at + c.rows * p.dz_stride * e, 256);
+    at = round_up(at + c.rows * p.dz.stride * e, 256);
   }
   if (c.dbias) {
     plan_groups(c.rows, ceil_div(c.out_features, 64 * (16 / e)), &p.groups, &p.rows_per_group);
@@ -291,12 +360,12 @@ BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
   p.partial_at = at;
   size_t partial = 0;
   if (c.dx) {
-    p.dx = plan_product(c.rows, c.in_features, c.out_features, c.dtype);
-    partial = std::max(partial, p.dx.bytes);
+    p.dx = plan_product(p.dz, true, p.w, false, c.rows, c.in_features, c.out_features, c.dtype);
+    partial = std::max(partial, p.dx.bytes());
   }
   if (c.dw) {
-    p.dw = plan_product(c.out_features, c.in_features, c.rows, c.dtype);
-    partial = std::max(partial, p.dw.bytes);
+    p.dw = plan_product(p.dz, false, p.x, false, c.out_features, c.in_features, c.rows, c.dtype);
+    partial = std::max(partial, p.dw.bytes());
   }
   p.bytes = at + partial;
   return p;
@@ -447,7 +516,7 @@ mscl_status_t mscl_linear_workspace(const mscl_linear_t* call, size_t* bytes) {
   Spans spans;
   const mscl_status_t st = check_linear(call, spans);
   if (st != MSCL_SUCCESS) return st;
-  *bytes = call->rows && call->out_features ? plan_linear(*call).bytes : 0;
+  *bytes = call->rows && call->out_features ? plan_linear(*call).bytes() : 0;
   return MSCL_SUCCESS;
 }
 
@@ -458,7 +527,7 @@ mscl_status_t mscl_linear(const mscl_linear_t* call, void* workspace, size_t wor
   const mscl_linear_t& c = *call;
   if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
   const ProductPlan p = plan_linear(c);
-  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes())) != MSCL_SUCCESS) return st;
   int cus = 0;
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
   Epilogue e;
@@ -473,10 +542,8 @@ mscl_status_t mscl_linear(const mscl_linear_t* call, void* workspace, size_t wor
   e.m = c.rows;
   e.n = c.out_features;
   e.act = c.activation;
-  const Operand a{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
-  const Operand b{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
   return with_codec(c.dtype, [&](auto t) {
-    return product<decltype(t), true, true>(p, a, b, c.in_features, e, bytes_at(workspace),
+    return product<decltype(t), true, true>(p, x_of(c), w_of(c), c.in_features, e, bytes_at(workspace),
                                             static_cast<hipStream_t>(stream));
   });
 }
@@ -506,7 +573,8 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = bytes_at(workspace);
-  Operand dz{bytes_at(c.dy), c.dy_stride, c.rows, c.out_features};
+  Operand dz = p.dz;
+  if (p.slope) dz.base = ws + p.dz_at;
   if (db || (p.slope && (dx || dw))) {
     SlopeArgs a;
     memset(&a, 0, sizeof a);
@@ -519,7 +587,7 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
     a.cols = c.out_features;
     if (p.slope) {
       a.dz = ws + p.dz_at;
-      a.dz_stride = p.dz_stride;
+      a.dz_stride = p.dz.stride;
     }
     uint32_t groups = p.groups;
     a.rows_per_group = p.rows_per_group;
@@ -542,7 +610,6 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
       st = join_columns(c.dtype, a.sums, a.sums_stride, c.out_features, groups, c.dbias, nullptr, 1, s);
       if (st != MSCL_SUCCESS) return st;
     }
-    if (p.slope) dz = Operand{ws + p.dz_at, p.dz_stride, c.rows, c.out_features};
   }
   Epilogue e;
   if (dx) {
@@ -551,9 +618,8 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
     e.y_stride = c.dx_stride;
     e.m = c.rows;
     e.n = c.in_features;
-    const Operand b{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
     st = with_codec(c.dtype, [&](auto t) {
-      return product<decltype(t), true, false>(p.dx, dz, b, c.out_features, e, ws + p.partial_at, s);
+      return product<decltype(t), true, false>(p.dx, dz, p.w, c.out_features, e, ws + p.partial_at, s);
     });
     if (st != MSCL_SUCCESS) return st;
   }
@@ -563,9 +629,8 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
     e.y_stride = c.dw_stride;
     e.m = c.out_features;
     e.n = c.in_features;
-    const Operand b{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
     st = with_codec(c.dtype, [&](auto t) {
-      return product<decltype(t), false, false>(p.dw, dz, b, c.rows, e, ws + p.partial_at, s);
+      return product<decltype(t), false, false>(p.dw, dz, p.x, c.rows, e, ws + p.partial_at, s);
     });
   }
   return st;

@@ -120,8 +120,8 @@ def layer_norm(x, w, b, eps):
     rel = 0.5 * off_var / (var + eps) + 4 * U
     rel = torch.where(rel > 0.25, torch.full_like(rel, math.inf), 1.5 * rel)  # first order holds below that
     off_h = rstd * off_d * (1 + rel) + h.abs() * (rel + 2 * U)
-    ww = torch.ones(n, dtype=torch.float64) if w is None else w.double()
-    bb = torch.zeros(n, dtype=torch.float64) if b is None else b.double()
+    ww = torch.ones(n, dtype=torch.float64, device=v.device) if w is None else w.double()
+    bb = torch.zeros(n, dtype=torch.float64, device=v.device) if b is None else b.double()
     y = h * ww + bb
     off = off_h * ww.abs() + 2 * U * ((h * ww).abs() + bb.abs())
     return ((y, rounded(y, off, t)), (mean[:, 0], off_mean[:, 0] + 2 * U * mean[:, 0].abs()),
@@ -135,7 +135,7 @@ def layer_norm_backward(dy, x, mean, rstd, w, param_type):
     m, r = mean.double()[:, None], rstd.double()[:, None]
     h = (v - m) * r
     off_h = 2 * U * h.abs()
-    ww = torch.ones(n, dtype=torch.float64) if w is None else w.double()
+    ww = torch.ones(n, dtype=torch.float64, device=v.device) if w is None else w.double()
     g = g0 * ww
     off_g = U * g.abs()
     c0, c1 = g.mean(1, keepdim=True), (g * h).mean(1, keepdim=True)
@@ -154,7 +154,7 @@ def layer_norm_backward(dy, x, mean, rstd, w, param_type):
 
 def assert_within(got, want, name):
     exact, bound = want
-    g = got.detach().cpu().double()
+    g = got.detach().to(exact.device).double()
     assert g.shape == exact.shape, f"{name}: shape {tuple(g.shape)}"
     assert bool(torch.isfinite(g).all()), f"{name}: not finite"
     over = (g - exact).abs() - bound

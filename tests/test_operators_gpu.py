@@ -109,6 +109,44 @@ def test_linear_backward(dtype, form):
             assert torch.equal(one[only], got[only]) and sum(g is None for g in one) == 2
 
 
+# Large products of 16-bit types (256 x 256 tiles): forward, and both gradients, with edges inside a tile, k that ends
+# inside a block, odd and even numbers of blocks, and operands that have to be laid out anew.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k,n,form", [(2304, 4096, 4096, "plain"), (2100, 4104, 4000, "plain"),
+                                        (2100, 4104, 4000, "columns"), (2300, 4099, 3907, "odd"),
+                                        (4097, 320, 2056, "plain"), (2049, 264, 4111, "columns")])
+def test_large_products(dtype, m, k, n, form):
+    gen = torch.Generator().manual_seed(18)
+    t = DTYPES[dtype]
+    x, w, b, r = linear_case(gen, m, k, n, t)
+    dy, z = normal(gen, m, n, dtype=t), normal(gen, m, n, scale=1.5, dtype=t)
+    for act in ("gelu", "none"):
+        note("large linear", dtype, m, k, n, form, act)
+        xg, wg, bg, rg, dyg, zg = (placed(v, form) for v in (x, w, b, r, dy, z))
+        got = M.linear_tensors(xg, wg, bg, rg, act, return_preact=True)
+        c = [v.cuda() for v in (x, w, b, r, dy, z)]  # the oracle's 64 bits on the GPU, from contiguous copies
+        for g, want, name in zip(got, O.linear(c[0], c[1], c[2], c[3], act), ("y", "z")):
+            O.assert_within(g, want, f"{name} {act}")
+        note("large linear backward", dtype, m, k, n, form, act)
+        back = M.linear_backward_tensors(dyg, xg, wg, zg, act)
+        for g, want, name in zip(back, O.linear_backward(c[4], c[0], c[1], c[5], act), ("dx", "dw", "db")):
+            O.assert_within(g, want, f"{name} {act}")
+        for a, b2 in zip(back, M.linear_backward_tensors(dyg, xg, wg, zg, act)):
+            assert torch.equal(a, b2)
+
+
+def test_large_product_keeps_nan_in_its_row_and_column():
+    gen = torch.Generator().manual_seed(19)
+    m, k, n = 2100, 712, 4100
+    x, w, b, _ = linear_case(gen, m, k, n, torch.bfloat16)
+    x[2099, 711], w[4099, 700] = math.nan, math.inf
+    x[:, 700] = x[:, 700].abs() + 1
+    note("large product with NaN")
+    y = M.linear_tensors(x.cuda(), w.cuda(), b.cuda()).cpu()
+    assert bool(torch.isnan(y[2099]).all()) and bool((y[:2099, 4099] == math.inf).all())
+    assert bool(torch.isfinite(y[:2099, :4099]).all())
+
+
 def test_linear_many_leading_dimensions():
     gen = torch.Generator().manual_seed(13)
     x, w, b, _ = linear_case(gen, 30, 24, 40, torch.bfloat16)
