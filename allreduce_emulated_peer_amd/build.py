@@ -61,4 +61,4 @@ def asm(out_path: str, src: str = SRC) -> str:
 if __name__ == "__main__":
     import sys
 
-    print(build(verbose=True, units=tuple(sys.argv[1:]) or UNITS))
+    print(build(verbose=True, units=tuple(u for u in sys.argv[1:] if u) if len(sys.argv) > 1 else UNITS))

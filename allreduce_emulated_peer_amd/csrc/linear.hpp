@@ -59,6 +59,25 @@ __device__ inline u32x4 load_upto(const char* p, int valid) {
   return v;
 }
 
+// Rounds V values and stores the first `valid` of them.
+template <class C>
+__device__ inline void store_upto(char* p, const float* v, int valid) {
+  const u32x4 b = C::pack(v);
+  if (valid >= C::V)
+    store_loose<C>(p, b);
+  else if (valid > 0)
+    store_partial<C>(p, 0, b, valid);
+}
+
+// Runs fn with whether a whole workgroup's columns exist as a constant.
+template <class Fn>
+__device__ inline void with_edges(bool full, Fn&& fn) {
+  if (full)
+    fn(std::true_type{});
+  else
+    fn(std::false_type{});
+}
+
 // ------------------------------------------------------------------ activations
 
 // Activations and their slopes in binary32.  kFast is taken where the result
@@ -175,43 +194,47 @@ __device__ inline void with_activation(int act, Fn&& fn) {
   }
 }
 
+// What the epilogue adds to V neighbouring sums.  A wave fetches all of its
+// tiles' before it finishes the first one: fetched one by one, each would
+// wait a memory latency behind the stores of the one before (8192 x 4096 x
+// 8192 fp16 with a residual: 482 us one by one, 421 us without residual).
+template <class C>
+__device__ inline u32x4 fetch_bias(const Epilogue& e, uint64_t n) {
+  if (!e.bias || n >= e.n) return u32x4{0u, 0u, 0u, 0u};
+  return load_upto<C>(e.bias + n * C::kElemBytes, e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
+}
+template <class C>
+__device__ inline u32x4 fetch_residual(const Epilogue& e, uint64_t m, uint64_t n) {
+  if (!e.residual || m >= e.m || n >= e.n) return u32x4{0u, 0u, 0u, 0u};
+  return load_upto<C>(e.residual + (m * e.residual_stride + n) * C::kElemBytes,
+                      e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
+}
+
 // Finishes V neighbouring sums of row m from column n on, and stores them.
 template <class C, int kAct>
-__device__ inline void finish(const Epilogue& e, uint64_t m, uint64_t n, float* v) {
+__device__ inline void finish(const Epilogue& e, uint64_t m, uint64_t n, float* v, const u32x4& bias,
+                              const u32x4& residual) {
   constexpr int V = C::V;
   constexpr bool kFast = C::kElemBytes == 2;
   if (m >= e.m || n >= e.n) return;
   const int valid = e.n - n < V ? static_cast<int>(e.n - n) : V;
-  const bool full = valid == V;
   float t[V];
   if (e.bias) {
-    C::unpack(load_upto<C>(e.bias + n * C::kElemBytes, valid), t);
+    C::unpack(bias, t);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += t[i];
   }
-  if (e.z) {
-    char* p = e.z + (m * e.z_stride + n) * C::kElemBytes;
-    const u32x4 b = C::pack(v);
-    if (full)
-      store_loose<C>(p, b);
-    else
-      store_partial<C>(p, 0, b, valid);
-  }
+  if (e.z) store_upto<C>(e.z + (m * e.z_stride + n) * C::kElemBytes, v, valid);
   if constexpr (kAct != MSCL_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = activate<kAct, kFast>(v[i]);
   }
   if (e.residual) {
-    C::unpack(load_upto<C>(e.residual + (m * e.residual_stride + n) * C::kElemBytes, valid), t);
+    C::unpack(residual, t);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += t[i];
   }
-  char* p = e.y + (m * e.y_stride + n) * C::kElemBytes;
-  const u32x4 b = C::pack(v);
-  if (full)
-    store_loose<C>(p, b);
-  else
-    store_partial<C>(p, 0, b, valid);
+  store_upto<C>(e.y + (m * e.y_stride + n) * C::kElemBytes, v, valid);
 }
 
 // V neighbouring sums of one share of k.  Partial rows are padded to whole
@@ -232,40 +255,69 @@ __device__ inline void swap_rows16(float& a, float& b) {
   b = __builtin_bit_cast(float, y);
 }
 
-// The sums of a wave's kM x kN tiles of 16 x 16 (tile (i, j) at row
-// m0 + 16 i, column n0 + 16 j), given to fn(m, n, V values).  In tile (i, j)
-// lane l holds row l % 16, columns 4 (l / 16) .. + 3; for a 16-bit type two
-// neighbouring tiles trade halves, so that each lane holds eight columns.
-template <class C, int kM, int kN, class Fn>
-__device__ inline void each_group(f32x4 (&acc)[kM][kN], uint64_t m0, uint64_t n0, Fn&& fn) {
-  const int lane = threadIdx.x & 63;
-  const int r = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < kM; ++i) {
-    const uint64_t m = m0 + 16 * i + r;
+// Where the V sums of group q of a wave's kM x kN tiles of 16 x 16 lie (tile
+// (i, j) at row m0 + 16 i, column n0 + 16 j).  In tile (i, j) lane l holds row
+// l % 16, columns 4 (l / 16) .. + 3; for a 16-bit type two neighbouring tiles
+// trade halves, so that each lane holds eight columns.
+template <class C, int kM, int kN>
+struct Groups {
+  static constexpr int kPerRow = C::V == 4 ? kN : kN / 2;
+  static constexpr int kCount = kM * kPerRow;
+  static_assert(C::V == 4 || kN % 2 == 0, "16-bit tiles come in pairs");
+
+  static __device__ inline uint64_t row(uint64_t m0, int q) { return m0 + 16 * (q / kPerRow) + (threadIdx.x & 15); }
+  static __device__ inline uint64_t column(uint64_t n0, int q) {
+    const int g = (threadIdx.x & 63) >> 4, j = q % kPerRow;
+    if constexpr (C::V == 4) return n0 + 16 * j + 4 * g;
+    return n0 + 16 * (2 * j + (g & 1)) + 8 * (g >> 1);
+  }
+  static __device__ inline void sums(const f32x4 (&acc)[kM][kN], int q, float* v) {
+    const int i = q / kPerRow, j = q % kPerRow;
     if constexpr (C::V == 4) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        fn(m, n0 + 16 * j + 4 * g, v);
-      }
+      for (int c = 0; c < 4; ++c) v[c] = acc[i][j][c];
     } else {
-      static_assert(kN % 2 == 0, "16-bit tiles come in pairs");
 #pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float a = acc[i][j][q], b = acc[i][j + 1][q];
-          swap_rows16(a, b);
-          v[q] = a;
-          v[4 + q] = b;
-        }
-        fn(m, n0 + 16 * (j + (g & 1)) + 8 * (g >> 1), v);
+      for (int c = 0; c < 4; ++c) {
+        float a = acc[i][2 * j][c], b = acc[i][2 * j + 1][c];
+        swap_rows16(a, b);
+        v[c] = a;
+        v[4 + c] = b;
       }
     }
   }
+};
+
+// Finishes and stores a wave's kParts blocks of tiles, block p at (m0, n0) of
+// at(p).
+template <class C, int kM, int kN, int kParts, class At>
+__device__ inline void finish_all(const Epilogue& e, const f32x4 (&acc)[kParts][kM][kN], At&& at) {
+  using G = Groups<C, kM, kN>;
+  u32x4 bias[kParts][G::kPerRow], residual[kParts][G::kCount];
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+#pragma unroll
+    for (int q = 0; q < G::kPerRow; ++q) bias[p][q] = fetch_bias<C>(e, G::column(at(p).second, q));
+#pragma unroll
+    for (int q = 0; q < G::kCount; ++q)
+      residual[p][q] = fetch_residual<C>(e, G::row(at(p).first, q), G::column(at(p).second, q));
+  }
+  with_activation(e.act, [&](auto act) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int q = 0; q < G::kCount; ++q) {
+        float v[C::V];
+        G::sums(acc[p], q, v);
+        finish<C, decltype(act)::value>(e, G::row(at(p).first, q), G::column(at(p).second, q), v,
+                                        bias[p][q % G::kPerRow], residual[p][q]);
+      }
+  });
 }
+
+struct Corner {
+  uint64_t first, second;
+};
 
 // ------------------------------------------------------------------ general tile kernel
 
@@ -402,11 +454,11 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
   uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * SA::kBlock;
   if (k_end > t.k) k_end = t.k;
 
-  f32x4 acc[kWM][kWN];
+  f32x4 acc[1][kWM][kWN];
 #pragma unroll
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int j = 0; j < kWN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   SA sa;
   SB sb;
@@ -436,7 +488,7 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
 #pragma unroll
       for (int i = 0; i < kWM; ++i)
 #pragma unroll
-        for (int j = 0; j < kWN; ++j) acc[i][j] = multiply<C>(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
     }
     if (more) {
       buf ^= 1;
@@ -446,13 +498,15 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
     __syncthreads();
   }
   if (t.e.partial) {
-    each_group<C>(acc, m0 + wm, n0 + wn,
-                  [&](uint64_t m, uint64_t n, float* v) { keep_partial<C>(t.e, blockIdx.y, m, n, v); });
+    using G = Groups<C, kWM, kWN>;
+#pragma unroll
+    for (int q = 0; q < G::kCount; ++q) {
+      float v[C::V];
+      G::sums(acc[0], q, v);
+      keep_partial<C>(t.e, blockIdx.y, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
+    }
   } else {
-    with_activation(t.e.act, [&](auto act) {
-      each_group<C>(acc, m0 + wm, n0 + wn,
-                    [&](uint64_t m, uint64_t n, float* v) { finish<C, decltype(act)::value>(t.e, m, n, v); });
-    });
+    finish_all<C>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
   }
 }
 
@@ -587,15 +641,13 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   // that one address register and the instruction's offset reach them all.
   auto region = [](uint32_t t, int which) { return (which >> 1) * (4 * kHalfBytes) + (t & 1) * (2 * kHalfBytes) + (which & 1) * kHalfBytes; };
 
-  f32x4 acc[2][2][4][2];
+  f32x4 acc[4][4][2];  // quarter (i, j) is 2 i + j
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int p = 0; p < 4; ++p)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) acc[i][j][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int y = 0; y < 2; ++y) acc[p][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 fa[2][2][4], fb[2][2][2];  // [set][step][tile]
 
   ca.copy(lds0 + region(0, 0), 0, 0, wave);
@@ -627,7 +679,8 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
       const int s = slot >> 2, x = slot & 3;
       read(slot);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) acc[i][j][x][y] = multiply<C>(fb[b][s][y], fa[i][s][x], acc[i][j][x][y]);
+      for (int y = 0; y < 2; ++y)
+        acc[2 * i + j][x][y] = multiply<C>(fb[b][s][y], fa[i][s][x], acc[2 * i + j][x][y]);
       if (slot == 3) copy();
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -666,13 +719,138 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   // workgroup's LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-  with_activation(args.e.act, [&](auto act) {
+  finish_all<C>(args.e, acc, [&](int p) {
+    return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
+  });
+}
+
+// ------------------------------------------------------------------ few rows
+
+// Products of up to 64 rows, where the pass over w bounds: 8 waves share
+// 16 kN rows of w (columns of y) and split k between them, each streams its
+// part of w straight into the MFMA operand registers (no LDS on the way,
+// every byte of w is used once), and the 8 waves' sums meet in LDS.  x is
+// small and comes from the caches; its rows past the end repeat the last one,
+// as do w's, and their results are not stored.  A step is 128 bytes of k;
+// the loads of the next kDeep steps are in flight while kDeep are multiplied.
+template <class C, int kM, int kN, int kDeep>
+__global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
+  constexpr int V = C::V;
+  constexpr int kStep = 8 * V;
+  constexpr int kPitch = 16 * kN + 4;  // floats; rows 16 apart lie 4 banks apart
+  __shared__ __align__(16) float sums[8][16 * kM * kPitch];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * (16 * kN);
+  const char* w[kN];
+  const char* x[kM];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < kN; ++j) {
+    const uint64_t n = n0 + 16 * j + r;
+    w[j] = t.b.base + ((n < t.b.rows ? n : t.b.rows - 1) * t.b.stride + g * V) * C::kElemBytes;
+  }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        each_group<C>(acc[i][j], m0 + i * 128 + wm * 64, n0 + j * 128 + wn * 32,
-                      [&](uint64_t m, uint64_t n, float* v) { finish<C, decltype(act)::value>(args.e, m, n, v); });
+  for (int i = 0; i < kM; ++i) {
+    const uint64_t m = 16 * i + r;
+    x[i] = t.a.base + ((m < t.a.rows ? m : t.a.rows - 1) * t.a.stride + g * V) * C::kElemBytes;
+  }
+  f32x4 acc[kM][kN];
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // this wave's whole steps of this share of k: [step, end)
+  const uint64_t whole = t.k / kStep;
+  const uint64_t share_first = static_cast<uint64_t>(blockIdx.y) * t.blocks_per_share;
+  const uint64_t share_end = share_first + t.blocks_per_share < whole ? share_first + t.blocks_per_share : whole;
+  const uint64_t per = (t.blocks_per_share + 7) / 8;
+  uint64_t step = share_first + wave * per;
+  uint64_t end = step + per < share_end ? step + per : share_end;
+  if (step > end) step = end;
+
+  u32x4 wq[2][kDeep][kN][2], xq[2][kDeep][kM][2];
+  auto load = [&](int set, uint64_t from) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const uint64_t at = (from + d) * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) wq[set][d][j][h] = load_loose<C>(w[j] + at + 64 * h);
+#pragma unroll
+        for (int i = 0; i < kM; ++i) xq[set][d][i][h] = load_loose<C>(x[i] + at + 64 * h);
+      }
+    }
+  };
+  auto compute = [&](int set) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+          for (int j = 0; j < kN; ++j) acc[i][j] = multiply<C>(wq[set][d][j][h], xq[set][d][i][h], acc[i][j]);
+  };
+  if (step + kDeep <= end) {
+    load(0, step);
+    for (;;) {
+      const bool second = step + 2 * kDeep <= end;
+      if (second) load(1, step + kDeep);
+      compute(0);
+      step += kDeep;
+      if (!second) break;
+      const bool third = step + 2 * kDeep <= end;
+      if (third) load(0, step + kDeep);
+      compute(1);
+      step += kDeep;
+      if (!third) break;
+    }
+  }
+  auto single = [&](uint64_t at, bool whole_step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 a[kM], b[kN];
+      const uint64_t k = at * kStep + h * (kStep / 2) + g * V;
+      const int valid = whole_step ? V : (k >= t.k ? 0 : (t.k - k < V ? static_cast<int>(t.k - k) : V));
+#pragma unroll
+      for (int j = 0; j < kN; ++j) b[j] = load_upto<C>(w[j] + at * 128 + 64 * h, valid);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) a[i] = load_upto<C>(x[i] + at * 128 + 64 * h, valid);
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) acc[i][j] = multiply<C>(b[j], a[i], acc[i][j]);
+    }
+  };
+  for (; step < end; ++step) single(step, true);
+  // k past the last whole step: the last share's last wave
+  if (t.k % kStep && blockIdx.y == gridDim.y - 1 && wave == 7) single(whole, false);
+
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      *reinterpret_cast<f32x4*>(&sums[wave][(16 * i + r) * kPitch + 16 * j + 4 * g]) = acc[i][j];
+  __syncthreads();
+  constexpr int kGroups = 16 * kM * 16 * kN / V;
+  with_activation(t.e.act, [&](auto act) {
+    for (int id = threadIdx.x; id < kGroups; id += 512) {
+      const int m = id / (16 * kN / V), n = id % (16 * kN / V) * V;
+      float v[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
+      if (t.e.partial)
+        keep_partial<C>(t.e, blockIdx.y, m, n0 + n, v);
+      else
+        finish<C, decltype(act)::value>(t.e, m, n0 + n, v, fetch_bias<C>(t.e, n0 + n),
+                                        fetch_residual<C>(t.e, m, n0 + n));
+    }
   });
 }
 
@@ -696,7 +874,8 @@ __global__ __launch_bounds__(256) void linear_join(const Epilogue e, int shares)
       for (int c = 0; c < 4; ++c) v[i + c] += q[c];
     }
   }
-  with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v); });
+  const u32x4 bias = fetch_bias<C>(e, n), residual = fetch_residual<C>(e, m, n);
+  with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v, bias, residual); });
 }
 
 // ------------------------------------------------------------------ operands laid out anew
@@ -757,26 +936,39 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] = 0.0f;
   with_activation(a.z ? a.act : MSCL_ACT_NONE, [&](auto act) {
+   with_edges(n - lane * V + 64 * V <= a.cols, [&](auto full) {
     constexpr int kAct = decltype(act)::value;
-#pragma unroll 2
-    for (uint64_t m = first + wave; m < end; m += 4) {
-      float g[V];
-      C::unpack(load_upto<C>(a.dy + (m * a.dy_stride + n) * C::kElemBytes, valid), g);
-      if constexpr (kAct != MSCL_ACT_NONE) {
-        float z[V];
-        C::unpack(load_upto<C>(a.z + (m * a.z_stride + n) * C::kElemBytes, valid), z);
+    constexpr bool kFull = decltype(full)::value;
+    constexpr int kRows = 4;  // in flight
+    for (uint64_t m0 = first + wave; m0 < end; m0 += 4 * kRows) {
+      u32x4 dy[kRows], z[kRows];
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] *= slope<kAct, kFast>(z[i]);
+      for (int q = 0; q < kRows; ++q) {
+        const uint64_t m = m0 + 4 * q < end ? m0 + 4 * q : end - 1;
+        const int there = kFull ? V : valid;
+        dy[q] = load_upto<C>(a.dy + (m * a.dy_stride + n) * C::kElemBytes, there);
+        if constexpr (kAct != MSCL_ACT_NONE) z[q] = load_upto<C>(a.z + (m * a.z_stride + n) * C::kElemBytes, there);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += g[i];
-      if (a.dz) {
-        char* p = a.dz + (m * a.dz_stride + n) * C::kElemBytes;
+      for (int q = 0; q < kRows; ++q) {
+        if (m0 + 4 * q >= end) continue;
+        float g[V];
+        C::unpack(dy[q], g);
+        if constexpr (kAct != MSCL_ACT_NONE) {
+          float t[V];
+          C::unpack(z[q], t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] *= slope<kAct, kFast>(t[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += g[i];
         // rows of dz are padded to whole vectors, and the padding is 0: that
-        // is what dy and z read as there
-        if (valid > 0) *reinterpret_cast<u32x4*>(p) = C::pack(g);
+        // is what dy reads as there
+        if (a.dz && (kFull || valid > 0))
+          *reinterpret_cast<u32x4*>(a.dz + ((m0 + 4 * q) * a.dz_stride + n) * C::kElemBytes) = C::pack(g);
       }
     }
+   });
   });
   if (!a.sums) return;
 #pragma unroll

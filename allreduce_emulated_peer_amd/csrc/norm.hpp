@@ -62,15 +62,6 @@ __device__ inline void load_params(const char* base, uint64_t n, int valid, floa
   }
 }
 
-template <class C>
-__device__ inline void store_upto(char* p, const float* v, int valid) {
-  const u32x4 b = C::pack(v);
-  if (valid >= C::V)
-    store_loose<C>(p, b);
-  else if (valid > 0)
-    store_partial<C>(p, 0, b, valid);
-}
-
 struct NormArgs {
   const char* x;
   const char* w;  // null: 1
@@ -191,6 +182,11 @@ __global__ __launch_bounds__(1024) void norm_rows_wide(const NormArgs a) {
 
 // ------------------------------------------------------------------ backward
 
+// Takes from the compiler what it knows of a held vector, so that values
+// derived from it are derived again after a reduction and not kept through it
+// (two rows of 8192 16-bit elements: 64 registers less, and no spills).
+__device__ inline void forget(u32x4& v) { asm volatile("" : "+v"(v)); }
+
 struct NormBackArgs {
   const char* dy;
   const char* x;
@@ -199,6 +195,7 @@ struct NormBackArgs {
   const char* w;  // null: 1
   char* dx;       // null: not wanted
   float* sums;    // [groups][2][sums_stride]: dw then db; null: not wanted
+  float* along;   // [rows][column blocks][2]: a block's sums of g and of g h
   uint64_t dy_stride, x_stride, dx_stride, sums_stride, rows, width;
   uint32_t rows_per_group;
 };
@@ -223,23 +220,29 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void norm_back_row
     xb[k] = load_upto<C>(x + n * C::kElemBytes, valid);
     gb[k] = load_upto<C>(dy + n * C::kElemBytes, valid);
   }
-  float g[kVecs][V], h[kVecs][V];
-  float s[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int k = 0; k < kVecs; ++k) {
+  // (g, h) of one vector, derived before and after the reduction
+  auto derive = [&](int k, float* g, float* h) {
     const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
     const int valid = n >= a.width ? 0 : (a.width - n < V ? static_cast<int>(a.width - n) : V);
     float w[V];
     load_params<P, V>(a.w, n, valid, 1.0f, w);
-    C::unpack(xb[k], h[k]);
-    C::unpack(gb[k], g[k]);
+    C::unpack(xb[k], h);
+    C::unpack(gb[k], g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = i < valid;
-      h[k][i] = in ? (h[k][i] - mean) * rstd : 0.0f;
-      g[k][i] = in ? g[k][i] * w[i] : 0.0f;
-      s[0] += g[k][i];
-      s[1] = fmaf(g[k][i], h[k][i], s[1]);
+      h[i] = i < valid ? (h[i] - mean) * rstd : 0.0f;
+      g[i] = i < valid ? g[i] * w[i] : 0.0f;
+    }
+  };
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    float g[V], h[V];
+    derive(k, g, h);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[0] += g[i];
+      s[1] = fmaf(g[i], h[i], s[1]);
     }
   }
   block_sums<kThreads, 2>(s, lds, 0);
@@ -250,10 +253,13 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void norm_back_row
   for (int k = 0; k < kVecs; ++k) {
     const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
     const int valid = n >= a.width ? 0 : (a.width - n < V ? static_cast<int>(a.width - n) : V);
-    float d[V];
+    float g[V], h[V];
+    forget(xb[k]);
+    forget(gb[k]);
+    derive(k, g, h);
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = rstd * (g[k][i] - c0 - h[k][i] * c1);
-    store_upto<C>(dx + n * C::kElemBytes, d, valid);
+    for (int i = 0; i < V; ++i) g[i] = rstd * (g[i] - c0 - h[i] * c1);
+    store_upto<C>(dx + n * C::kElemBytes, g, valid);
   }
 }
 
@@ -301,10 +307,38 @@ __global__ __launch_bounds__(1024) void norm_back_rows_wide(const NormBackArgs a
   });
 }
 
-// dw and db over a group of rows: 64 lanes cover 64 V columns, the 4 waves
-// take the group's rows in turn.
-template <class C>
-__global__ __launch_bounds__(256) void norm_back_columns(const NormBackArgs a) {
+// The rows that a wave of the two kernels below has in flight, 4 apart.  Rows
+// past `end` are read as the last one and count as 0.  kFull: all of the
+// wave's vectors are whole, so that no load hangs on a lane's branch.
+constexpr int kTileRows = 4;
+template <class C, bool kFull>
+struct TileRows {
+  u32x4 x[kTileRows], dy[kTileRows];
+  float mean[kTileRows], rstd[kTileRows];
+  __device__ inline void load(const NormBackArgs& a, uint64_t row0, uint64_t end, uint64_t n, int valid) {
+#pragma unroll
+    for (int q = 0; q < kTileRows; ++q) {
+      const uint64_t row = row0 + 4 * q < end ? row0 + 4 * q : end - 1;
+      mean[q] = a.mean[row];
+      rstd[q] = a.rstd[row];
+      x[q] = load_upto<C>(a.x + (row * a.x_stride + n) * C::kElemBytes, kFull ? C::V : valid);
+      dy[q] = load_upto<C>(a.dy + (row * a.dy_stride + n) * C::kElemBytes, kFull ? C::V : valid);
+    }
+#pragma unroll
+    for (int q = 0; q < kTileRows; ++q)
+      if (row0 + 4 * q >= end) {
+        mean[q] = rstd[q] = 0.0f;
+        dy[q] = u32x4{0u, 0u, 0u, 0u};
+      }
+  }
+};
+
+// Few rows: two launches.  The first reads x and dy by tiles (a group of rows
+// by 64 V columns; the 4 waves take the group's rows in turn) and sums both
+// ways: down its columns for dw and db, along its part of each row for dx's
+// two means.
+template <class C, class P>
+__global__ __launch_bounds__(256) void norm_back_tiles(const NormBackArgs a) {
   constexpr int V = C::V;
   __shared__ float part[4][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -313,21 +347,47 @@ __global__ __launch_bounds__(256) void norm_back_columns(const NormBackArgs a) {
   const uint64_t first = static_cast<uint64_t>(blockIdx.y) * a.rows_per_group;
   uint64_t end = first + a.rows_per_group;
   if (end > a.rows) end = a.rows;
-  float dw[V], db[V];
+  float dw[V], db[V], w[V];
+  load_params<P, V>(a.w, n, valid, 1.0f, w);
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
-#pragma unroll 2
-  for (uint64_t row = first + wave; row < end; row += 4) {
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float h[V], g[V];
-    C::unpack(load_upto<C>(a.x + (row * a.x_stride + n) * C::kElemBytes, valid), h);
-    C::unpack(load_upto<C>(a.dy + (row * a.dy_stride + n) * C::kElemBytes, valid), g);
+  with_edges(n - lane * V + 64 * V <= a.width, [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
+    for (uint64_t row0 = first + wave; row0 < end; row0 += 4 * kTileRows) {
+      TileRows<C, kFull> rows;
+      rows.load(a, row0, end, n, valid);
+      float s[kTileRows][2];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      dw[i] = fmaf(g[i], (h[i] - mean) * rstd, dw[i]);
-      db[i] += g[i];
+      for (int q = 0; q < kTileRows; ++q) {
+        float h[V], g[V];
+        C::unpack(rows.x[q], h);
+        C::unpack(rows.dy[q], g);
+        s[q][0] = s[q][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          h[i] = kFull || i < valid ? (h[i] - rows.mean[q]) * rows.rstd[q] : 0.0f;
+          dw[i] = fmaf(g[i], h[i], dw[i]);
+          db[i] += g[i];
+          const float gw = kFull || i < valid ? g[i] * w[i] : 0.0f;
+          s[q][0] += gw;
+          s[q][1] = fmaf(gw, h[i], s[q][1]);
+        }
+      }
+      if (a.dx) {
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+#pragma unroll
+          for (int q = 0; q < kTileRows; ++q) {
+            s[q][0] += __shfl_xor(s[q][0], d, 64);
+            s[q][1] += __shfl_xor(s[q][1], d, 64);
+          }
+#pragma unroll
+        for (int q = 0; q < kTileRows; ++q)
+          if (lane == 0 && row0 + 4 * q < end)
+            *reinterpret_cast<f32x2*>(a.along + ((row0 + 4 * q) * gridDim.x + blockIdx.x) * 2) = f32x2{s[q][0], s[q][1]};
+      }
     }
-  }
+  });
   for (int which = 0; which < 2; ++which) {
     if (which) __syncthreads();
 #pragma unroll
@@ -341,6 +401,154 @@ __global__ __launch_bounds__(256) void norm_back_columns(const NormBackArgs a) {
   }
 }
 
+// dx, dw and db in one pass over x and dy, for many rows.  A workgroup of
+// 512 threads stays and walks over the rows: kThreads of them hold a row
+// (so 512 / kThreads rows side by side), kRows rows in turn go through one
+// reduction, and each thread keeps its columns' weights and its columns' sums
+// of dw and db in registers.  The next rows are on their way while the present
+// ones are reduced.  At the end each workgroup writes one row of partial sums
+// of dw and of db, which column_join adds: 256 workgroups' partial sums are
+// 4 KiB a column, a second read of x and dy 4 or 8 bytes a row and column.
+template <class C, class P, int kThreads, int kVecs, int kRows>
+__global__ __launch_bounds__(512) void norm_back_fused(const NormBackArgs a) {
+  constexpr int V = C::V;
+  constexpr int kSlots = 512 / kThreads, kWaves = kThreads / 64;
+  __shared__ float lds[2][8][2 * kRows];
+  const int tid = threadIdx.x % kThreads;
+  const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  int valid[kVecs];
+  float w[kVecs][V], dw[kVecs][V], db[kVecs][V];
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
+    valid[k] = n >= a.width ? 0 : (a.width - n < V ? static_cast<int>(a.width - n) : V);
+    load_params<P, V>(a.w, n, valid[k], 1.0f, w[k]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+  }
+  const uint64_t round = static_cast<uint64_t>(gridDim.x) * kSlots * kRows;
+  uint64_t row0 = (static_cast<uint64_t>(blockIdx.x) * kSlots + slot) * kRows;
+  struct Held {
+    u32x4 x[kVecs], dy[kVecs];
+    float mean, rstd;
+  };
+  Held now[kRows], next[kRows];
+  auto load = [&](Held* to, uint64_t first) {
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const uint64_t row = first + q;
+      const bool in = row < a.rows;  // a row that is not there adds 0 to every sum
+      to[q].mean = in ? a.mean[row] : 0.0f;
+      to[q].rstd = in ? a.rstd[row] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
+        to[q].x[k] = load_upto<C>(a.x + (row * a.x_stride + n) * C::kElemBytes, in ? valid[k] : 0);
+        to[q].dy[k] = load_upto<C>(a.dy + (row * a.dy_stride + n) * C::kElemBytes, in ? valid[k] : 0);
+      }
+    }
+  };
+  const float inv = 1.0f / static_cast<float>(a.width);
+  int turn = 0;
+  load(now, row0);
+  // every wave of the workgroup runs the same number of rounds
+  for (uint64_t first = static_cast<uint64_t>(blockIdx.x) * kSlots * kRows; first < a.rows; first += round) {
+    load(next, row0 + round);
+    float s[2 * kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      s[2 * q] = s[2 * q + 1] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        float h[V], g[V];
+        C::unpack(now[q].x[k], h);
+        C::unpack(now[q].dy[k], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          h[i] = i < valid[k] ? (h[i] - now[q].mean) * now[q].rstd : 0.0f;
+          dw[k][i] = fmaf(g[i], h[i], dw[k][i]);
+          db[k][i] += g[i];
+          const float gw = i < valid[k] ? g[i] * w[k][i] : 0.0f;
+          s[2 * q] += gw;
+          s[2 * q + 1] = fmaf(gw, h[i], s[2 * q + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * kRows; ++i)
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) s[i] += __shfl_xor(s[i], d, 64);
+    if constexpr (kWaves > 1) {
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < 2 * kRows; ++i) lds[turn][threadIdx.x >> 6][i] = s[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2 * kRows; ++i) {
+        s[i] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) s[i] += lds[turn][slot * kWaves + v][i];
+      }
+      turn ^= 1;
+    }
+    if (a.dx) {
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) {
+        if (row0 + q >= a.rows) continue;
+        const float c0 = s[2 * q] * inv, c1 = s[2 * q + 1] * inv;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
+          float h[V], g[V];
+          forget(now[q].x[k]);
+          forget(now[q].dy[k]);
+          C::unpack(now[q].x[k], h);
+          C::unpack(now[q].dy[k], g);
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            g[i] = now[q].rstd * (g[i] * w[k][i] - c0 - (h[i] - now[q].mean) * now[q].rstd * c1);
+          store_upto<C>(a.dx + ((row0 + q) * a.dx_stride + n) * C::kElemBytes, g, valid[k]);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) now[q] = next[q];
+    row0 += round;
+  }
+  if constexpr (kSlots == 1) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float* out = a.sums + (2 * static_cast<uint64_t>(blockIdx.x) + which) * a.sums_stride;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const uint64_t n = (static_cast<uint64_t>(k) * kThreads + tid) * V;
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {  // rows of the partial sums are padded to whole vectors
+          const float* v = which ? &db[k][i] : &dw[k][i];
+          if (n + i < a.width) *reinterpret_cast<f32x4*>(out + n + i) = f32x4{v[0], v[1], v[2], v[3]};
+        }
+      }
+    }
+  } else {
+    static_assert(kSlots == 1 || kVecs == 1, "several rows side by side hold one vector a thread");
+    __shared__ float part[kSlots][kThreads * V + 1];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i) part[slot][tid * V + i] = which ? db[0][i] : dw[0][i];
+      __syncthreads();
+      float* out = a.sums + (2 * static_cast<uint64_t>(blockIdx.x) + which) * a.sums_stride;
+      for (uint64_t c = threadIdx.x; c < a.width; c += 512) {
+        float t = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kSlots; ++v) t += part[v][c];
+        out[c] = t;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ column sums
 
 struct JoinArgs {
@@ -350,14 +558,13 @@ struct JoinArgs {
   uint32_t groups, kinds;
 };
 
-// Adds the groups' column sums (blockIdx.y: the kind) in a fixed order and
-// rounds them: 32 columns a workgroup, 8 threads a column.
+// Adds the groups' column sums of one kind in a fixed order and rounds them:
+// 32 columns a workgroup, 8 threads a column.
 template <class P>
-__global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
+__device__ inline void join_block(const JoinArgs& a, uint64_t block, uint32_t kind) {
   __shared__ float part[8][33];
   const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-  const uint64_t col = static_cast<uint64_t>(blockIdx.x) * 32 + c;
-  const uint32_t kind = blockIdx.y;
+  const uint64_t col = block * 32 + c;
   float s = 0.0f;
   if (col < a.width)
 #pragma unroll 4
@@ -370,6 +577,71 @@ __global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
     for (int i = 0; i < 8; ++i) t += part[i][c];
     reinterpret_cast<typename P::Bits*>(a.out[kind])[col] = P::narrow(t);
   }
+}
+
+template <class P>
+__global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
+  join_block<P>(a, blockIdx.x, blockIdx.y);
+}
+
+// The second launch for few rows: the first `tiles` workgroups turn
+// norm_back_tiles' row sums into dx, tile by tile (x and dy come from the
+// caches by then), the others join its column sums.
+template <class C, class P>
+__global__ __launch_bounds__(256) void norm_back_apply(const NormBackArgs a, const JoinArgs join, uint32_t blocks,
+                                                       uint32_t tiles, uint32_t joins) {
+  constexpr int V = C::V;
+  if (blockIdx.x >= tiles) {
+    const uint32_t id = blockIdx.x - tiles;
+    join_block<P>(join, id % joins, id / joins);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t n = (static_cast<uint64_t>(blockIdx.x % blocks) * 64 + lane) * V;
+  const int valid = n >= a.width ? 0 : (a.width - n < V ? static_cast<int>(a.width - n) : V);
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x / blocks) * a.rows_per_group;
+  uint64_t end = first + a.rows_per_group;
+  if (end > a.rows) end = a.rows;
+  float w[V];
+  load_params<P, V>(a.w, n, valid, 1.0f, w);
+  const float inv = 1.0f / static_cast<float>(a.width);
+  with_edges(n - lane * V + 64 * V <= a.width, [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
+    for (uint64_t row0 = first + wave; row0 < end; row0 += 4 * kTileRows) {
+      TileRows<C, kFull> rows;
+      rows.load(a, row0, end, n, valid);
+      float s[kTileRows][2];
+#pragma unroll
+      for (int q = 0; q < kTileRows; ++q) s[q][0] = s[q][1] = 0.0f;
+      for (uint32_t b = lane; b < blocks; b += 64)
+#pragma unroll
+        for (int q = 0; q < kTileRows; ++q)
+          if (row0 + 4 * q < end) {
+            const f32x2 p = *reinterpret_cast<const f32x2*>(a.along + ((row0 + 4 * q) * blocks + b) * 2);
+            s[q][0] += p[0];
+            s[q][1] += p[1];
+          }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1)
+#pragma unroll
+        for (int q = 0; q < kTileRows; ++q) {
+          s[q][0] += __shfl_xor(s[q][0], d, 64);
+          s[q][1] += __shfl_xor(s[q][1], d, 64);
+        }
+#pragma unroll
+      for (int q = 0; q < kTileRows; ++q) {
+        if (row0 + 4 * q >= end) continue;
+        const float c0 = s[q][0] * inv, c1 = s[q][1] * inv;
+        float h[V], g[V];
+        C::unpack(rows.x[q], h);
+        C::unpack(rows.dy[q], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          g[i] = rows.rstd[q] * (g[i] * w[i] - c0 - (h[i] - rows.mean[q]) * rows.rstd[q] * c1);
+        store_upto<C>(a.dx + ((row0 + 4 * q) * a.dx_stride + n) * C::kElemBytes, g, kFull ? V : valid);
+      }
+    }
+  });
 }
 
 }  // namespace mscl

@@ -185,7 +185,7 @@ constexpr int kCus = 256;  // of an MI355X: the plans must not depend on a devic
 
 // How one product m x n x k runs.
 struct ProductPlan {
-  int tile = 64;         // 64 or 128: linear_tile's square; 256: linear_big's
+  int tile = 64;         // 64 or 128: linear_tile's square; 256: linear_big's; 16, 32: linear_few's rows of w
   bool pack_a = false, pack_b = false;  // operands laid out anew for linear_big
   uint32_t shares = 1;   // of k
   uint32_t blocks_per_share = 1;
@@ -224,6 +224,19 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     }
     p.pack_a = p.pack_b = false;
   }
+  if (a_along && b_along && m <= 64 && k > 0) {
+    const uint64_t whole = std::max<uint64_t>(1, k / block);
+    p.tile = ceil_div(n, 32) >= kCus ? 32 : 16;
+    const uint64_t groups = ceil_div(n, p.tile);
+    // 8 waves of a workgroup split k already; shares only where the
+    // workgroups leave compute units idle, and of 4 steps a wave at least
+    const uint64_t shares = groups < kCus ? std::max<uint64_t>(1, std::min(kCus / groups, whole / 32)) : 1;
+    p.blocks_per_share = static_cast<uint32_t>(ceil_div(whole, shares));
+    p.shares = static_cast<uint32_t>(ceil_div(whole, p.blocks_per_share));
+    p.partial_stride = round_up(n, 8);
+    if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
+    return p;
+  }
   const uint64_t large = ceil_div(m, 128) * ceil_div(n, 128);
   p.tile = large >= kCus ? 128 : 64;
   const uint64_t tiles = ceil_div(m, p.tile) * ceil_div(n, p.tile);
@@ -256,10 +269,31 @@ hipError_t allow_lds() {
   return e;
 }
 
+template <class C>
+void launch_few(int tile, const TileArgs& t, dim3 grid, hipStream_t stream) {
+  const uint64_t m = t.e.m;
+  if (tile == 16) {
+    if (m <= 16)
+      linear_few<C, 1, 1, 4><<<grid, 512, 0, stream>>>(t);
+    else if (m <= 32)
+      linear_few<C, 2, 1, 2><<<grid, 512, 0, stream>>>(t);
+    else
+      linear_few<C, 4, 1, 2><<<grid, 512, 0, stream>>>(t);
+  } else {
+    if (m <= 16)
+      linear_few<C, 1, 2, 2><<<grid, 512, 0, stream>>>(t);
+    else if (m <= 32)
+      linear_few<C, 2, 2, 2><<<grid, 512, 0, stream>>>(t);
+    else
+      linear_few<C, 4, 2, 1><<<grid, 512, 0, stream>>>(t);
+  }
+}
+
 template <class C, bool kAAlong, bool kBAlong>
 mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, const Epilogue& e0, char* workspace,
                       hipStream_t stream) {
-  const uint64_t tm = ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
+  const bool few = p.tile <= 32;
+  const uint64_t tm = few ? 1 : ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
   if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
   const uint32_t groups = static_cast<uint32_t>(tm * tn);
   if constexpr (C::kElemBytes == 2) {
@@ -286,7 +320,9 @@ mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, co
   t.tiles_n = static_cast<uint32_t>(tn);
   t.blocks_per_share = p.blocks_per_share;
   const dim3 grid(groups, p.shares);
-  if (p.tile == 128)
+  if (few) {
+    if constexpr (kAAlong && kBAlong) launch_few<C>(p.tile, t, grid, stream);
+  } else if (p.tile == 128)
     linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
   else
     linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
@@ -431,19 +467,50 @@ mscl_status_t check_layer_norm_backward(const mscl_layer_norm_backward_t* c, Spa
 
 struct NormBackPlan {
   bool sums = false;
+  bool fused = false;  // norm_back_fused, with `groups` workgroups
   uint32_t groups = 0, rows_per_group = 0;
+  uint64_t blocks = 0;  // of columns, in norm_back_tiles
   uint64_t sums_stride = 0;
-  size_t bytes = 0;
+  size_t along_at = 0, bytes = 0;
 };
+
+// Threads that hold a row of `vecs` vectors in norm_back_fused.
+int fused_threads(uint64_t vecs) { return vecs <= 64 ? 64 : vecs <= 128 ? 128 : vecs <= 256 ? 256 : 512; }
 
 NormBackPlan plan_layer_norm_backward(const mscl_layer_norm_backward_t& c) {
   NormBackPlan p;
   p.sums = c.dweight || c.dbias;
   if (!p.sums) return p;
-  plan_groups(c.rows, ceil_div(c.width, 64 * (16 / bytes_of(c.dtype))), &p.groups, &p.rows_per_group);
-  p.sums_stride = round_up(c.width, 4);
-  p.bytes = size_t(p.groups) * 2 * p.sums_stride * 4;
+  p.sums_stride = round_up(c.width, 8);
+  const uint64_t e = bytes_of(c.dtype), vecs = ceil_div(c.width, 16 / e);
+  // Partial sums written and read (16 bytes a column and workgroup) against a
+  // second read of x and dy (2 e bytes a row and column).
+  if (c.dx && vecs <= (e == 4 ? 2048 : 1024) && c.rows * 2 * e >= 16 * kCus) {
+    p.fused = true;
+    const uint64_t at_once = vecs > 1024 ? 1 : 2 * (512 / fused_threads(vecs));
+    p.groups = static_cast<uint32_t>(std::min<uint64_t>(kCus, ceil_div(c.rows, at_once)));
+  } else {
+    p.blocks = ceil_div(c.width, 64 * (16 / e));
+    plan_groups(c.rows, p.blocks, &p.groups, &p.rows_per_group);
+  }
+  p.along_at = round_up(size_t(p.groups) * 2 * p.sums_stride * 4, 256);
+  p.bytes = p.along_at + (c.dx ? c.rows * p.blocks * 8 : 0);
   return p;
+}
+
+template <class C, class P>
+void launch_norm_back_fused(const NormBackArgs& a, uint32_t groups, hipStream_t s) {
+  const uint64_t vecs = ceil_div(a.width, C::V);
+  if (C::V == 4 && vecs > 1024)
+    norm_back_fused<C, P, 512, C::V == 4 ? 4 : 2, C::V == 4 ? 1 : 2><<<groups, 512, 0, s>>>(a);
+  else if (vecs > 512)
+    norm_back_fused<C, P, 512, 2, 2><<<groups, 512, 0, s>>>(a);
+  else switch (fused_threads(vecs)) {
+    case 64: norm_back_fused<C, P, 64, 1, 2><<<groups, 512, 0, s>>>(a); break;
+    case 128: norm_back_fused<C, P, 128, 1, 2><<<groups, 512, 0, s>>>(a); break;
+    case 256: norm_back_fused<C, P, 256, 1, 2><<<groups, 512, 0, s>>>(a); break;
+    default: norm_back_fused<C, P, 512, 1, 2><<<groups, 512, 0, s>>>(a);
+  }
 }
 
 // A row's 16-byte vectors -> threads and vectors per thread that hold it.
@@ -485,12 +552,14 @@ void launch_norm_back(const NormBackArgs& a, hipStream_t s) {
     norm_back_rows<C, P, 256, 4><<<rows, 256, 0, s>>>(a);
   else if (vecs <= 2048)
     norm_back_rows<C, P, 1024, 2><<<rows, 1024, 0, s>>>(a);
+  else if (vecs <= 4096 && C::V == 4)
+    norm_back_rows<C, P, 1024, C::V == 4 ? 4 : 2><<<rows, 1024, 0, s>>>(a);
   else
     norm_back_rows_wide<C, P><<<rows, 1024, 0, s>>>(a);
 }
 
-mscl_status_t join_columns(int param_dtype, const float* sums, uint64_t stride, uint64_t width, uint32_t groups,
-                           void* first, void* second, uint32_t kinds, hipStream_t stream) {
+JoinArgs join_args(const float* sums, uint64_t stride, uint64_t width, uint32_t groups, void* first, void* second,
+                   uint32_t kinds) {
   JoinArgs j;
   j.sums = sums;
   j.out[0] = bytes_at(first);
@@ -499,6 +568,12 @@ mscl_status_t join_columns(int param_dtype, const float* sums, uint64_t stride, 
   j.width = width;
   j.groups = groups;
   j.kinds = kinds;
+  return j;
+}
+
+mscl_status_t join_columns(int param_dtype, const float* sums, uint64_t stride, uint64_t width, uint32_t groups,
+                           void* first, void* second, uint32_t kinds, hipStream_t stream) {
+  const JoinArgs j = join_args(sums, stride, width, groups, first, second, kinds);
   const uint64_t blocks = ceil_div(width, 32);
   if (blocks > kMostGroups) return bad("the rows are too wide");
   return with_codec(param_dtype, [&](auto p) {
@@ -696,20 +771,34 @@ mscl_status_t mscl_layer_norm_backward(const mscl_layer_norm_backward_t* call, v
   a.dx = bytes_at(c.dx);
   a.dx_stride = c.dx_stride;
   a.sums = reinterpret_cast<float*>(workspace);
+  a.along = nullptr;
   a.sums_stride = p.sums_stride;
   a.rows = c.rows;
   a.width = c.width;
   a.rows_per_group = p.rows_per_group;
-  if (p.sums) {  // before dx, which may be written over dy
-    const uint64_t blocks = ceil_div(c.width, 64 * (16 / bytes_of(c.dtype)));
-    if (blocks > kMostGroups) return bad("the rows are too wide");
-    st = with_codec(c.dtype, [&](auto t) {
-      norm_back_columns<decltype(t)><<<dim3(static_cast<uint32_t>(blocks), p.groups), 256, 0, s>>>(a);
-      return launched("norm_back_columns");
+  if (p.fused) {
+    st = with_codecs(c.dtype, c.param_dtype, [&](auto t, auto q) {
+      launch_norm_back_fused<decltype(t), decltype(q)>(a, p.groups, s);
+      return launched("norm_back_fused");
     });
     if (st != MSCL_SUCCESS) return st;
-    st = join_columns(c.param_dtype, a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2, s);
-    if (st != MSCL_SUCCESS) return st;
+    return join_columns(c.param_dtype, a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2, s);
+  }
+  if (p.sums) {
+    a.along = reinterpret_cast<float*>(bytes_at(workspace) + p.along_at);
+    const uint64_t tiles = c.dx ? p.blocks * ceil_div(c.rows, p.rows_per_group) : 0, joins = ceil_div(c.width, 32);
+    if (joins > kMostGroups / 4 || tiles > kMostGroups / 2) return bad("the matrices have too many tiles");
+    return with_codecs(c.dtype, c.param_dtype, [&](auto t, auto q) {
+      using T = decltype(t);
+      using Q = decltype(q);
+      norm_back_tiles<T, Q><<<dim3(static_cast<uint32_t>(p.blocks), p.groups), 256, 0, s>>>(a);
+      const mscl_status_t done = launched("norm_back_tiles");
+      if (done != MSCL_SUCCESS) return done;
+      const JoinArgs j = join_args(a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2);
+      norm_back_apply<T, Q><<<static_cast<uint32_t>(tiles + 2 * joins), 256, 0, s>>>(
+          a, j, static_cast<uint32_t>(p.blocks), static_cast<uint32_t>(tiles), static_cast<uint32_t>(joins));
+      return launched("norm_back_apply");
+    });
   }
   if (!c.dx || c.rows == 0) return MSCL_SUCCESS;
   return with_codecs(c.dtype, c.param_dtype, [&](auto t, auto q) {

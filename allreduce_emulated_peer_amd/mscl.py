@@ -287,10 +287,25 @@ def allreduce_tensors(inputs, outputs, algo: int = ALGO_AUTO, stream=None) -> No
 
 # ---------------------------------------------------------------- linear layer and layer norm
 
-def _codes():
-    import torch
+# A call on small matrices takes as long on the host as on the GPU, so these
+# functions look each thing up once and take the common case (a matrix, on the
+# current device and stream) first.
+_torch = None
+_CODES = {}  # torch dtype -> element type code
+_raw_stream = None
 
-    return {torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16}
+
+def _need_torch():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+
+        _CODES.update({torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16})
+        # the current stream's handle without a Stream object around it (2 us less), where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch = torch
+    return _torch
 
 
 def _same_kind(like, **tensors):
@@ -306,31 +321,35 @@ def _same_kind(like, **tensors):
 
 def _matrix(name, t, cols):
     """`t` as rows of `cols` elements that lie next to each other: a view where strides allow one."""
-    if t.dim() == 0 or t.shape[-1] != cols:
+    shape = t.shape
+    if not shape or shape[-1] != cols:
         raise ValueError(f"{name} must have {cols} columns")
-    if t.dim() != 2:
-        t = t.reshape(-1, cols) if cols else t.reshape(t.shape[:-1].numel(), 0)
-    if t.stride(1) != 1 and cols > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < cols:
-        raise ValueError(f"the rows of {name} must not overlap")
+    if len(shape) != 2:
+        t = t.reshape(-1, cols) if cols else t.reshape(shape[:-1].numel(), 0)
+    if not t.is_contiguous():
+        row, element = t.stride()
+        if element != 1 and cols > 1:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        if row < cols and t.shape[0] > 1:
+            raise ValueError(f"the rows of {name} must not overlap")
     return t
 
 
 def _vector(name, t, n):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
 def _on_stream(device, stream, tensors, run):
     """run(stream handle) with `device` current and allocations made for `stream` (default: torch's current one)."""
-    import torch
-
-    if stream is None and device.index == torch.cuda.current_device():
-        return run(torch.cuda.current_stream(device).cuda_stream)
+    torch = _torch
+    index = device.index
+    if index == torch.cuda.current_device():
+        if stream is None:
+            return run(_raw_stream(index))
     with torch.cuda.device(device):
         if stream is None:
-            return run(torch.cuda.current_stream(device).cuda_stream)
+            return run(_raw_stream(index))
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
@@ -342,13 +361,13 @@ def _on_stream(device, stream, tensors, run):
 
 def _workspace(query, call, like):
     """The workspace that a call asks for, as (tensor or None, its bytes)."""
-    import torch
-
     need = ctypes.c_size_t()
-    _check(query(call, ctypes.byref(need)), query.__name__)
+    status = query(call, ctypes.byref(need))
+    if status:
+        _check(status, query.__name__)
     if need.value == 0:
         return None, 0
-    return torch.empty(need.value, dtype=torch.uint8, device=like.device), need.value
+    return _torch.empty(need.value, dtype=_torch.uint8, device=like.device), need.value
 
 
 def _address(t):
@@ -368,10 +387,8 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
     ACTIVATION_CODES.  Returns y (..., out), or (y, preact) with return_preact:
     what linear_backward_tensors needs where there is an activation.
     """
-    import torch
-
-    lib = load()
-    dtype = _codes().get(x.dtype)
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = _CODES.get(x.dtype)
     if dtype is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
     if activation not in ACTIVATION_CODES:
@@ -399,7 +416,9 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
                            _row_stride(rm), y.data_ptr(), n, _address(z), n, rows, k, n, dtype,
                            ACTIVATION_CODES[activation])
         space, size = _workspace(lib.mscl_linear_workspace, call, x)
-        _check(lib.mscl_linear(call, _address(space), size, handle or None), "mscl_linear")
+        status = lib.mscl_linear(call, _address(space), size, handle or None)
+        if status:
+            _check(status, "mscl_linear")
         if x.dim() != 2:
             y = y.view(x.shape[:-1] + (n,))
             z = z.view(y.shape) if return_preact else None
@@ -416,10 +435,8 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
     linear_tensors returned with return_preact (needed unless activation is
     "none").  A gradient that is not needed is None.
     """
-    import torch
-
-    lib = load()
-    dtype = _codes().get(dy.dtype)
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = _CODES.get(dy.dtype)
     if dtype is None:
         raise ValueError(f"unsupported dtype {dy.dtype}")
     if activation not in ACTIVATION_CODES:
@@ -452,7 +469,9 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
                                     wm.stride(0), _address(zm), _row_stride(zm), _address(dx), k, _address(dw), k,
                                     _address(db), rows, k, n, dtype, ACTIVATION_CODES[activation])
         space, size = _workspace(lib.mscl_linear_backward_workspace, call, dy)
-        _check(lib.mscl_linear_backward(call, _address(space), size, handle or None), "mscl_linear_backward")
+        status = lib.mscl_linear_backward(call, _address(space), size, handle or None)
+        if status:
+            _check(status, "mscl_linear_backward")
         if need_dx and x.dim() != 2:
             dx = dx.view(x.shape)
         return dx, dw, db
@@ -462,17 +481,17 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
 
 def _param_code(like, **tensors):
     """The parameters' type: that of the rows, or float32; None entries say nothing."""
-    import torch
-
-    kinds = {t.dtype for t in tensors.values() if t is not None}
-    if len(kinds) > 1 or not kinds <= {like.dtype, torch.float32}:
-        raise ValueError(f"parameters must all be of {like.dtype} or all of float32")
+    kind = None
     for name, t in tensors.items():
         if t is not None:
+            if kind is None:
+                kind = t.dtype
+            if t.dtype != kind or kind != like.dtype and kind != _torch.float32:
+                raise ValueError(f"parameters must all be of {like.dtype} or all of float32")
             if t.device != like.device:
                 raise ValueError(f"{name} must be on {like.device}")
             _vector(name, t, like.shape[-1])
-    return kinds.pop() if kinds else like.dtype
+    return kind or like.dtype
 
 
 def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, stream=None):
@@ -482,10 +501,8 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     with return_stats: float32 of x's leading shape, what
     layer_norm_backward_tensors needs.
     """
-    import torch
-
-    lib = load()
-    codes = _codes()
+    torch, lib = _torch or _need_torch(), _lib or load()
+    codes = _CODES
     if x.dtype not in codes:
         raise ValueError(f"unsupported dtype {x.dtype}")
     if x.dim() == 0 or x.shape[-1] == 0:
@@ -500,12 +517,14 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     rows = xm.shape[0]
 
     def run(handle):
-        y = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        y = torch.empty_like(xm) if xm.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
         rstd = torch.empty_like(mean) if return_stats else None
         call = LAYER_NORM.pack(xm.data_ptr(), xm.stride(0), _address(weight), _address(bias), y.data_ptr(), width,
                                _address(mean), _address(rstd), rows, width, eps, codes[x.dtype], param)
-        _check(lib.mscl_layer_norm(call, handle or None), "mscl_layer_norm")
+        status = lib.mscl_layer_norm(call, handle or None)
+        if status:
+            _check(status, "mscl_layer_norm")
         if x.dim() != 2:
             y = y.view(x.shape)
         return (y, mean, rstd) if return_stats else y
@@ -520,10 +539,8 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
     weight's dtype (dy's without a weight).  A gradient that is not needed is
     None.
     """
-    import torch
-
-    lib = load()
-    codes = _codes()
+    torch, lib = _torch or _need_torch(), _lib or load()
+    codes = _CODES
     if dy.dtype not in codes:
         raise ValueError(f"unsupported dtype {dy.dtype}")
     if dy.dim() == 0 or dy.shape[-1] == 0:
@@ -549,7 +566,9 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
                                         rstd.data_ptr(), _address(weight), _address(dx), width, _address(dw),
                                         _address(db), rows, width, codes[dy.dtype], codes[kind])
         space, size = _workspace(lib.mscl_layer_norm_backward_workspace, call, dy)
-        _check(lib.mscl_layer_norm_backward(call, _address(space), size, handle or None), "mscl_layer_norm_backward")
+        status = lib.mscl_layer_norm_backward(call, _address(space), size, handle or None)
+        if status:
+            _check(status, "mscl_layer_norm_backward")
         if need_dx and dy.dim() != 2:
             dx = dx.view(dy.shape)
         return dx, dw, db

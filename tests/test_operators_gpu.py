@@ -296,7 +296,8 @@ def test_offsets_beyond_32_bits():
 
 NORM_SIZES = [(1, 1), (3, 2), (5, 7), (1, 8), (9, 64), (4, 129), (7, 511), (33, 512), (6, 1000), (2, 1025), (17, 2048),
               (3, 2049), (5, 4097), (70, 768), (2, 8192), (3, 8193), (2, 16387), (1, 20001), (2, 33000), (1, 70001),
-              (260, 300), (1030, 24), (2051, 40)]
+              (260, 300), (1030, 24), (2051, 40), (1100, 700), (1025, 1500),
+              (1100, 3000), (1027, 5000), (2050, 12001)]
 
 
 def norm_case(gen, rows, width, t, p):
