@@ -724,6 +724,187 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   });
 }
 
+// ------------------------------------------------------------------ binary32 products
+
+// A binary32 value is the sum of three bfloat16 values: its nearest, the
+// nearest to what is left, and what is left then (8 bits each, so nothing of
+// the 24 is lost above bfloat16's smallest values).  Of the nine products of
+// two such sums the six largest are taken, on the bfloat16 matrix units; the
+// others are below 2^-26 of the product, less than one binary32 rounding of
+// it.  Six bfloat16 MFMAs take 96 cycles where the binary32 MFMAs of the same
+// 16 x 16 x 32 take 256.
+// Infinities and NaN have no such parts (inf - inf): they make the tile's sums
+// non-finite, and a tile with a non-finite sum is summed again in binary32.
+struct Parts {
+  u32x4 part[3];  // of eight values
+};
+
+__device__ inline Parts split(const u32x4& lo, const u32x4& hi) {
+  float v[8];
+  F32::unpack(lo, v);
+  F32::unpack(hi, v + 4);
+  Parts o;
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    o.part[p] = BF16::pack(v);
+    if (p == 2) break;
+    float t[8];
+    BF16::unpack(o.part[p], t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] -= t[i];
+  }
+  return o;
+}
+
+// One operand's kT x 64 block of k: binary32 from memory, three planes of
+// bfloat16 in LDS, each in Stage<BF16>'s layout.
+template <bool kAlong, int kT>
+struct SplitStage {
+  using S = Stage<BF16, kAlong, kT, 256>;
+  static constexpr int kChunks = S::kChunks, kPerRow = S::kPerRow;
+  static constexpr int kBytes = 3 * S::kBytes;
+  u32x4 held[kChunks][2];
+
+  __device__ inline void load(const Operand& o, uint64_t first, uint64_t k0, uint64_t k_end) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = i * 256 + threadIdx.x;
+      const int r = id / kPerRow, c = id % kPerRow;
+      const uint64_t row = (kAlong ? first : k0) + r;
+      const uint64_t col = (kAlong ? k0 : first) + static_cast<uint64_t>(c) * 8;
+      const uint64_t rows = kAlong ? o.rows : k_end;
+      const uint64_t cols = kAlong ? k_end : o.cols;
+      int valid = 0;
+      if (row < rows && col < cols) valid = cols - col < 8 ? static_cast<int>(cols - col) : 8;
+      const char* p = o.base + (row * o.stride + col) * 4;
+      held[i][0] = load_upto<F32>(p, valid);
+      held[i][1] = load_upto<F32>(p + 16, valid - 4);
+    }
+  }
+  __device__ inline void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = i * 256 + threadIdx.x;
+      const int r = id / kPerRow, c = id % kPerRow;
+      const Parts o = split(held[i][0], held[i][1]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<u32x4*>(lds + p * S::kBytes + (r * kPerRow + S::swizzle(r, c)) * 16) = o.part[p];
+    }
+  }
+  static __device__ inline u32x4 fragment(const char* lds, int plane, int p, int s) {
+    return S::fragment(lds + plane * S::kBytes, p, s);
+  }
+};
+
+// One value of an operand, 0 outside of it.
+template <bool kAlong>
+__device__ inline float value_at(const Operand& o, uint64_t i, uint64_t k, uint64_t k_end) {
+  const uint64_t row = kAlong ? i : k, col = kAlong ? k : i;
+  if (row >= o.rows || col >= o.cols || k >= k_end) return 0.0f;
+  return *reinterpret_cast<const float*>(o.base + (row * o.stride + col) * 4);
+}
+
+// kBM x kBN tiles by 4 waves in a square, 64 k at a time.  One LDS buffer, as
+// three planes of it let two workgroups share a compute unit: one splits and
+// stores while the other multiplies.
+template <bool kAAlong, bool kBAlong, int kBM, int kBN>
+__global__ __launch_bounds__(256, 2) void linear_split(const TileArgs t) {
+  using SA = SplitStage<kAAlong, kBM>;
+  using SB = SplitStage<kBAlong, kBN>;
+  constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t tm = blockIdx.x % t.tiles_m, tn = blockIdx.x / t.tiles_m;
+  const uint64_t m0 = static_cast<uint64_t>(tm) * kBM, n0 = static_cast<uint64_t>(tn) * kBN;
+  const int wave = threadIdx.x >> 6;
+  const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
+  const uint64_t k_first = static_cast<uint64_t>(blockIdx.y) * t.blocks_per_share * 64;
+  uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * 64;
+  if (k_end > t.k) k_end = t.k;
+
+  f32x4 acc[1][kWM][kWN];
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  SA sa;
+  SB sb;
+  if (k_first < k_end) {
+    sa.load(t.a, m0, k_first, k_end);
+    sb.load(t.b, n0, k_first, k_end);
+  }
+  for (uint64_t k0 = k_first; k0 < k_end; k0 += 64) {
+    sa.store(lds);
+    sb.store(lds + SA::kBytes);
+    __syncthreads();
+    if (k0 + 64 < k_end) {
+      sa.load(t.a, m0, k0 + 64, k_end);
+      sb.load(t.b, n0, k0 + 64, k_end);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 fb[3][kWN];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
+#pragma unroll
+      for (int i = 0; i < kWM; ++i) {
+        u32x4 fa[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
+        // the smaller products first
+#pragma unroll
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+          for (int p = 0; p <= sum; ++p)
+#pragma unroll
+            for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+      }
+    }
+    __syncthreads();
+  }
+
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int j = 0; j < kWN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) odd |= !(fabsf(acc[0][i][j][c]) < INFINITY);
+  if (__any(odd)) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (uint64_t k = k_first; k < k_end; k += 4) {
+      float a[kWM], b[kWN];
+#pragma unroll
+      for (int i = 0; i < kWM; ++i) a[i] = value_at<kAAlong>(t.a, m0 + wm + 16 * i + r, k + g, k_end);
+#pragma unroll
+      for (int j = 0; j < kWN; ++j) b[j] = value_at<kBAlong>(t.b, n0 + wn + 16 * j + r, k + g, k_end);
+#pragma unroll
+      for (int i = 0; i < kWM; ++i)
+#pragma unroll
+        for (int j = 0; j < kWN; ++j)
+          acc[0][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[i], acc[0][i][j], 0, 0, 0);
+    }
+  }
+  if (t.e.partial) {
+    using G = Groups<F32, kWM, kWN>;
+#pragma unroll
+    for (int q = 0; q < G::kCount; ++q) {
+      float v[4];
+      G::sums(acc[0], q, v);
+      keep_partial<F32>(t.e, blockIdx.y, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
+    }
+  } else {
+    finish_all<F32>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
+  }
+}
+
 // ------------------------------------------------------------------ few rows
 
 // Products of up to 64 rows, where the pass over w bounds: 8 waves share

@@ -185,7 +185,8 @@ constexpr int kCus = 256;  // of an MI355X: the plans must not depend on a devic
 
 // How one product m x n x k runs.
 struct ProductPlan {
-  int tile = 64;         // 64 or 128: linear_tile's square; 256: linear_big's; 16, 32: linear_few's rows of w
+  enum { kTile, kBig, kFew, kSplit } kind = kTile;
+  int tile_m = 64, tile_n = 64;
   bool pack_a = false, pack_b = false;  // operands laid out anew for linear_big
   uint32_t shares = 1;   // of k
   uint32_t blocks_per_share = 1;
@@ -217,7 +218,8 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     p.pack_b = !lies_well(b);
     if (within_reach(p.pack_a ? packed_stride(a.cols) : a.stride, a.cols, a_along) &&
         within_reach(p.pack_b ? packed_stride(b.cols) : b.stride, b.cols, b_along)) {
-      p.tile = 256;
+      p.kind = ProductPlan::kBig;
+      p.tile_m = p.tile_n = 256;
       if (p.pack_a) p.a_bytes = packed_bytes(a);
       if (p.pack_b) p.b_bytes = packed_bytes(b);
       return p;
@@ -226,8 +228,10 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
   }
   if (a_along && b_along && m <= 64 && k > 0) {
     const uint64_t whole = std::max<uint64_t>(1, k / block);
-    p.tile = ceil_div(n, 32) >= kCus ? 32 : 16;
-    const uint64_t groups = ceil_div(n, p.tile);
+    p.kind = ProductPlan::kFew;
+    p.tile_m = 64;
+    p.tile_n = ceil_div(n, 32) >= kCus ? 32 : 16;
+    const uint64_t groups = ceil_div(n, p.tile_n);
     // 8 waves of a workgroup split k already; shares only where the
     // workgroups leave compute units idle, and of 4 steps a wave at least
     const uint64_t shares = groups < kCus ? std::max<uint64_t>(1, std::min(kCus / groups, whole / 32)) : 1;
@@ -237,13 +241,19 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
     return p;
   }
-  const uint64_t large = ceil_div(m, 128) * ceil_div(n, 128);
-  p.tile = large >= kCus ? 128 : 64;
-  const uint64_t tiles = ceil_div(m, p.tile) * ceil_div(n, p.tile);
+  uint64_t steps = blocks;  // of 64 k
+  if (dtype == MSCL_FLOAT32) {
+    p.kind = ProductPlan::kSplit;
+    p.tile_m = ceil_div(m, 128) * ceil_div(n, 64) >= kCus / 2 ? 128 : 64;
+    steps = ceil_div(k, 64);
+  } else if (ceil_div(m, 128) * ceil_div(n, 128) >= kCus) {
+    p.tile_m = p.tile_n = 128;
+  }
+  const uint64_t tiles = ceil_div(m, p.tile_m) * ceil_div(n, p.tile_n);
   uint64_t shares = 1;
-  if (tiles < 2 * kCus && blocks >= 8) shares = std::min({ceil_div(2 * kCus, tiles), blocks / 4, uint64_t(32)});
-  p.blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(blocks, shares)));
-  p.shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(blocks, p.blocks_per_share)));
+  if (tiles < 2 * kCus && steps >= 8) shares = std::min({2 * kCus / tiles, steps / 4, uint64_t(32)});
+  p.blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, std::max<uint64_t>(1, shares))));
+  p.shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, p.blocks_per_share)));
   p.partial_stride = round_up(n, 8);
   if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
   return p;
@@ -258,15 +268,24 @@ mscl_status_t pack(Operand* o, char* to, hipStream_t stream) {
   return launched("linear_pack");
 }
 
-// linear_big's LDS is more than a kernel gets unasked.
-template <class C, bool kAAlong, bool kBAlong>
-hipError_t allow_lds() {
+// More dynamic LDS than a kernel gets unasked.
+template <auto kKernel>
+hipError_t allow_lds(int bytes) {
   static std::atomic<bool> done{false};
   if (done.load(std::memory_order_acquire)) return hipSuccess;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_big<C, kAAlong, kBAlong>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == hipSuccess) done.store(true, std::memory_order_release);
   return e;
+}
+
+template <bool kAAlong, bool kBAlong, int kBM, int kBN>
+mscl_status_t launch_split(const TileArgs& t, dim3 grid, hipStream_t stream) {
+  constexpr int kLds = SplitStage<kAAlong, kBM>::kBytes + SplitStage<kBAlong, kBN>::kBytes;
+  const hipError_t err = allow_lds<&linear_split<kAAlong, kBAlong, kBM, kBN>>(kLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  linear_split<kAAlong, kBAlong, kBM, kBN><<<grid, 256, kLds, stream>>>(t);
+  return launched("linear_split");
 }
 
 template <class C>
@@ -292,17 +311,16 @@ void launch_few(int tile, const TileArgs& t, dim3 grid, hipStream_t stream) {
 template <class C, bool kAAlong, bool kBAlong>
 mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, const Epilogue& e0, char* workspace,
                       hipStream_t stream) {
-  const bool few = p.tile <= 32;
-  const uint64_t tm = few ? 1 : ceil_div(e0.m, p.tile), tn = ceil_div(e0.n, p.tile);
+  const uint64_t tm = ceil_div(e0.m, p.tile_m), tn = ceil_div(e0.n, p.tile_n);
   if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
   const uint32_t groups = static_cast<uint32_t>(tm * tn);
   if constexpr (C::kElemBytes == 2) {
-    if (p.tile == 256) {
+    if (p.kind == ProductPlan::kBig) {
       mscl_status_t st = MSCL_SUCCESS;
       if (p.pack_a) st = pack<C>(&a, workspace, stream);
       if (st == MSCL_SUCCESS && p.pack_b) st = pack<C>(&b, workspace + p.a_bytes, stream);
       if (st != MSCL_SUCCESS) return st;
-      const hipError_t err = allow_lds<C, kAAlong, kBAlong>();
+      const hipError_t err = allow_lds<&linear_big<C, kAAlong, kBAlong>>(kBigLds);
       if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
       BigArgs t{a, b, e0, round_up(k, C::V), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
       linear_big<C, kAAlong, kBAlong><<<groups, 512, kBigLds, stream>>>(t);
@@ -320,13 +338,20 @@ mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, co
   t.tiles_n = static_cast<uint32_t>(tn);
   t.blocks_per_share = p.blocks_per_share;
   const dim3 grid(groups, p.shares);
-  if (few) {
-    if constexpr (kAAlong && kBAlong) launch_few<C>(p.tile, t, grid, stream);
-  } else if (p.tile == 128)
-    linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
-  else
-    linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
-  mscl_status_t st = launched("linear_tile");
+  mscl_status_t st = MSCL_SUCCESS;
+  if (p.kind == ProductPlan::kFew) {
+    if constexpr (kAAlong && kBAlong) launch_few<C>(p.tile_n, t, grid, stream);
+    st = launched("linear_few");
+  } else if constexpr (C::kElemBytes == 4) {
+    st = p.tile_m == 128 ? launch_split<kAAlong, kBAlong, 128, 64>(t, grid, stream)
+                         : launch_split<kAAlong, kBAlong, 64, 64>(t, grid, stream);
+  } else {
+    if (p.tile_m == 128)
+      linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
+    else
+      linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
+    st = launched("linear_tile");
+  }
   if (st != MSCL_SUCCESS || p.shares == 1) return st;
   const uint64_t joins = ceil_div(ceil_div(e0.n, C::V) * e0.m, 256);
   if (joins > kMostGroups) return bad("the matrices have too many tiles");

@@ -147,6 +147,48 @@ def test_large_product_keeps_nan_in_its_row_and_column():
     assert bool(torch.isfinite(y[:2099, :4099]).all())
 
 
+@pytest.mark.parametrize("m,k,n", [(70, 130, 90), (1001, 300, 1537), (513, 2047, 260)])
+def test_binary32_products_over_the_whole_range(m, k, n):
+    """Rows and columns of very different size, and sums that leave the range, next to infinities and NaN."""
+    gen = torch.Generator().manual_seed(20)
+    x, w, b, dy = linear_case(gen, m, k, n, torch.float32)
+    x = x * torch.exp2(torch.randint(-60, 60, (m, 1), generator=gen).float())
+    w = w * torch.exp2(torch.randint(-60, 60, (n, 1), generator=gen).float())
+    note("binary32 range", m, k, n)
+    c = [v.cuda() for v in (x, w, dy)]
+    O.assert_within(M.linear_tensors(c[0], c[1]), O.linear(c[0], c[1], None, None, "none")[0], "y")
+    for g, want, name in zip(M.linear_backward_tensors(c[2], c[0], c[1]), O.linear_backward(c[2], c[0], c[1], None, "none"),
+                             ("dx", "dw", "db")):
+        O.assert_within(g, want, name)
+    top = torch.finfo(torch.float32).max
+    x, w = x.sign(), w.sign()
+    x[3, :], w[5, :] = 0, 0
+    x[3, 0], x[3, 1], w[:, 0], w[:, 1] = top, top, 1, 1  # twice the largest value
+    w[5, 0] = 1
+    x[7, 2], w[:, 2] = math.inf, 1
+    w[9, 4], x[:, 4] = -math.inf, 1
+    x[11, 6] = math.nan
+    y = M.linear_tensors(x.cuda(), w.cuda()).cpu()
+    assert y[3, 5] == math.inf and y[3, 6] == math.inf and y[7, 5] == math.inf and y[5, 9] == -math.inf
+    assert bool(torch.isnan(y[11]).all()) and bool(torch.isnan(y[7, 9]))
+    rows = [i for i in range(m) if i not in (3, 7, 11)]
+    cols = [i for i in range(n) if i != 9]
+    assert bool((y[rows][:, 9] == -math.inf).all())
+    want = x[rows].double() @ w[cols].double().t()
+    assert torch.equal(y[rows][:, cols].double(), want)  # sums of signs are exact
+
+
+def test_binary32_products_of_the_largest_and_smallest_values():
+    top, low = torch.finfo(torch.float32).max, torch.finfo(torch.float32).smallest_normal
+    x, w = torch.zeros(80, 70), torch.zeros(100, 70)
+    x[3, 0], x[4, 1], x[5, 2] = top, -top, low
+    w[:, 0], w[:, 1], w[:, 2] = 1, 1, 1
+    note("largest and smallest values")
+    y = M.linear_tensors(x.cuda(), w.cuda()).cpu()
+    assert bool((y[3] == top).all()) and bool((y[4] == -top).all()) and bool((y[5] == low).all())
+    assert not bool(y[[i for i in range(80) if i not in (3, 4, 5)]].any())
+
+
 def test_linear_many_leading_dimensions():
     gen = torch.Generator().manual_seed(13)
     x, w, b, _ = linear_case(gen, 30, 24, 40, torch.bfloat16)
