@@ -319,6 +319,41 @@ struct Corner {
   uint64_t first, second;
 };
 
+// ------------------------------------------------------------------ column sums
+
+struct JoinArgs {
+  const float* sums;  // [groups][kinds][stride]
+  char* out[2];       // null: not wanted
+  uint64_t stride, width;
+  uint32_t groups, kinds;
+};
+
+// Adds the groups' column sums of one kind in a fixed order and rounds them:
+// 32 columns a workgroup, 8 threads a column.
+template <class P>
+__device__ inline void join_block(const JoinArgs& a, uint64_t block, uint32_t kind) {
+  __shared__ float part[8][33];
+  const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const uint64_t col = block * 32 + c;
+  float s = 0.0f;
+  if (col < a.width)
+#pragma unroll 4
+    for (uint32_t g = q; g < a.groups; g += 8) s += a.sums[(static_cast<uint64_t>(g) * a.kinds + kind) * a.stride + col];
+  part[q][c] = s;
+  __syncthreads();
+  if (q == 0 && col < a.width && a.out[kind]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += part[i][c];
+    reinterpret_cast<typename P::Bits*>(a.out[kind])[col] = P::narrow(t);
+  }
+}
+
+template <class P>
+__global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
+  join_block<P>(a, blockIdx.x, blockIdx.y);
+}
+
 // ------------------------------------------------------------------ general tile kernel
 
 struct Operand {
@@ -336,16 +371,17 @@ struct TileArgs {
   uint32_t blocks_per_share;  // blocks of k that one share (blockIdx.y) sums
 };
 
-// One operand's kT x (128-byte block of k) tile, from memory through
+// One operand's kT x (64 k) tile of a 16-bit type, from memory through
 // registers into LDS.  kAlong: kT rows of 128 bytes, 16-byte chunk c of row r
 // at chunk c ^ (r % 8), so that eight neighbouring rows' equal chunks lie in
-// different banks.  kDown: one row of kT elements for each k; 32-byte (16-bit
-// types, read transposed) or 64-byte (binary32) segments are xored with bits
-// of k so that the rows that one instruction reads lie in different banks.
+// different banks.  kDown: one row of kT elements for each k, read
+// transposed; 32-byte segments are xored with bits of k so that the rows that
+// one instruction reads lie in different banks.
 template <class C, bool kAlong, int kT, int kThreads>
 struct Stage {
   static constexpr int V = C::V;
-  static constexpr int kBlock = 8 * V;  // k per block
+  static_assert(V == 8, "binary32 operands are split first");
+  static constexpr int kBlock = 64;  // k
   static constexpr int kChunks = kT * 8 / kThreads;  // 16-byte chunks per thread
   static constexpr int kBytes = kT * 128;
   static constexpr int kPerRow = kAlong ? 8 : kT / V;  // chunks per LDS row
@@ -353,12 +389,10 @@ struct Stage {
 
   static __device__ inline int swizzle(int row, int chunk) {
     if constexpr (kAlong) return chunk ^ (row & 7);
-    if constexpr (V == 8) {  // segments of 2 chunks; rows k .. k + 3 and k + 8 .. k + 11 are read at once
-      constexpr int kSegs = kT / 16;
-      const int key = kSegs >= 8 ? ((row & 3) | ((row >> 3 & 1) << 2)) : ((row >> 1 & 1) | ((row >> 3 & 1) << 1));
-      return chunk ^ ((key & (kSegs - 1)) << 1);
-    }
-    return chunk ^ ((row >> 2 & 3) << 2);  // binary32: rows 4 apart are read at once
+    // segments of 2 chunks; rows k .. k + 3 and k + 8 .. k + 11 are read at once
+    constexpr int kSegs = kT / 16;
+    const int key = kSegs >= 8 ? ((row & 3) | ((row >> 3 & 1) << 2)) : ((row >> 1 & 1) | ((row >> 3 & 1) << 1));
+    return chunk ^ ((key & (kSegs - 1)) << 1);
   }
 
   __device__ inline void load(const Operand& o, uint64_t first, uint64_t k0, uint64_t k_end) {
@@ -392,7 +426,7 @@ struct Stage {
     const int r = lane & 15, g = lane >> 4;
     if constexpr (kAlong) {
       return *reinterpret_cast<const u32x4*>(lds + ((p + r) * 8 + swizzle(p + r, 4 * s + g)) * 16);
-    } else if constexpr (V == 8) {
+    } else {
       // lane l gives the address of row k + (l % 16) / 4, columns 4 (l % 4) .. + 3
       // of its quarter's 4 x 16 square and receives column l % 16
       u32x4 out;
@@ -405,15 +439,6 @@ struct Stage {
         const u32x2 w = __builtin_bit_cast(u32x2, q);
         out[2 * h] = w[0];
         out[2 * h + 1] = w[1];
-      }
-      return out;
-    } else {
-      u32x4 out;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 16 * s + 4 * g + j;
-        const int col = p + r;
-        out[j] = *reinterpret_cast<const uint32_t*>(lds + (k * kPerRow + swizzle(k, col >> 2)) * 16 + (col & 3) * 4);
       }
       return out;
     }
@@ -437,20 +462,20 @@ __device__ inline f32x4 multiply(const u32x4& b, const u32x4& a, f32x4 acc) {
   }
 }
 
-// Any sizes, strides and alignments: kBM x kBN tiles by 4 waves in a square,
-// 128 bytes of k at a time, the next block's loads in flight while the
-// present one is multiplied, two LDS buffers.  blockIdx.y is the share of k.
-template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
-__global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
+// Any sizes, strides and alignments of a 16-bit type: kBM x kBN tiles by 4
+// waves in a square, 64 k at a time, two LDS buffers.  The next kDeep blocks'
+// loads are in flight in registers.
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep>
+__device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
   using SA = Stage<C, kAAlong, kBM, 256>;
   using SB = Stage<C, kBAlong, kBN, 256>;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
-  __shared__ __align__(16) char lds[2 * (SA::kBytes + SB::kBytes)];
-  const uint32_t tm = blockIdx.x % t.tiles_m, tn = blockIdx.x / t.tiles_m;
+  static_assert(kDeep % 2 == 0, "the LDS buffers alternate");
+  const uint32_t tm = tile % t.tiles_m, tn = tile / t.tiles_m;
   const uint64_t m0 = static_cast<uint64_t>(tm) * kBM, n0 = static_cast<uint64_t>(tn) * kBN;
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
-  const uint64_t k_first = static_cast<uint64_t>(blockIdx.y) * t.blocks_per_share * SA::kBlock;
+  const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * SA::kBlock;
   uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * SA::kBlock;
   if (k_end > t.k) k_end = t.k;
 
@@ -460,42 +485,43 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
 #pragma unroll
     for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  SA sa;
-  SB sb;
-  int buf = 0;
-  if (k_first < k_end) {
-    sa.load(t.a, m0, k_first, k_end);
-    sb.load(t.b, n0, k_first, k_end);
-    sa.store(lds);
-    sb.store(lds + SA::kBytes);
+  SA sa[kDeep];
+  SB sb[kDeep];
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    const uint64_t k = k_first + d * SA::kBlock;
+    if (k < k_end) {
+      sa[d].load(t.a, m0, k, k_end);
+      sb[d].load(t.b, n0, k, k_end);
+    }
   }
-  __syncthreads();
-  for (uint64_t k0 = k_first; k0 < k_end; k0 += SA::kBlock) {
-    const bool more = k0 + SA::kBlock < k_end;
-    if (more) {
-      sa.load(t.a, m0, k0 + SA::kBlock, k_end);
-      sb.load(t.b, n0, k0 + SA::kBlock, k_end);
+  for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * SA::kBlock) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const uint64_t k = k0 + d * SA::kBlock;
+      if (k >= k_end) break;
+      char* la = lds + (d & 1) * (SA::kBytes + SB::kBytes);
+      char* lb = la + SA::kBytes;
+      sa[d].store(la);
+      sb[d].store(lb);
+      __syncthreads();
+      if (k + kDeep * SA::kBlock < k_end) {
+        sa[d].load(t.a, m0, k + kDeep * SA::kBlock, k_end);
+        sb[d].load(t.b, n0, k + kDeep * SA::kBlock, k_end);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        u32x4 fa[kWM], fb[kWN];
+#pragma unroll
+        for (int i = 0; i < kWM; ++i) fa[i] = SA::fragment(la, wm + 16 * i, s);
+#pragma unroll
+        for (int j = 0; j < kWN; ++j) fb[j] = SB::fragment(lb, wn + 16 * j, s);
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+#pragma unroll
+          for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
+      }
     }
-    const char* la = lds + buf * (SA::kBytes + SB::kBytes);
-    const char* lb = la + SA::kBytes;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 fa[kWM], fb[kWN];
-#pragma unroll
-      for (int i = 0; i < kWM; ++i) fa[i] = SA::fragment(la, wm + 16 * i, s);
-#pragma unroll
-      for (int j = 0; j < kWN; ++j) fb[j] = SB::fragment(lb, wn + 16 * j, s);
-#pragma unroll
-      for (int i = 0; i < kWM; ++i)
-#pragma unroll
-        for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
-    }
-    if (more) {
-      buf ^= 1;
-      sa.store(lds + buf * (SA::kBytes + SB::kBytes));
-      sb.store(lds + buf * (SA::kBytes + SB::kBytes) + SA::kBytes);
-    }
-    __syncthreads();
   }
   if (t.e.partial) {
     using G = Groups<C, kWM, kWN>;
@@ -503,7 +529,7 @@ __global__ __launch_bounds__(256) void linear_tile(const TileArgs t) {
     for (int q = 0; q < G::kCount; ++q) {
       float v[C::V];
       G::sums(acc[0], q, v);
-      keep_partial<C>(t.e, blockIdx.y, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
+      keep_partial<C>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
     }
   } else {
     finish_all<C>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
@@ -807,18 +833,18 @@ __device__ inline float value_at(const Operand& o, uint64_t i, uint64_t k, uint6
 
 // kBM x kBN tiles by 4 waves in a square, 64 k at a time.  One LDS buffer, as
 // three planes of it let two workgroups share a compute unit: one splits and
-// stores while the other multiplies.
-template <bool kAAlong, bool kBAlong, int kBM, int kBN>
-__global__ __launch_bounds__(256, 2) void linear_split(const TileArgs t) {
+// stores while the other multiplies.  kDeep blocks' loads are in flight, as in
+// linear_tile.
+template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep>
+__device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
   using SA = SplitStage<kAAlong, kBM>;
   using SB = SplitStage<kBAlong, kBN>;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
-  extern __shared__ __align__(16) char lds[];
-  const uint32_t tm = blockIdx.x % t.tiles_m, tn = blockIdx.x / t.tiles_m;
+  const uint32_t tm = tile % t.tiles_m, tn = tile / t.tiles_m;
   const uint64_t m0 = static_cast<uint64_t>(tm) * kBM, n0 = static_cast<uint64_t>(tn) * kBN;
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
-  const uint64_t k_first = static_cast<uint64_t>(blockIdx.y) * t.blocks_per_share * 64;
+  const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * 64;
   uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * 64;
   if (k_end > t.k) k_end = t.k;
 
@@ -828,42 +854,51 @@ __global__ __launch_bounds__(256, 2) void linear_split(const TileArgs t) {
 #pragma unroll
     for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  SA sa;
-  SB sb;
-  if (k_first < k_end) {
-    sa.load(t.a, m0, k_first, k_end);
-    sb.load(t.b, n0, k_first, k_end);
+  SA sa[kDeep];
+  SB sb[kDeep];
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    const uint64_t k = k_first + d * 64;
+    if (k < k_end) {
+      sa[d].load(t.a, m0, k, k_end);
+      sb[d].load(t.b, n0, k, k_end);
+    }
   }
-  for (uint64_t k0 = k_first; k0 < k_end; k0 += 64) {
-    sa.store(lds);
-    sb.store(lds + SA::kBytes);
-    __syncthreads();
-    if (k0 + 64 < k_end) {
-      sa.load(t.a, m0, k0 + 64, k_end);
-      sb.load(t.b, n0, k0 + 64, k_end);
-    }
+  for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * 64) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 fb[3][kWN];
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
-#pragma unroll
-      for (int i = 0; i < kWM; ++i) {
-        u32x4 fa[3];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
-        // the smaller products first
-#pragma unroll
-        for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-          for (int p = 0; p <= sum; ++p)
-#pragma unroll
-            for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+    for (int d = 0; d < kDeep; ++d) {
+      const uint64_t k = k0 + d * 64;
+      if (k >= k_end) break;
+      sa[d].store(lds);
+      sb[d].store(lds + SA::kBytes);
+      __syncthreads();
+      if (k + kDeep * 64 < k_end) {
+        sa[d].load(t.a, m0, k + kDeep * 64, k_end);
+        sb[d].load(t.b, n0, k + kDeep * 64, k_end);
       }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        u32x4 fb[3][kWN];
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
+#pragma unroll
+        for (int i = 0; i < kWM; ++i) {
+          u32x4 fa[3];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
+          // the smaller products first
+#pragma unroll
+          for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+            for (int p = 0; p <= sum; ++p)
+#pragma unroll
+              for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 
   bool odd = false;
@@ -898,11 +933,95 @@ __global__ __launch_bounds__(256, 2) void linear_split(const TileArgs t) {
     for (int q = 0; q < G::kCount; ++q) {
       float v[4];
       G::sums(acc[0], q, v);
-      keep_partial<F32>(t.e, blockIdx.y, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
+      keep_partial<F32>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
     }
   } else {
     finish_all<F32>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
   }
+}
+
+// ------------------------------------------------------------------ launches of tiles
+
+// LDS of one tile's workgroup.
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
+constexpr int tile_lds() {
+  if constexpr (C::kElemBytes == 4)
+    return SplitStage<kAAlong, kBM>::kBytes + SplitStage<kBAlong, kBN>::kBytes;
+  else
+    return 2 * (Stage<C, kAAlong, kBM, 256>::kBytes + Stage<C, kBAlong, kBN, 256>::kBytes);
+}
+
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
+__device__ inline void any_tile(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
+  if constexpr (C::kElemBytes == 4)
+    split_body<kAAlong, kBAlong, kBM, kBN, 1>(t, tile, share, lds);
+  else
+    tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 128 ? 2 : 4>(t, tile, share, lds);
+}
+
+// One product; blockIdx.y is the share of k.
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
+__global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs t) {
+  extern __shared__ __align__(16) char lds[];
+  any_tile<C, kAAlong, kBAlong, kBM, kBN>(t, blockIdx.x, blockIdx.y, lds);
+}
+
+// Both gradients' products and the bias gradient's last sums in one launch:
+// small products leave the device half empty, and each launch costs about 2 us
+// on the host.
+struct PairArgs {
+  TileArgs dx, dw;
+  JoinArgs db;
+  uint32_t dx_tiles, dw_tiles, dx_groups, dw_groups;  // groups: tiles x shares
+};
+
+template <class C, int kBM, int kBN>
+__global__ __launch_bounds__(256, 2) void linear_pair(const PairArgs p) {
+  extern __shared__ __align__(16) char lds[];
+  uint32_t id = blockIdx.x;
+  if (id < p.dx_groups) {
+    any_tile<C, true, false, kBM, kBN>(p.dx, id % p.dx_tiles, id / p.dx_tiles, lds);
+    return;
+  }
+  id -= p.dx_groups;
+  if (id < p.dw_groups) {
+    any_tile<C, false, false, kBM, kBN>(p.dw, id % p.dw_tiles, id / p.dw_tiles, lds);
+    return;
+  }
+  join_block<C>(p.db, id - p.dw_groups, 0);
+}
+
+// Adds the shares of k in their order and finishes the sums of one group of V.
+template <class C>
+__device__ inline void join_shares(const Epilogue& e, int shares, uint64_t id) {
+  constexpr int V = C::V;
+  const uint64_t per_row = (e.n + V - 1) / V;
+  if (id >= per_row * e.m) return;
+  const uint64_t m = id / per_row, n = id % per_row * V;
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.0f;
+  for (int s = 0; s < shares; ++s) {
+    const float* p = e.partial + (static_cast<uint64_t>(s) * e.m + m) * e.partial_stride + n;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f32x4 q = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[i + c] += q[c];
+    }
+  }
+  const u32x4 bias = fetch_bias<C>(e, n), residual = fetch_residual<C>(e, m, n);
+  with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v, bias, residual); });
+}
+
+// Up to two products' shares: the first `groups` workgroups join a's.
+template <class C>
+__global__ __launch_bounds__(256) void linear_join(const Epilogue a, int a_shares, const Epilogue b, int b_shares,
+                                                   uint32_t groups) {
+  if (blockIdx.x < groups)
+    join_shares<C>(a, a_shares, static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x);
+  else
+    join_shares<C>(b, b_shares, static_cast<uint64_t>(blockIdx.x - groups) * 256 + threadIdx.x);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -1033,30 +1152,6 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
                                         fetch_residual<C>(t.e, m, n0 + n));
     }
   });
-}
-
-// Adds the shares of k in their order and finishes the sums.
-template <class C>
-__global__ __launch_bounds__(256) void linear_join(const Epilogue e, int shares) {
-  constexpr int V = C::V;
-  const uint64_t per_row = (e.n + V - 1) / V;
-  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= per_row * e.m) return;
-  const uint64_t m = id / per_row, n = id % per_row * V;
-  float v[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.0f;
-  for (int s = 0; s < shares; ++s) {
-    const float* p = e.partial + (static_cast<uint64_t>(s) * e.m + m) * e.partial_stride + n;
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const f32x4 q = *reinterpret_cast<const f32x4*>(p + i);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[i + c] += q[c];
-    }
-  }
-  const u32x4 bias = fetch_bias<C>(e, n), residual = fetch_residual<C>(e, m, n);
-  with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v, bias, residual); });
 }
 
 // ------------------------------------------------------------------ operands laid out anew

@@ -549,41 +549,6 @@ __global__ __launch_bounds__(512) void norm_back_fused(const NormBackArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ column sums
-
-struct JoinArgs {
-  const float* sums;  // [groups][kinds][stride]
-  char* out[2];       // null: not wanted
-  uint64_t stride, width;
-  uint32_t groups, kinds;
-};
-
-// Adds the groups' column sums of one kind in a fixed order and rounds them:
-// 32 columns a workgroup, 8 threads a column.
-template <class P>
-__device__ inline void join_block(const JoinArgs& a, uint64_t block, uint32_t kind) {
-  __shared__ float part[8][33];
-  const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-  const uint64_t col = block * 32 + c;
-  float s = 0.0f;
-  if (col < a.width)
-#pragma unroll 4
-    for (uint32_t g = q; g < a.groups; g += 8) s += a.sums[(static_cast<uint64_t>(g) * a.kinds + kind) * a.stride + col];
-  part[q][c] = s;
-  __syncthreads();
-  if (q == 0 && col < a.width && a.out[kind]) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += part[i][c];
-    reinterpret_cast<typename P::Bits*>(a.out[kind])[col] = P::narrow(t);
-  }
-}
-
-template <class P>
-__global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
-  join_block<P>(a, blockIdx.x, blockIdx.y);
-}
-
 // The second launch for few rows: the first `tiles` workgroups turn
 // norm_back_tiles' row sums into dx, tile by tile (x and dy come from the
 // caches by then), the others join its column sums.

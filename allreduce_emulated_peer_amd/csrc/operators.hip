@@ -179,13 +179,37 @@ mscl_status_t with_codecs(int dtype, int param_dtype, Fn&& fn) {
   return param_dtype == MSCL_FLOAT32 ? fn(BF16{}, F32{}) : fn(BF16{}, BF16{});
 }
 
+// ------------------------------------------------------------------ column sums
+
+JoinArgs join_args(const float* sums, uint64_t stride, uint64_t width, uint32_t groups, void* first, void* second,
+                   uint32_t kinds) {
+  JoinArgs j;
+  j.sums = sums;
+  j.out[0] = bytes_at(first);
+  j.out[1] = bytes_at(second);
+  j.stride = stride;
+  j.width = width;
+  j.groups = groups;
+  j.kinds = kinds;
+  return j;
+}
+
+mscl_status_t join_columns(int param_dtype, const JoinArgs& j, uint32_t kinds, hipStream_t stream) {
+  const uint64_t blocks = ceil_div(j.width, 32);
+  if (blocks > kMostGroups) return bad("the rows are too wide");
+  return with_codec(param_dtype, [&](auto p) {
+    column_join<decltype(p)><<<dim3(static_cast<uint32_t>(blocks), kinds), 256, 0, stream>>>(j);
+    return launched("column_join");
+  });
+}
+
 // ------------------------------------------------------------------ matrix products
 
 constexpr int kCus = 256;  // of an MI355X: the plans must not depend on a device, as workspaces are sized without one
 
 // How one product m x n x k runs.
 struct ProductPlan {
-  enum { kTile, kBig, kFew, kSplit } kind = kTile;
+  enum { kTile, kBig, kFew } kind = kTile;
   int tile_m = 64, tile_n = 64;
   bool pack_a = false, pack_b = false;  // operands laid out anew for linear_big
   uint32_t shares = 1;   // of k
@@ -207,6 +231,29 @@ bool within_reach(uint64_t stride, uint64_t cols, bool along) {
 
 uint64_t packed_stride(uint64_t cols) { return round_up(cols, 64); }
 size_t packed_bytes(const Operand& o) { return round_up(o.rows * packed_stride(o.cols) * 2, 256); }
+
+// linear_tile's tile for a launch of `large` tiles of 128 x 128.
+void choose_tile(ProductPlan* p, uint64_t large, int dtype) {
+  if (dtype == MSCL_FLOAT32) {
+    p->tile_m = 2 * large >= kCus / 2 ? 128 : 64;  // by 64
+  } else if (large >= kCus) {
+    p->tile_m = p->tile_n = 128;
+  }
+}
+
+// Shares of k for a product of m x n in a launch of `tiles` tiles: as many as
+// the device holds at once (two workgroups a compute unit), of 4 blocks of 64
+// k at least.  512 x 512 fp32 with k = 2048: 1 share 53 us, 2 30, 4 20, 8 18;
+// 300 x 700 with k = 1024: 1 share 29 us, 4 14, 8 15.
+void choose_shares(ProductPlan* p, uint64_t m, uint64_t n, uint64_t k, uint64_t tiles) {
+  const uint64_t steps = ceil_div(k, 64);
+  uint64_t shares = 1;
+  if (tiles < 2 * kCus && steps >= 8) shares = std::min({2 * kCus / tiles, steps / 4, uint64_t(32)});
+  p->blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, std::max<uint64_t>(1, shares))));
+  p->shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, p->blocks_per_share)));
+  p->partial_stride = round_up(n, 8);
+  if (p->shares > 1) p->partial_bytes = round_up(p->shares * m * p->partial_stride * 4, 256);
+}
 
 ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool b_along, uint64_t m, uint64_t n,
                          uint64_t k, int dtype) {
@@ -241,21 +288,8 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
     return p;
   }
-  uint64_t steps = blocks;  // of 64 k
-  if (dtype == MSCL_FLOAT32) {
-    p.kind = ProductPlan::kSplit;
-    p.tile_m = ceil_div(m, 128) * ceil_div(n, 64) >= kCus / 2 ? 128 : 64;
-    steps = ceil_div(k, 64);
-  } else if (ceil_div(m, 128) * ceil_div(n, 128) >= kCus) {
-    p.tile_m = p.tile_n = 128;
-  }
-  const uint64_t tiles = ceil_div(m, p.tile_m) * ceil_div(n, p.tile_n);
-  uint64_t shares = 1;
-  if (tiles < 2 * kCus && steps >= 8) shares = std::min({2 * kCus / tiles, steps / 4, uint64_t(32)});
-  p.blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, std::max<uint64_t>(1, shares))));
-  p.shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, p.blocks_per_share)));
-  p.partial_stride = round_up(n, 8);
-  if (p.shares > 1) p.partial_bytes = p.shares * m * p.partial_stride * 4;
+  choose_tile(&p, ceil_div(m, 128) * ceil_div(n, 128), dtype);
+  choose_shares(&p, m, n, k, ceil_div(m, p.tile_m) * ceil_div(n, p.tile_n));
   return p;
 }
 
@@ -279,13 +313,40 @@ hipError_t allow_lds(int bytes) {
   return e;
 }
 
-template <bool kAAlong, bool kBAlong, int kBM, int kBN>
-mscl_status_t launch_split(const TileArgs& t, dim3 grid, hipStream_t stream) {
-  constexpr int kLds = SplitStage<kAAlong, kBM>::kBytes + SplitStage<kBAlong, kBN>::kBytes;
-  const hipError_t err = allow_lds<&linear_split<kAAlong, kBAlong, kBM, kBN>>(kLds);
+TileArgs tile_args(const ProductPlan& p, const Operand& a, const Operand& b, uint64_t k, const Epilogue& e,
+                   char* workspace) {
+  TileArgs t;
+  t.a = a;
+  t.b = b;
+  t.e = e;
+  t.k = k;
+  t.e.partial = p.shares > 1 ? reinterpret_cast<float*>(workspace) : nullptr;
+  t.e.partial_stride = p.partial_stride;
+  t.tiles_m = static_cast<uint32_t>(ceil_div(e.m, p.tile_m));
+  t.tiles_n = static_cast<uint32_t>(ceil_div(e.n, p.tile_n));
+  t.blocks_per_share = p.blocks_per_share;
+  return t;
+}
+
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
+mscl_status_t launch_tile(const TileArgs& t, uint32_t shares, hipStream_t stream) {
+  constexpr int kLds = tile_lds<C, kAAlong, kBAlong, kBM, kBN>();
+  const hipError_t err = allow_lds<&linear_tile<C, kAAlong, kBAlong, kBM, kBN>>(kLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
-  linear_split<kAAlong, kBAlong, kBM, kBN><<<grid, 256, kLds, stream>>>(t);
-  return launched("linear_split");
+  linear_tile<C, kAAlong, kBAlong, kBM, kBN><<<dim3(t.tiles_m * t.tiles_n, shares), 256, kLds, stream>>>(t);
+  return launched("linear_tile");
+}
+
+// The joins of up to two products; a product of one share has none.
+template <class C>
+mscl_status_t launch_join(const Epilogue& a, uint32_t a_shares, const Epilogue& b, uint32_t b_shares, hipStream_t stream) {
+  const uint64_t first = a_shares > 1 ? ceil_div(ceil_div(a.n, C::V) * a.m, 256) : 0;
+  const uint64_t second = b_shares > 1 ? ceil_div(ceil_div(b.n, C::V) * b.m, 256) : 0;
+  if (first + second == 0) return MSCL_SUCCESS;
+  if (first + second > kMostGroups) return bad("the matrices have too many tiles");
+  linear_join<C><<<static_cast<uint32_t>(first + second), 256, 0, stream>>>(
+      a, static_cast<int>(a_shares), b, static_cast<int>(b_shares), static_cast<uint32_t>(first));
+  return launched("linear_join");
 }
 
 template <class C>
@@ -327,36 +388,44 @@ mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, co
       return launched("linear_big");
     }
   }
-  TileArgs t;
-  t.a = a;
-  t.b = b;
-  t.e = e0;
-  t.k = k;
-  t.e.partial = p.shares > 1 ? reinterpret_cast<float*>(workspace) : nullptr;
-  t.e.partial_stride = p.partial_stride;
-  t.tiles_m = static_cast<uint32_t>(tm);
-  t.tiles_n = static_cast<uint32_t>(tn);
-  t.blocks_per_share = p.blocks_per_share;
-  const dim3 grid(groups, p.shares);
+  const TileArgs t = tile_args(p, a, b, k, e0, workspace);
   mscl_status_t st = MSCL_SUCCESS;
   if (p.kind == ProductPlan::kFew) {
-    if constexpr (kAAlong && kBAlong) launch_few<C>(p.tile_n, t, grid, stream);
+    if constexpr (kAAlong && kBAlong) launch_few<C>(p.tile_n, t, dim3(groups, p.shares), stream);
     st = launched("linear_few");
-  } else if constexpr (C::kElemBytes == 4) {
-    st = p.tile_m == 128 ? launch_split<kAAlong, kBAlong, 128, 64>(t, grid, stream)
-                         : launch_split<kAAlong, kBAlong, 64, 64>(t, grid, stream);
+  } else if (p.tile_m == 128) {
+    st = launch_tile<C, kAAlong, kBAlong, 128, C::kElemBytes == 4 ? 64 : 128>(t, p.shares, stream);
   } else {
-    if (p.tile_m == 128)
-      linear_tile<C, kAAlong, kBAlong, 128, 128><<<grid, 256, 0, stream>>>(t);
-    else
-      linear_tile<C, kAAlong, kBAlong, 64, 64><<<grid, 256, 0, stream>>>(t);
-    st = launched("linear_tile");
+    st = launch_tile<C, kAAlong, kBAlong, 64, 64>(t, p.shares, stream);
   }
-  if (st != MSCL_SUCCESS || p.shares == 1) return st;
-  const uint64_t joins = ceil_div(ceil_div(e0.n, C::V) * e0.m, 256);
-  if (joins > kMostGroups) return bad("the matrices have too many tiles");
-  linear_join<C><<<static_cast<uint32_t>(joins), 256, 0, stream>>>(t.e, static_cast<int>(p.shares));
-  return launched("linear_join");
+  if (st != MSCL_SUCCESS) return st;
+  return launch_join<C>(t.e, p.shares, t.e, 1, stream);
+}
+
+// dx and dw in one launch, and db's last sums with them (groups 0: no db).
+template <class C, int kBM, int kBN>
+mscl_status_t launch_pair(const PairArgs& a, uint32_t db_groups, hipStream_t stream) {
+  constexpr int kLds = std::max(tile_lds<C, true, false, kBM, kBN>(), tile_lds<C, false, false, kBM, kBN>());
+  const hipError_t err = allow_lds<&linear_pair<C, kBM, kBN>>(kLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  linear_pair<C, kBM, kBN><<<a.dx_groups + a.dw_groups + db_groups, 256, kLds, stream>>>(a);
+  return launched("linear_pair");
+}
+
+template <class C>
+mscl_status_t pair(const ProductPlan& dx, bool want_dx, const ProductPlan& dw, bool want_dw, PairArgs& a,
+                   uint32_t db_groups, hipStream_t stream) {
+  const uint64_t dx_tiles = uint64_t(a.dx.tiles_m) * a.dx.tiles_n, dw_tiles = uint64_t(a.dw.tiles_m) * a.dw.tiles_n;
+  if (dx_tiles * dx.shares + dw_tiles * dw.shares > kMostGroups / 2) return bad("the matrices have too many tiles");
+  a.dx_tiles = static_cast<uint32_t>(dx_tiles);
+  a.dw_tiles = static_cast<uint32_t>(dw_tiles);
+  a.dx_groups = want_dx ? a.dx_tiles * dx.shares : 0;
+  a.dw_groups = want_dw ? a.dw_tiles * dw.shares : 0;
+  if (a.dx_groups + a.dw_groups + db_groups == 0) return MSCL_SUCCESS;
+  const mscl_status_t st = dx.tile_m == 128 ? launch_pair<C, 128, C::kElemBytes == 4 ? 64 : 128>(a, db_groups, stream)
+                                            : launch_pair<C, 64, 64>(a, db_groups, stream);
+  if (st != MSCL_SUCCESS) return st;
+  return launch_join<C>(a.dx.e, want_dx ? dx.shares : 1, a.dw.e, want_dw ? dw.shares : 1, stream);
 }
 
 mscl_status_t check_linear(const mscl_linear_t* c, Spans& s) {
@@ -384,6 +453,7 @@ ProductPlan plan_linear(const mscl_linear_t& c) {
 struct BackwardPlan {
   ProductPlan dx, dw;
   bool slope = false;  // dz is computed into the workspace
+  bool pair = false;   // dx and dw in one launch
   Operand dz, x, w;    // dz without its address where it is computed
   uint32_t groups = 0, rows_per_group = 0;  // of the bias gradient's partial sums
   size_t dz_at = 0, sums_at = 0, partial_at = 0, bytes = 0;
@@ -420,13 +490,28 @@ BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
   }
   p.partial_at = at;
   size_t partial = 0;
-  if (c.dx) {
+  // The plans go by sizes and layouts, not by which gradients are wanted: a
+  // gradient has the same bits alone.
+  if (!c.dx) p.w = Operand{nullptr, c.in_features, c.out_features, c.in_features};
+  if (!c.dw) p.x = Operand{nullptr, c.in_features, c.rows, c.in_features};
+  if (c.rows && c.out_features && c.in_features) {
     p.dx = plan_product(p.dz, true, p.w, false, c.rows, c.in_features, c.out_features, c.dtype);
-    partial = std::max(partial, p.dx.bytes());
-  }
-  if (c.dw) {
     p.dw = plan_product(p.dz, false, p.x, false, c.out_features, c.in_features, c.rows, c.dtype);
-    partial = std::max(partial, p.dw.bytes());
+    p.pair = p.dx.kind == ProductPlan::kTile && p.dw.kind == ProductPlan::kTile;
+  }
+  if (p.pair) {
+    const uint64_t k = ceil_div(c.in_features, 128);
+    p.dx = p.dw = ProductPlan();
+    choose_tile(&p.dx, (ceil_div(c.rows, 128) + ceil_div(c.out_features, 128)) * k, c.dtype);
+    choose_tile(&p.dw, (ceil_div(c.rows, 128) + ceil_div(c.out_features, 128)) * k, c.dtype);
+    const uint64_t tiles = (ceil_div(c.rows, p.dx.tile_m) + ceil_div(c.out_features, p.dw.tile_m)) *
+                           ceil_div(c.in_features, p.dx.tile_n);
+    choose_shares(&p.dx, c.rows, c.in_features, c.out_features, tiles);
+    choose_shares(&p.dw, c.out_features, c.in_features, c.rows, tiles);
+    partial = (c.dx ? p.dx.partial_bytes : 0) + (c.dw ? p.dw.partial_bytes : 0);
+  } else {
+    if (c.dx) partial = std::max(partial, p.dx.bytes());
+    if (c.dw) partial = std::max(partial, p.dw.bytes());
   }
   p.bytes = at + partial;
   return p;
@@ -583,30 +668,6 @@ void launch_norm_back(const NormBackArgs& a, hipStream_t s) {
     norm_back_rows_wide<C, P><<<rows, 1024, 0, s>>>(a);
 }
 
-JoinArgs join_args(const float* sums, uint64_t stride, uint64_t width, uint32_t groups, void* first, void* second,
-                   uint32_t kinds) {
-  JoinArgs j;
-  j.sums = sums;
-  j.out[0] = bytes_at(first);
-  j.out[1] = bytes_at(second);
-  j.stride = stride;
-  j.width = width;
-  j.groups = groups;
-  j.kinds = kinds;
-  return j;
-}
-
-mscl_status_t join_columns(int param_dtype, const float* sums, uint64_t stride, uint64_t width, uint32_t groups,
-                           void* first, void* second, uint32_t kinds, hipStream_t stream) {
-  const JoinArgs j = join_args(sums, stride, width, groups, first, second, kinds);
-  const uint64_t blocks = ceil_div(width, 32);
-  if (blocks > kMostGroups) return bad("the rows are too wide");
-  return with_codec(param_dtype, [&](auto p) {
-    column_join<decltype(p)><<<dim3(static_cast<uint32_t>(blocks), kinds), 256, 0, stream>>>(j);
-    return launched("column_join");
-  });
-}
-
 }  // namespace
 
 extern "C" {
@@ -675,6 +736,8 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
   char* ws = bytes_at(workspace);
   Operand dz = p.dz;
   if (p.slope) dz.base = ws + p.dz_at;
+  JoinArgs db_join;
+  memset(&db_join, 0, sizeof db_join);
   if (db || (p.slope && (dx || dw))) {
     SlopeArgs a;
     memset(&a, 0, sizeof a);
@@ -706,31 +769,41 @@ mscl_status_t mscl_linear_backward(const mscl_linear_backward_t* call, void* wor
       });
       if (st != MSCL_SUCCESS) return st;
     }
-    if (db) {
-      st = join_columns(c.dtype, a.sums, a.sums_stride, c.out_features, groups, c.dbias, nullptr, 1, s);
-      if (st != MSCL_SUCCESS) return st;
-    }
+    db_join = join_args(a.sums, c.out_features, c.out_features, groups, c.dbias, nullptr, 1);
   }
-  Epilogue e;
+  Epilogue ex, ew;
+  memset(&ex, 0, sizeof ex);
+  ex.y = bytes_at(c.dx);
+  ex.y_stride = c.dx_stride;
+  ex.m = c.rows;
+  ex.n = c.in_features;
+  memset(&ew, 0, sizeof ew);
+  ew.y = bytes_at(c.dw);
+  ew.y_stride = c.dw_stride;
+  ew.m = c.out_features;
+  ew.n = c.in_features;
+  char* partial = ws + p.partial_at;
+  if (p.pair) {
+    return with_codec(c.dtype, [&](auto t) {
+      PairArgs a;
+      a.dx = tile_args(p.dx, dz, p.w, c.out_features, ex, partial);
+      a.dw = tile_args(p.dw, dz, p.x, c.rows, ew, partial + (dx ? p.dx.partial_bytes : 0));
+      a.db = db_join;
+      const uint64_t db_groups = db ? ceil_div(c.out_features, 32) : 0;
+      if (db_groups > kMostGroups / 2) return bad("the matrices have too many tiles");
+      return pair<decltype(t)>(p.dx, dx, p.dw, dw, a, static_cast<uint32_t>(db_groups), s);
+    });
+  }
+  if (db && (st = join_columns(c.dtype, db_join, 1, s)) != MSCL_SUCCESS) return st;
   if (dx) {
-    memset(&e, 0, sizeof e);
-    e.y = bytes_at(c.dx);
-    e.y_stride = c.dx_stride;
-    e.m = c.rows;
-    e.n = c.in_features;
     st = with_codec(c.dtype, [&](auto t) {
-      return product<decltype(t), true, false>(p.dx, dz, p.w, c.out_features, e, ws + p.partial_at, s);
+      return product<decltype(t), true, false>(p.dx, dz, p.w, c.out_features, ex, partial, s);
     });
     if (st != MSCL_SUCCESS) return st;
   }
   if (dw) {
-    memset(&e, 0, sizeof e);
-    e.y = bytes_at(c.dw);
-    e.y_stride = c.dw_stride;
-    e.m = c.out_features;
-    e.n = c.in_features;
     st = with_codec(c.dtype, [&](auto t) {
-      return product<decltype(t), false, false>(p.dw, dz, p.x, c.rows, e, ws + p.partial_at, s);
+      return product<decltype(t), false, false>(p.dw, dz, p.x, c.rows, ew, partial, s);
     });
   }
   return st;
@@ -807,7 +880,8 @@ mscl_status_t mscl_layer_norm_backward(const mscl_layer_norm_backward_t* call, v
       return launched("norm_back_fused");
     });
     if (st != MSCL_SUCCESS) return st;
-    return join_columns(c.param_dtype, a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2, s);
+    const JoinArgs j = join_args(a.sums, a.sums_stride, c.width, p.groups, c.dweight, c.dbias, 2);
+    return join_columns(c.param_dtype, j, 2, s);
   }
   if (p.sums) {
     a.along = reinterpret_cast<float*>(bytes_at(workspace) + p.along_at);
