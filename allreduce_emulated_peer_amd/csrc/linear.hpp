@@ -1026,19 +1026,20 @@ __global__ __launch_bounds__(256) void linear_join(const Epilogue a, int a_share
 
 // ------------------------------------------------------------------ few rows
 
-// Products of up to 64 rows, where the pass over w bounds: 8 waves share
+// Products of up to 32 rows, where the pass over w bounds: 8 waves share
 // 16 kN rows of w (columns of y) and split k between them, each streams its
 // part of w straight into the MFMA operand registers (no LDS on the way,
 // every byte of w is used once), and the 8 waves' sums meet in LDS.  x is
 // small and comes from the caches; its rows past the end repeat the last one,
 // as do w's, and their results are not stored.  A step is 128 bytes of k;
 // the loads of the next kDeep steps are in flight while kDeep are multiplied.
+// 1 x 8192 x 4096 bf16, from memory: 14.6 us (4.6 TB/s).
 template <class C, int kM, int kN, int kDeep>
 __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
   constexpr int V = C::V;
   constexpr int kStep = 8 * V;
   constexpr int kPitch = 16 * kN + 4;  // floats; rows 16 apart lie 4 banks apart
-  __shared__ __align__(16) float sums[8][16 * kM * kPitch];
+  __shared__ __align__(16) float sums[4][16 * kM * kPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * (16 * kN);
@@ -1128,12 +1129,19 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
   // k past the last whole step: the last share's last wave
   if (t.k % kStep && blockIdx.y == gridDim.y - 1 && wave == 7) single(whole, false);
 
+  // waves 4..7 hand their sums to waves 0..3
 #pragma unroll
-  for (int i = 0; i < kM; ++i)
+  for (int turn = 1; turn >= 0; --turn) {
+    if (wave >> 2 == turn)
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
-      *reinterpret_cast<f32x4*>(&sums[wave][(16 * i + r) * kPitch + 16 * j + 4 * g]) = acc[i][j];
-  __syncthreads();
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          f32x4& at = *reinterpret_cast<f32x4*>(&sums[wave & 3][(16 * i + r) * kPitch + 16 * j + 4 * g]);
+          at = turn ? acc[i][j] : at + acc[i][j];
+        }
+    __syncthreads();
+  }
   constexpr int kGroups = 16 * kM * 16 * kN / V;
   with_activation(t.e.act, [&](auto act) {
     for (int id = threadIdx.x; id < kGroups; id += 512) {
@@ -1142,7 +1150,7 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
 #pragma unroll
       for (int c = 0; c < V; ++c) v[c] = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
       if (t.e.partial)

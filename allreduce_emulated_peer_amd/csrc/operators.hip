@@ -273,11 +273,16 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     }
     p.pack_a = p.pack_b = false;
   }
-  if (a_along && b_along && m <= 64 && k > 0) {
+  // Up to 32 rows (bf16, us: 32 x 4096 x 8192 19 against 21 by tiles, 64 x
+  // 4096 x 8192 27 against 23).  Each wave reads all of x's part of k again,
+  // so with more than 8 rows 32 rows of w share it where that still fills the
+  // device (16 x 4096 x 8192: 17 against 20; 16 x 2048 x 2048: 8.0 against
+  // 6.3), with more than 16 always (32 x 8192 x 4096: 24 against 26).
+  if (a_along && b_along && m <= 32 && k > 0) {
     const uint64_t whole = std::max<uint64_t>(1, k / block);
     p.kind = ProductPlan::kFew;
-    p.tile_m = 64;
-    p.tile_n = ceil_div(n, 32) >= kCus ? 32 : 16;
+    p.tile_m = 32;
+    p.tile_n = m > 16 || (m > 8 && ceil_div(n, 32) >= kCus) ? 32 : 16;
     const uint64_t groups = ceil_div(n, p.tile_n);
     // 8 waves of a workgroup split k already; shares only where the
     // workgroups leave compute units idle, and of 4 steps a wave at least
@@ -350,23 +355,13 @@ mscl_status_t launch_join(const Epilogue& a, uint32_t a_shares, const Epilogue& 
 }
 
 template <class C>
-void launch_few(int tile, const TileArgs& t, dim3 grid, hipStream_t stream) {
-  const uint64_t m = t.e.m;
-  if (tile == 16) {
-    if (m <= 16)
-      linear_few<C, 1, 1, 4><<<grid, 512, 0, stream>>>(t);
-    else if (m <= 32)
-      linear_few<C, 2, 1, 2><<<grid, 512, 0, stream>>>(t);
-    else
-      linear_few<C, 4, 1, 2><<<grid, 512, 0, stream>>>(t);
-  } else {
-    if (m <= 16)
-      linear_few<C, 1, 2, 2><<<grid, 512, 0, stream>>>(t);
-    else if (m <= 32)
-      linear_few<C, 2, 2, 2><<<grid, 512, 0, stream>>>(t);
-    else
-      linear_few<C, 4, 2, 1><<<grid, 512, 0, stream>>>(t);
-  }
+void launch_few(int rows_of_w, const TileArgs& t, dim3 grid, hipStream_t stream) {
+  if (t.e.m > 16)
+    linear_few<C, 2, 2, 1><<<grid, 512, 0, stream>>>(t);
+  else if (rows_of_w == 32)
+    linear_few<C, 1, 2, 1><<<grid, 512, 0, stream>>>(t);
+  else
+    linear_few<C, 1, 1, 2><<<grid, 512, 0, stream>>>(t);
 }
 
 template <class C, bool kAAlong, bool kBAlong>
@@ -623,27 +618,35 @@ void launch_norm_back_fused(const NormBackArgs& a, uint32_t groups, hipStream_t 
   }
 }
 
-// A row's 16-byte vectors -> threads and vectors per thread that hold it.
+template <class C, class P, int kThreads, int kVecs>
+void launch_norm_rows(const NormArgs& a, hipStream_t s) {
+  const uint64_t groups = kThreads < 256 ? ceil_div(a.rows, 256 / kThreads) : a.rows;
+  norm_rows<C, P, kThreads, kVecs><<<static_cast<uint32_t>(groups), kThreads < 256 ? 256 : kThreads, 0, s>>>(a);
+}
+
+// A row's 16-byte vectors -> threads and vectors per thread that hold it.  Few
+// rows want the shortest way through a row, one vector a thread (32 x 8192
+// bf16: 1024 threads 3.9 us, 256 threads 5.1); many rows want few threads
+// with several vectors in flight each (8192 x 8192 bf16: 1024 threads 68 us,
+// 512 53, 256 48; 8192 x 2048: 256 threads 17.0 us, 64 threads 15.4).
 template <class C, class P>
 void launch_norm(const NormArgs& a, hipStream_t s) {
-  const uint64_t vecs = ceil_div(a.width, C::V);
-  const uint32_t rows = static_cast<uint32_t>(a.rows), quads = static_cast<uint32_t>(ceil_div(a.rows, 4));
-  if (vecs <= 64)
-    norm_rows<C, P, 64, 1><<<quads, 256, 0, s>>>(a);
-  else if (vecs <= 128)
-    norm_rows<C, P, 64, 2><<<quads, 256, 0, s>>>(a);
-  else if (vecs <= 256)
-    norm_rows<C, P, 256, 1><<<rows, 256, 0, s>>>(a);
-  else if (vecs <= 512)
-    norm_rows<C, P, 256, 2><<<rows, 256, 0, s>>>(a);
-  else if (vecs <= 1024)
-    norm_rows<C, P, 256, 4><<<rows, 256, 0, s>>>(a);
-  else if (vecs <= 2048)
-    norm_rows<C, P, 1024, 2><<<rows, 1024, 0, s>>>(a);
-  else if (vecs <= 4096)
-    norm_rows<C, P, 1024, 4><<<rows, 1024, 0, s>>>(a);
-  else
-    norm_rows_wide<C, P><<<rows, 1024, 0, s>>>(a);
+  const bool aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.rows == 1 || a.x_stride % C::V == 0);
+  const uint64_t vecs = ceil_div(a.width, C::V) + (aligned ? 0 : 1);
+  if (vecs <= 64) return launch_norm_rows<C, P, 64, 1>(a, s);
+  if (a.rows <= 2 * kCus) {
+    if (vecs <= 256) return launch_norm_rows<C, P, 256, 1>(a, s);
+    if (vecs <= 512) return launch_norm_rows<C, P, 512, 1>(a, s);
+    if (vecs <= 1024) return launch_norm_rows<C, P, 1024, 1>(a, s);
+  }
+  if (vecs <= 128) return launch_norm_rows<C, P, 64, 2>(a, s);
+  if (vecs <= 256) return launch_norm_rows<C, P, 64, 4>(a, s);
+  if (vecs <= 512) return launch_norm_rows<C, P, 256, 2>(a, s);
+  if (vecs <= 768) return launch_norm_rows<C, P, 256, 3>(a, s);
+  if (vecs <= 1024) return launch_norm_rows<C, P, 256, 4>(a, s);
+  if (vecs <= 2048) return launch_norm_rows<C, P, 512, 4>(a, s);
+  if (vecs <= 4096) return launch_norm_rows<C, P, 1024, 4>(a, s);
+  norm_rows_wide<C, P><<<static_cast<uint32_t>(a.rows), 1024, 0, s>>>(a);
 }
 
 template <class C, class P>

@@ -340,23 +340,19 @@ def _vector(name, t, n):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
-def _on_stream(device, stream, tensors, run):
-    """run(stream handle) with `device` current and allocations made for `stream` (default: torch's current one)."""
+def _elsewhere(device, stream, tensors, call):
+    """call() with `device` current and, if it is given, on `stream` (a torch stream or a handle)."""
     torch = _torch
-    index = device.index
-    if index == torch.cuda.current_device():
-        if stream is None:
-            return run(_raw_stream(index))
     with torch.cuda.device(device):
         if stream is None:
-            return run(_raw_stream(index))
+            return call()
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-            return run(stream.cuda_stream)
+            return call()
 
 
 def _workspace(query, call, like):
@@ -409,22 +405,23 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
             raise ValueError(f"residual must be {tuple(x.shape[:-1]) + (n,)}")
         rm = _matrix("residual", residual, n)
 
-    def run(handle):
-        y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
-        z = torch.empty_like(y) if return_preact else None
-        call = LINEAR.pack(xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), _address(bias), _address(rm),
-                           _row_stride(rm), y.data_ptr(), n, _address(z), n, rows, k, n, dtype,
-                           ACTIVATION_CODES[activation])
-        space, size = _workspace(lib.mscl_linear_workspace, call, x)
-        status = lib.mscl_linear(call, _address(space), size, handle or None)
-        if status:
-            _check(status, "mscl_linear")
-        if x.dim() != 2:
-            y = y.view(x.shape[:-1] + (n,))
-            z = z.view(y.shape) if return_preact else None
-        return (y, z) if return_preact else y
-
-    return _on_stream(x.device, stream, (x, weight, bias, residual), run)
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, (x, weight, bias, residual),
+                          lambda: linear_tensors(x, weight, bias, residual, activation, return_preact))
+    y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    z = torch.empty_like(y) if return_preact else None
+    call = LINEAR.pack(xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), _address(bias), _address(rm),
+                       _row_stride(rm), y.data_ptr(), n, _address(z), n, rows, k, n, dtype,
+                       ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_linear_workspace, call, x)
+    status = lib.mscl_linear(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_linear")
+    if x.dim() != 2:
+        y = y.view(x.shape[:-1] + (n,))
+        z = z.view(y.shape) if return_preact else None
+    return (y, z) if return_preact else y
 
 
 def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_dx=True, need_dw=True, need_db=True,
@@ -461,22 +458,23 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
             raise ValueError("preact must have dy's shape")
         zm = _matrix("preact", preact, n)
 
-    def run(handle):
-        dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device) if need_dx else None
-        dw = torch.empty((n, k), dtype=dy.dtype, device=dy.device) if need_dw else None
-        db = torch.empty((n,), dtype=dy.dtype, device=dy.device) if need_db else None
-        call = LINEAR_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(),
-                                    wm.stride(0), _address(zm), _row_stride(zm), _address(dx), k, _address(dw), k,
-                                    _address(db), rows, k, n, dtype, ACTIVATION_CODES[activation])
-        space, size = _workspace(lib.mscl_linear_backward_workspace, call, dy)
-        status = lib.mscl_linear_backward(call, _address(space), size, handle or None)
-        if status:
-            _check(status, "mscl_linear_backward")
-        if need_dx and x.dim() != 2:
-            dx = dx.view(x.shape)
-        return dx, dw, db
-
-    return _on_stream(dy.device, stream, (dy, x, weight, preact), run)
+    index = dy.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(dy.device, stream, (dy, x, weight, preact),
+                          lambda: linear_backward_tensors(dy, x, weight, preact, activation, need_dx, need_dw, need_db))
+    dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device) if need_dx else None
+    dw = torch.empty((n, k), dtype=dy.dtype, device=dy.device) if need_dw else None
+    db = torch.empty((n,), dtype=dy.dtype, device=dy.device) if need_db else None
+    call = LINEAR_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(),
+                                wm.stride(0), _address(zm), _row_stride(zm), _address(dx), k, _address(dw), k,
+                                _address(db), rows, k, n, dtype, ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_linear_backward_workspace, call, dy)
+    status = lib.mscl_linear_backward(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_linear_backward")
+    if need_dx and x.dim() != 2:
+        dx = dx.view(x.shape)
+    return dx, dw, db
 
 
 def _param_code(like, **tensors):
@@ -516,20 +514,21 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     xm = _matrix("x", x, width)
     rows = xm.shape[0]
 
-    def run(handle):
-        y = torch.empty_like(xm) if xm.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
-        rstd = torch.empty_like(mean) if return_stats else None
-        call = LAYER_NORM.pack(xm.data_ptr(), xm.stride(0), _address(weight), _address(bias), y.data_ptr(), width,
-                               _address(mean), _address(rstd), rows, width, eps, codes[x.dtype], param)
-        status = lib.mscl_layer_norm(call, handle or None)
-        if status:
-            _check(status, "mscl_layer_norm")
-        if x.dim() != 2:
-            y = y.view(x.shape)
-        return (y, mean, rstd) if return_stats else y
-
-    return _on_stream(x.device, stream, (x, weight, bias), run)
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, (x, weight, bias),
+                          lambda: layer_norm_tensors(x, weight, bias, eps, return_stats))
+    y = torch.empty_like(xm) if xm.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
+    rstd = torch.empty_like(mean) if return_stats else None
+    call = LAYER_NORM.pack(xm.data_ptr(), xm.stride(0), _address(weight), _address(bias), y.data_ptr(), width,
+                           _address(mean), _address(rstd), rows, width, eps, codes[x.dtype], param)
+    status = lib.mscl_layer_norm(call, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_layer_norm")
+    if x.dim() != 2:
+        y = y.view(x.shape)
+    return (y, mean, rstd) if return_stats else y
 
 
 def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, need_dw=True, need_db=True, stream=None):
@@ -558,19 +557,20 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
     gm, xm = _matrix("dy", dy, width), _matrix("x", x, width)
     rows = gm.shape[0]
 
-    def run(handle):
-        dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device) if need_dx else None
-        dw = torch.empty((width,), dtype=kind, device=dy.device) if need_dw else None
-        db = torch.empty((width,), dtype=kind, device=dy.device) if need_db else None
-        call = LAYER_NORM_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), mean.data_ptr(),
-                                        rstd.data_ptr(), _address(weight), _address(dx), width, _address(dw),
-                                        _address(db), rows, width, codes[dy.dtype], codes[kind])
-        space, size = _workspace(lib.mscl_layer_norm_backward_workspace, call, dy)
-        status = lib.mscl_layer_norm_backward(call, _address(space), size, handle or None)
-        if status:
-            _check(status, "mscl_layer_norm_backward")
-        if need_dx and dy.dim() != 2:
-            dx = dx.view(dy.shape)
-        return dx, dw, db
-
-    return _on_stream(dy.device, stream, (dy, x, mean, rstd, weight), run)
+    index = dy.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(dy.device, stream, (dy, x, mean, rstd, weight),
+                          lambda: layer_norm_backward_tensors(dy, x, mean, rstd, weight, need_dx, need_dw, need_db))
+    dx = torch.empty((rows, width), dtype=dy.dtype, device=dy.device) if need_dx else None
+    dw = torch.empty((width,), dtype=kind, device=dy.device) if need_dw else None
+    db = torch.empty((width,), dtype=kind, device=dy.device) if need_db else None
+    call = LAYER_NORM_BACKWARD.pack(gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), mean.data_ptr(),
+                                    rstd.data_ptr(), _address(weight), _address(dx), width, _address(dw),
+                                    _address(db), rows, width, codes[dy.dtype], codes[kind])
+    space, size = _workspace(lib.mscl_layer_norm_backward_workspace, call, dy)
+    status = lib.mscl_layer_norm_backward(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_layer_norm_backward")
+    if need_dx and dy.dim() != 2:
+        dx = dx.view(dy.shape)
+    return dx, dw, db
