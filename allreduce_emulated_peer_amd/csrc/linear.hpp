@@ -356,6 +356,26 @@ __global__ __launch_bounds__(256) void column_join(const JoinArgs a) {
 
 // ------------------------------------------------------------------ general tile kernel
 
+// Workgroup w of a launch runs on XCD w % 8, and each XCD has an L2 of its
+// own.  This hands each XCD one run of neighbouring work items out of `total`.
+__device__ inline uint32_t xcd_run(uint32_t w, uint32_t total) {
+  const uint32_t per = total / 8, more = total % 8, x = w % 8, i = w / 8;
+  return x * per + (x < more ? x : more) + i;
+}
+
+// Tile `id` in bands of 8 tile rows, down each band's columns: what is in
+// flight on one XCD then shares rows of A and columns of B in its L2.
+struct TileAt {
+  uint32_t m, n;
+  __device__ inline TileAt(uint32_t id, uint32_t tiles_m, uint32_t tiles_n) {
+    constexpr uint32_t kBand = 8;
+    const uint32_t band = id / (kBand * tiles_n), in_band = id % (kBand * tiles_n);
+    const uint32_t high = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
+    m = band * kBand + in_band % high;
+    n = in_band / high;
+  }
+};
+
 struct Operand {
   const char* base;
   uint64_t stride;  // elements between memory rows
@@ -368,7 +388,69 @@ struct TileArgs {
   Epilogue e;
   uint64_t k;
   uint32_t tiles_m, tiles_n;
-  uint32_t blocks_per_share;  // blocks of k that one share (blockIdx.y) sums
+  uint32_t blocks_per_share;  // blocks of k that one share sums
+};
+
+// Where one operand's kT x (64 k) tiles of a run of k come from: a thread's
+// 8-element chunks, block after block, kParts 16-byte loads each.  Addresses
+// are set up once and then only advance; inside the matrix no bound is looked
+// at.  Rows (kAlong) and columns (kDown) past the matrix meet only results
+// that are not stored: a row past the end repeats the last one.
+template <class C, bool kAlong, int kT, int kThreads, int kParts>
+struct Feed {
+  static constexpr int kChunks = kT * 8 / kThreads;
+  static constexpr int kPerRow = kAlong ? 8 : kT / 8;  // chunks per LDS row
+  static constexpr int e = C::kElemBytes;
+  const char* p[kChunks];
+  uint64_t k, k_end, step;  // step: bytes between blocks
+  uint64_t cols_left;       // kDown: columns from the tile's first on
+  bool whole;               // kDown: all of the tile's columns exist
+
+  __device__ inline void init(const Operand& o, uint64_t first, uint64_t k_first, uint64_t k_end_) {
+    k = k_first;
+    k_end = k_end_;
+    step = kAlong ? 64 * e : 64 * o.stride * e;
+    cols_left = kAlong ? 0 : o.cols - first;
+    whole = kAlong || cols_left >= kT;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = i * kThreads + threadIdx.x;
+      const int r = id / kPerRow, c = id % kPerRow;
+      uint64_t row = (kAlong ? first : k_first) + r;
+      if (kAlong && row >= o.rows) row = o.rows - 1;
+      p[i] = o.base + (row * o.stride + (kAlong ? k_first : first) + static_cast<uint64_t>(c) * 8) * e;
+    }
+  }
+
+  // fn(chunk, part, address, how many of the part's elements exist) for the
+  // next block.
+  template <class Fn>
+  __device__ inline void next(Fn&& fn) {
+    constexpr int V = C::V;
+    if (whole && k + 64 <= k_end) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int id = i * kThreads + threadIdx.x;
+        const int r = id / kPerRow, c = id % kPerRow;
+        int64_t valid;
+        if constexpr (kAlong)
+          valid = static_cast<int64_t>(k_end - k) - c * 8;
+        else
+          valid = k + r < k_end ? static_cast<int64_t>(cols_left) - c * 8 : 0;
+        const int n = valid < 0 ? 0 : (valid > 8 ? 8 : static_cast<int>(valid));
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, n - q * V);
+      }
+    }
+    k += 64;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) p[i] += step;
+  }
 };
 
 // One operand's kT x (64 k) tile of a 16-bit type, from memory through
@@ -395,19 +477,8 @@ struct Stage {
     return chunk ^ ((key & (kSegs - 1)) << 1);
   }
 
-  __device__ inline void load(const Operand& o, uint64_t first, uint64_t k0, uint64_t k_end) {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int id = i * kThreads + threadIdx.x;
-      const int r = id / kPerRow, c = id % kPerRow;
-      const uint64_t row = (kAlong ? first : k0) + r;
-      const uint64_t col = (kAlong ? k0 : first) + static_cast<uint64_t>(c) * V;
-      const uint64_t rows = kAlong ? o.rows : k_end;
-      const uint64_t cols = kAlong ? k_end : o.cols;
-      int valid = 0;
-      if (row < rows && col < cols) valid = cols - col < V ? static_cast<int>(cols - col) : V;
-      held[i] = load_upto<C>(o.base + (row * o.stride + col) * C::kElemBytes, valid);
-    }
+  __device__ inline void load(Feed<C, kAlong, kT, kThreads, 1>& f) {
+    f.next([&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -471,8 +542,8 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
   using SB = Stage<C, kBAlong, kBN, 256>;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
   static_assert(kDeep % 2 == 0, "the LDS buffers alternate");
-  const uint32_t tm = tile % t.tiles_m, tn = tile / t.tiles_m;
-  const uint64_t m0 = static_cast<uint64_t>(tm) * kBM, n0 = static_cast<uint64_t>(tn) * kBN;
+  const TileAt at(tile, t.tiles_m, t.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * kBN;
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * SA::kBlock;
@@ -487,12 +558,15 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
 
   SA sa[kDeep];
   SB sb[kDeep];
+  Feed<C, kAAlong, kBM, 256, 1> feed_a;
+  Feed<C, kBAlong, kBN, 256, 1> feed_b;
+  feed_a.init(t.a, m0, k_first, k_end);
+  feed_b.init(t.b, n0, k_first, k_end);
 #pragma unroll
   for (int d = 0; d < kDeep; ++d) {
-    const uint64_t k = k_first + d * SA::kBlock;
-    if (k < k_end) {
-      sa[d].load(t.a, m0, k, k_end);
-      sb[d].load(t.b, n0, k, k_end);
+    if (k_first + d * SA::kBlock < k_end) {
+      sa[d].load(feed_a);
+      sb[d].load(feed_b);
     }
   }
   for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * SA::kBlock) {
@@ -506,8 +580,8 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
       sb[d].store(lb);
       __syncthreads();
       if (k + kDeep * SA::kBlock < k_end) {
-        sa[d].load(t.a, m0, k + kDeep * SA::kBlock, k_end);
-        sb[d].load(t.b, n0, k + kDeep * SA::kBlock, k_end);
+        sa[d].load(feed_a);
+        sb[d].load(feed_b);
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -642,20 +716,8 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   const int wm = wave >> 2, wn = wave & 3;
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
 
-  // Workgroup w runs on XCD w % 8: each XCD gets a run of neighbouring tiles,
-  // and runs go down bands of 8 tile rows, so that what is in flight on one
-  // XCD shares operands in its L2.
-  const uint32_t tiles = args.tiles_m * args.tiles_n;
-  uint32_t id = blockIdx.x;
-  {
-    const uint32_t per = tiles / 8, more = tiles % 8, x = id % 8, i = id / 8;
-    id = x * per + (x < more ? x : more) + i;
-  }
-  constexpr uint32_t kBand = 8;
-  const uint32_t band = id / (kBand * args.tiles_n), in_band = id % (kBand * args.tiles_n);
-  const uint32_t high = args.tiles_m - band * kBand < kBand ? args.tiles_m - band * kBand : kBand;
-  const uint64_t m0 = static_cast<uint64_t>(band * kBand + in_band % high) * 256;
-  const uint64_t n0 = static_cast<uint64_t>(in_band / high) * 256;
+  const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
 
   Copier<C, kAAlong> ca;
   Copier<C, kBAlong> cb;
@@ -791,21 +853,8 @@ struct SplitStage {
   static constexpr int kBytes = 3 * S::kBytes;
   u32x4 held[kChunks][2];
 
-  __device__ inline void load(const Operand& o, uint64_t first, uint64_t k0, uint64_t k_end) {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int id = i * 256 + threadIdx.x;
-      const int r = id / kPerRow, c = id % kPerRow;
-      const uint64_t row = (kAlong ? first : k0) + r;
-      const uint64_t col = (kAlong ? k0 : first) + static_cast<uint64_t>(c) * 8;
-      const uint64_t rows = kAlong ? o.rows : k_end;
-      const uint64_t cols = kAlong ? k_end : o.cols;
-      int valid = 0;
-      if (row < rows && col < cols) valid = cols - col < 8 ? static_cast<int>(cols - col) : 8;
-      const char* p = o.base + (row * o.stride + col) * 4;
-      held[i][0] = load_upto<F32>(p, valid);
-      held[i][1] = load_upto<F32>(p + 16, valid - 4);
-    }
+  __device__ inline void load(Feed<F32, kAlong, kT, 256, 2>& f) {
+    f.next([&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -840,8 +889,8 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
   using SA = SplitStage<kAAlong, kBM>;
   using SB = SplitStage<kBAlong, kBN>;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
-  const uint32_t tm = tile % t.tiles_m, tn = tile / t.tiles_m;
-  const uint64_t m0 = static_cast<uint64_t>(tm) * kBM, n0 = static_cast<uint64_t>(tn) * kBN;
+  const TileAt at(tile, t.tiles_m, t.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * kBN;
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * 64;
@@ -856,12 +905,15 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
 
   SA sa[kDeep];
   SB sb[kDeep];
+  Feed<F32, kAAlong, kBM, 256, 2> feed_a;
+  Feed<F32, kBAlong, kBN, 256, 2> feed_b;
+  feed_a.init(t.a, m0, k_first, k_end);
+  feed_b.init(t.b, n0, k_first, k_end);
 #pragma unroll
   for (int d = 0; d < kDeep; ++d) {
-    const uint64_t k = k_first + d * 64;
-    if (k < k_end) {
-      sa[d].load(t.a, m0, k, k_end);
-      sb[d].load(t.b, n0, k, k_end);
+    if (k_first + d * 64 < k_end) {
+      sa[d].load(feed_a);
+      sb[d].load(feed_b);
     }
   }
   for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * 64) {
@@ -873,8 +925,8 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
       sb[d].store(lds + SA::kBytes);
       __syncthreads();
       if (k + kDeep * 64 < k_end) {
-        sa[d].load(t.a, m0, k + kDeep * 64, k_end);
-        sb[d].load(t.b, n0, k + kDeep * 64, k_end);
+        sa[d].load(feed_a);
+        sb[d].load(feed_b);
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -959,11 +1011,12 @@ __device__ inline void any_tile(const TileArgs& t, uint32_t tile, uint32_t share
     tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 128 ? 2 : 4>(t, tile, share, lds);
 }
 
-// One product; blockIdx.y is the share of k.
+// One product: all tiles of the first share of k, then of the next one.
 template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
 __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs t) {
   extern __shared__ __align__(16) char lds[];
-  any_tile<C, kAAlong, kBAlong, kBM, kBN>(t, blockIdx.x, blockIdx.y, lds);
+  const uint32_t id = xcd_run(blockIdx.x, gridDim.x), tiles = t.tiles_m * t.tiles_n;
+  any_tile<C, kAAlong, kBAlong, kBM, kBN>(t, id % tiles, id / tiles, lds);
 }
 
 // Both gradients' products and the bias gradient's last sums in one launch:
@@ -980,11 +1033,13 @@ __global__ __launch_bounds__(256, 2) void linear_pair(const PairArgs p) {
   extern __shared__ __align__(16) char lds[];
   uint32_t id = blockIdx.x;
   if (id < p.dx_groups) {
+    id = xcd_run(id, p.dx_groups);
     any_tile<C, true, false, kBM, kBN>(p.dx, id % p.dx_tiles, id / p.dx_tiles, lds);
     return;
   }
   id -= p.dx_groups;
   if (id < p.dw_groups) {
+    id = xcd_run(id, p.dw_groups);
     any_tile<C, false, false, kBM, kBN>(p.dw, id % p.dw_tiles, id / p.dw_tiles, lds);
     return;
   }

@@ -241,15 +241,16 @@ void choose_tile(ProductPlan* p, uint64_t large, int dtype) {
   }
 }
 
-// Shares of k for a product of m x n in a launch of `tiles` tiles: as many as
-// the device holds at once (two workgroups a compute unit), of 4 blocks of 64
-// k at least.  512 x 512 fp32 with k = 2048: 1 share 53 us, 2 30, 4 20, 8 18;
-// 300 x 700 with k = 1024: 1 share 29 us, 4 14, 8 15.
-void choose_shares(ProductPlan* p, uint64_t m, uint64_t n, uint64_t k, uint64_t tiles) {
+// Shares of k for a product of m x n: no workgroup's run of blocks of 64 k is
+// longer than the launch's blocks (of all of its tiles) divided over what the
+// device holds at once, two workgroups a compute unit; 4 blocks at least.
+// 512 x 512 fp32 with k = 2048: 1 share 53 us, 2 30, 4 20, 8 18; 300 x 700
+// with k = 1024: 1 share 29 us, 4 14, 8 15.
+void choose_shares(ProductPlan* p, uint64_t m, uint64_t n, uint64_t k, uint64_t launch_blocks) {
   const uint64_t steps = ceil_div(k, 64);
-  uint64_t shares = 1;
-  if (tiles < 2 * kCus && steps >= 8) shares = std::min({2 * kCus / tiles, steps / 4, uint64_t(32)});
-  p->blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, std::max<uint64_t>(1, shares))));
+  const uint64_t run = std::max<uint64_t>(4, ceil_div(launch_blocks, 2 * kCus));
+  const uint64_t shares = std::min<uint64_t>(32, std::max<uint64_t>(1, steps / run));
+  p->blocks_per_share = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, shares)));
   p->shares = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(steps, p->blocks_per_share)));
   p->partial_stride = round_up(n, 8);
   if (p->shares > 1) p->partial_bytes = round_up(p->shares * m * p->partial_stride * 4, 256);
@@ -294,7 +295,7 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
     return p;
   }
   choose_tile(&p, ceil_div(m, 128) * ceil_div(n, 128), dtype);
-  choose_shares(&p, m, n, k, ceil_div(m, p.tile_m) * ceil_div(n, p.tile_n));
+  choose_shares(&p, m, n, k, ceil_div(m, p.tile_m) * ceil_div(n, p.tile_n) * ceil_div(k, 64));
   return p;
 }
 
@@ -338,7 +339,7 @@ mscl_status_t launch_tile(const TileArgs& t, uint32_t shares, hipStream_t stream
   constexpr int kLds = tile_lds<C, kAAlong, kBAlong, kBM, kBN>();
   const hipError_t err = allow_lds<&linear_tile<C, kAAlong, kBAlong, kBM, kBN>>(kLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
-  linear_tile<C, kAAlong, kBAlong, kBM, kBN><<<dim3(t.tiles_m * t.tiles_n, shares), 256, kLds, stream>>>(t);
+  linear_tile<C, kAAlong, kBAlong, kBM, kBN><<<t.tiles_m * t.tiles_n * shares, 256, kLds, stream>>>(t);
   return launched("linear_tile");
 }
 
@@ -368,7 +369,7 @@ template <class C, bool kAAlong, bool kBAlong>
 mscl_status_t product(const ProductPlan& p, Operand a, Operand b, uint64_t k, const Epilogue& e0, char* workspace,
                       hipStream_t stream) {
   const uint64_t tm = ceil_div(e0.m, p.tile_m), tn = ceil_div(e0.n, p.tile_n);
-  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  if (tm > kMostGroups / tn / p.shares) return bad("the matrices have too many tiles");
   const uint32_t groups = static_cast<uint32_t>(tm * tn);
   if constexpr (C::kElemBytes == 2) {
     if (p.kind == ProductPlan::kBig) {
@@ -499,10 +500,11 @@ BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
     p.dx = p.dw = ProductPlan();
     choose_tile(&p.dx, (ceil_div(c.rows, 128) + ceil_div(c.out_features, 128)) * k, c.dtype);
     choose_tile(&p.dw, (ceil_div(c.rows, 128) + ceil_div(c.out_features, 128)) * k, c.dtype);
-    const uint64_t tiles = (ceil_div(c.rows, p.dx.tile_m) + ceil_div(c.out_features, p.dw.tile_m)) *
-                           ceil_div(c.in_features, p.dx.tile_n);
-    choose_shares(&p.dx, c.rows, c.in_features, c.out_features, tiles);
-    choose_shares(&p.dw, c.out_features, c.in_features, c.rows, tiles);
+    const uint64_t launch = (ceil_div(c.rows, p.dx.tile_m) * ceil_div(c.out_features, 64) +
+                             ceil_div(c.out_features, p.dw.tile_m) * ceil_div(c.rows, 64)) *
+                            ceil_div(c.in_features, p.dx.tile_n);
+    choose_shares(&p.dx, c.rows, c.in_features, c.out_features, launch);
+    choose_shares(&p.dw, c.out_features, c.in_features, c.rows, launch);
     partial = (c.dx ? p.dx.partial_bytes : 0) + (c.dw ? p.dw.partial_bytes : 0);
   } else {
     if (c.dx) partial = std::max(partial, p.dx.bytes());
