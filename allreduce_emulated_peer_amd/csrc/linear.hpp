@@ -392,66 +392,113 @@ struct TileArgs {
 };
 
 // Where one operand's kT x (64 k) tiles of a run of k come from: a thread's
-// 8-element chunks, block after block, kParts 16-byte loads each.  Addresses
-// are set up once and then only advance; inside the matrix no bound is looked
-// at.  Rows (kAlong) and columns (kDown) past the matrix meet only results
-// that are not stored: a row past the end repeats the last one.
+// 8-element chunks, block after block, kParts 16-byte loads each.  Rows
+// (kAlong) and columns (kDown) past the matrix meet only results that are not
+// stored: a row past the end repeats the last one.
+// The whole blocks' loads hang on no branch, or the compiler could not count
+// which of the loads in flight a use has to wait for, and would wait for all:
+// addresses are set up once and advance, past the last whole block by 0.
 template <class C, bool kAlong, int kT, int kThreads, int kParts>
 struct Feed {
   static constexpr int kChunks = kT * 8 / kThreads;
   static constexpr int kPerRow = kAlong ? 8 : kT / 8;  // chunks per LDS row
   static constexpr int e = C::kElemBytes;
   const char* p[kChunks];
-  uint64_t k, k_end, step;  // step: bytes between blocks
-  uint64_t cols_left;       // kDown: columns from the tile's first on
-  bool whole;               // kDown: all of the tile's columns exist
+  uint64_t step;      // bytes between blocks
+  uint64_t cols;      // kDown: columns from the tile's first on
+  uint32_t left = 0;  // whole blocks not yet loaded
 
-  __device__ inline void init(const Operand& o, uint64_t first, uint64_t k_first, uint64_t k_end_) {
-    k = k_first;
-    k_end = k_end_;
+  __device__ inline void init(const Operand& o, uint64_t first, uint64_t k) {
     step = kAlong ? 64 * e : 64 * o.stride * e;
-    cols_left = kAlong ? 0 : o.cols - first;
-    whole = kAlong || cols_left >= kT;
+    cols = kAlong ? 0 : o.cols - first;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int id = i * kThreads + threadIdx.x;
       const int r = id / kPerRow, c = id % kPerRow;
-      uint64_t row = (kAlong ? first : k_first) + r;
+      uint64_t row = (kAlong ? first : k) + r;
       if (kAlong && row >= o.rows) row = o.rows - 1;
-      p[i] = o.base + (row * o.stride + (kAlong ? k_first : first) + static_cast<uint64_t>(c) * 8) * e;
+      p[i] = o.base + (row * o.stride + (kAlong ? k : first) + static_cast<uint64_t>(c) * 8) * e;
     }
   }
+  // Whether all of the tile's columns exist.
+  __device__ inline bool whole() const { return kAlong || cols >= kT; }
 
   // fn(chunk, part, address, how many of the part's elements exist) for the
-  // next block.
+  // next whole block.
   template <class Fn>
   __device__ inline void next(Fn&& fn) {
-    constexpr int V = C::V;
-    if (whole && k + 64 <= k_end) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, V);
-    } else {
+      for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, C::V);
+    const uint64_t by = left > 1 ? step : 0;
+    if (left > 1) --left;
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int id = i * kThreads + threadIdx.x;
-        const int r = id / kPerRow, c = id % kPerRow;
-        int64_t valid;
-        if constexpr (kAlong)
-          valid = static_cast<int64_t>(k_end - k) - c * 8;
-        else
-          valid = k + r < k_end ? static_cast<int64_t>(cols_left) - c * 8 : 0;
-        const int n = valid < 0 ? 0 : (valid > 8 ? 8 : static_cast<int>(valid));
+    for (int i = 0; i < kChunks; ++i) p[i] += by;
+  }
+
+  // The same for a block at k of which k_end - k may be less than 64, or
+  // whose columns may end.
+  template <class Fn>
+  __device__ inline void edge(const Operand& o, uint64_t first, uint64_t k, uint64_t k_end, Fn&& fn) {
+    init(o, first, k);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, n - q * V);
-      }
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = i * kThreads + threadIdx.x;
+      const int r = id / kPerRow, c = id % kPerRow;
+      int64_t valid;
+      if constexpr (kAlong)
+        valid = static_cast<int64_t>(k_end - k) - c * 8;
+      else
+        valid = k + r < k_end ? static_cast<int64_t>(cols) - c * 8 : 0;
+      const int n = valid < 0 ? 0 : (valid > 8 ? 8 : static_cast<int>(valid));
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, n - q * C::V);
     }
-    k += 64;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) p[i] += step;
   }
 };
+
+// Walks over the blocks of k of a tile: kDeep whole blocks' loads in flight,
+// then what is left one by one.  store(d) puts set d into an LDS buffer,
+// compute(d) multiplies it; kBuffers LDS buffers alternate.
+template <int kDeep, int kBuffers, class FA, class FB, class SA, class SB, class Store, class Compute>
+__device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_t k_first, uint64_t k_end, FA& feed_a,
+                            FB& feed_b, SA (&sa)[kDeep], SB (&sb)[kDeep], Store&& store, Compute&& compute) {
+  feed_a.init(t.a, m0, k_first);
+  feed_b.init(t.b, n0, k_first);
+  uint64_t k = k_first;
+  const uint32_t blocks =
+      k_end > k_first && feed_a.whole() && feed_b.whole() ? static_cast<uint32_t>((k_end - k_first) / 64) : 0;
+  if (blocks > 0) {
+    feed_a.left = feed_b.left = blocks;
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      sa[d].load(feed_a);
+      sb[d].load(feed_b);
+    }
+    for (uint32_t block = 0; block < blocks; block += kDeep) {
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        if (block + d >= blocks) break;
+        store(d);
+        __syncthreads();
+        sa[d].load(feed_a);
+        sb[d].load(feed_b);
+        compute(d);
+        if constexpr (kBuffers == 1) __syncthreads();
+      }
+    }
+    k += static_cast<uint64_t>(blocks) * 64;
+  }
+  for (; k < k_end; k += 64) {
+    sa[0].load_edge(feed_a, t.a, m0, k, k_end);
+    sb[0].load_edge(feed_b, t.b, n0, k, k_end);
+    __syncthreads();
+    store(0);
+    __syncthreads();
+    compute(0);
+  }
+}
 
 // One operand's kT x (64 k) tile of a 16-bit type, from memory through
 // registers into LDS.  kAlong: kT rows of 128 bytes, 16-byte chunk c of row r
@@ -479,6 +526,10 @@ struct Stage {
 
   __device__ inline void load(Feed<C, kAlong, kT, kThreads, 1>& f) {
     f.next([&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
+  }
+  __device__ inline void load_edge(Feed<C, kAlong, kT, kThreads, 1>& f, const Operand& o, uint64_t first, uint64_t k,
+                                   uint64_t k_end) {
+    f.edge(o, first, k, k_end, [&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -560,43 +611,29 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
   SB sb[kDeep];
   Feed<C, kAAlong, kBM, 256, 1> feed_a;
   Feed<C, kBAlong, kBN, 256, 1> feed_b;
-  feed_a.init(t.a, m0, k_first, k_end);
-  feed_b.init(t.b, n0, k_first, k_end);
+  auto buffer = [&](int d) { return lds + (d & 1) * (SA::kBytes + SB::kBytes); };
+  walk<kDeep, 2>(
+      t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
+      [&](int d) {
+        sa[d].store(buffer(d));
+        sb[d].store(buffer(d) + SA::kBytes);
+      },
+      [&](int d) {
+        const char* la = buffer(d);
+        const char* lb = la + SA::kBytes;
 #pragma unroll
-  for (int d = 0; d < kDeep; ++d) {
-    if (k_first + d * SA::kBlock < k_end) {
-      sa[d].load(feed_a);
-      sb[d].load(feed_b);
-    }
-  }
-  for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * SA::kBlock) {
+        for (int s = 0; s < 2; ++s) {
+          u32x4 fa[kWM], fb[kWN];
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const uint64_t k = k0 + d * SA::kBlock;
-      if (k >= k_end) break;
-      char* la = lds + (d & 1) * (SA::kBytes + SB::kBytes);
-      char* lb = la + SA::kBytes;
-      sa[d].store(la);
-      sb[d].store(lb);
-      __syncthreads();
-      if (k + kDeep * SA::kBlock < k_end) {
-        sa[d].load(feed_a);
-        sb[d].load(feed_b);
-      }
+          for (int i = 0; i < kWM; ++i) fa[i] = SA::fragment(la, wm + 16 * i, s);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 fa[kWM], fb[kWN];
+          for (int j = 0; j < kWN; ++j) fb[j] = SB::fragment(lb, wn + 16 * j, s);
 #pragma unroll
-        for (int i = 0; i < kWM; ++i) fa[i] = SA::fragment(la, wm + 16 * i, s);
+          for (int i = 0; i < kWM; ++i)
 #pragma unroll
-        for (int j = 0; j < kWN; ++j) fb[j] = SB::fragment(lb, wn + 16 * j, s);
-#pragma unroll
-        for (int i = 0; i < kWM; ++i)
-#pragma unroll
-          for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
-      }
-    }
-  }
+            for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
+        }
+      });
   if (t.e.partial) {
     using G = Groups<C, kWM, kWN>;
 #pragma unroll
@@ -856,6 +893,10 @@ struct SplitStage {
   __device__ inline void load(Feed<F32, kAlong, kT, 256, 2>& f) {
     f.next([&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
   }
+  __device__ inline void load_edge(Feed<F32, kAlong, kT, 256, 2>& f, const Operand& o, uint64_t first, uint64_t k,
+                                   uint64_t k_end) {
+    f.edge(o, first, k, k_end, [&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
+  }
   __device__ inline void store(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -907,51 +948,35 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
   SB sb[kDeep];
   Feed<F32, kAAlong, kBM, 256, 2> feed_a;
   Feed<F32, kBAlong, kBN, 256, 2> feed_b;
-  feed_a.init(t.a, m0, k_first, k_end);
-  feed_b.init(t.b, n0, k_first, k_end);
+  walk<kDeep, 1>(
+      t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
+      [&](int d) {
+        sa[d].store(lds);
+        sb[d].store(lds + SA::kBytes);
+      },
+      [&](int) {
 #pragma unroll
-  for (int d = 0; d < kDeep; ++d) {
-    if (k_first + d * 64 < k_end) {
-      sa[d].load(feed_a);
-      sb[d].load(feed_b);
-    }
-  }
-  for (uint64_t k0 = k_first; k0 < k_end; k0 += kDeep * 64) {
+        for (int s = 0; s < 2; ++s) {
+          u32x4 fb[3][kWN];
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const uint64_t k = k0 + d * 64;
-      if (k >= k_end) break;
-      sa[d].store(lds);
-      sb[d].store(lds + SA::kBytes);
-      __syncthreads();
-      if (k + kDeep * 64 < k_end) {
-        sa[d].load(feed_a);
-        sb[d].load(feed_b);
-      }
+          for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 fb[3][kWN];
+            for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+          for (int i = 0; i < kWM; ++i) {
+            u32x4 fa[3];
 #pragma unroll
-          for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
+            for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
+            // the smaller products first
 #pragma unroll
-        for (int i = 0; i < kWM; ++i) {
-          u32x4 fa[3];
+            for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-          for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
-          // the smaller products first
+              for (int p = 0; p <= sum; ++p)
 #pragma unroll
-          for (int sum = 2; sum >= 0; --sum)
-#pragma unroll
-            for (int p = 0; p <= sum; ++p)
-#pragma unroll
-              for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+                for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+          }
         }
-      }
-      __syncthreads();
-    }
-  }
+      });
 
   bool odd = false;
 #pragma unroll
@@ -1149,19 +1174,27 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
 #pragma unroll
           for (int j = 0; j < kN; ++j) acc[i][j] = multiply<C>(wq[set][d][j][h], xq[set][d][i][h], acc[i][j]);
   };
+  // The multiplication stands in the branch with the loads it overlaps: behind
+  // a join of paths with and without them the compiler waits for all.
   if (step + kDeep <= end) {
     load(0, step);
     for (;;) {
-      const bool second = step + 2 * kDeep <= end;
-      if (second) load(1, step + kDeep);
+      if (step + 2 * kDeep > end) {
+        compute(0);
+        step += kDeep;
+        break;
+      }
+      load(1, step + kDeep);
       compute(0);
       step += kDeep;
-      if (!second) break;
-      const bool third = step + 2 * kDeep <= end;
-      if (third) load(0, step + kDeep);
+      if (step + 2 * kDeep > end) {
+        compute(1);
+        step += kDeep;
+        break;
+      }
+      load(0, step + kDeep);
       compute(1);
       step += kDeep;
-      if (!third) break;
     }
   }
   auto single = [&](uint64_t at, bool whole_step) {
