@@ -475,15 +475,27 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
     for (int d = 0; d < kDeep; ++d) {
       sa[d].load(feed_a);
       sb[d].load(feed_b);
+      __builtin_amdgcn_sched_barrier(0);  // in this order, as the loop's waits count on it
     }
-    for (uint32_t block = 0; block < blocks; block += kDeep) {
+    // whole groups of kDeep blocks, so that the loop has one way out, then the rest
+    uint32_t block = 0;
+    for (; block + kDeep <= blocks; block += kDeep) {
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
-        if (block + d >= blocks) break;
         store(d);
         __syncthreads();
         sa[d].load(feed_a);
         sb[d].load(feed_b);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(d);
+        if constexpr (kBuffers == 1) __syncthreads();
+      }
+    }
+#pragma unroll
+    for (int d = 0; d + 1 < kDeep; ++d) {
+      if (block + d < blocks) {
+        store(d);
+        __syncthreads();
         compute(d);
         if constexpr (kBuffers == 1) __syncthreads();
       }
