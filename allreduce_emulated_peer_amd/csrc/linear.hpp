@@ -289,10 +289,24 @@ struct Groups {
 };
 
 // Finishes and stores a wave's kParts blocks of tiles, block p at (m0, n0) of
-// at(p).
-template <class C, int kM, int kN, int kParts, class At>
+// at(p).  kPlain: a gradient's product, of which nothing but the sums is
+// wanted (its kernels have half the code and need fewer registers).
+template <class C, bool kPlain, int kM, int kN, int kParts, class At>
 __device__ inline void finish_all(const Epilogue& e, const f32x4 (&acc)[kParts][kM][kN], At&& at) {
   using G = Groups<C, kM, kN>;
+  if constexpr (kPlain) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int q = 0; q < G::kCount; ++q) {
+        const uint64_t m = G::row(at(p).first, q), n = G::column(at(p).second, q);
+        float v[C::V];
+        G::sums(acc[p], q, v);
+        if (m < e.m && n < e.n)
+          store_upto<C>(e.y + (m * e.y_stride + n) * C::kElemBytes, v, e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
+      }
+    return;
+  }
   u32x4 bias[kParts][G::kPerRow], residual[kParts][G::kCount];
 #pragma unroll
   for (int p = 0; p < kParts; ++p) {
@@ -403,7 +417,9 @@ struct Feed {
   static constexpr int kChunks = kT * 8 / kThreads;
   static constexpr int kPerRow = kAlong ? 8 : kT / 8;  // chunks per LDS row
   static constexpr int e = C::kElemBytes;
-  const char* p[kChunks];
+  // kAlong: each chunk's address; kDown: the first one's, the others lie `apart`
+  const char* p[kAlong ? kChunks : 1];
+  uint64_t apart;
   uint64_t step;      // bytes between blocks
   uint64_t cols;      // kDown: columns from the tile's first on
   uint32_t left = 0;  // whole blocks not yet loaded
@@ -411,14 +427,19 @@ struct Feed {
   __device__ inline void init(const Operand& o, uint64_t first, uint64_t k) {
     step = kAlong ? 64 * e : 64 * o.stride * e;
     cols = kAlong ? 0 : o.cols - first;
+    apart = kThreads / kPerRow * o.stride * e;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
+    for (int i = 0; i < (kAlong ? kChunks : 1); ++i) {
       const int id = i * kThreads + threadIdx.x;
       const int r = id / kPerRow, c = id % kPerRow;
       uint64_t row = (kAlong ? first : k) + r;
       if (kAlong && row >= o.rows) row = o.rows - 1;
       p[i] = o.base + (row * o.stride + (kAlong ? k : first) + static_cast<uint64_t>(c) * 8) * e;
     }
+  }
+  __device__ inline const char* chunk(int i) const {
+    if constexpr (kAlong) return p[i];
+    return p[0] + i * apart;
   }
   // Whether all of the tile's columns exist.
   __device__ inline bool whole() const { return kAlong || cols >= kT; }
@@ -430,11 +451,11 @@ struct Feed {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, C::V);
+      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, C::V);
     const uint64_t by = left > 1 ? step : 0;
     if (left > 1) --left;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) p[i] += by;
+    for (int i = 0; i < (kAlong ? kChunks : 1); ++i) p[i] += by;
   }
 
   // The same for a block at k of which k_end - k may be less than 64, or
@@ -453,14 +474,14 @@ struct Feed {
         valid = k + r < k_end ? static_cast<int64_t>(cols) - c * 8 : 0;
       const int n = valid < 0 ? 0 : (valid > 8 ? 8 : static_cast<int>(valid));
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) fn(i, q, p[i] + q * 16, n - q * C::V);
+      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, n - q * C::V);
     }
   }
 };
 
 // Walks over the blocks of k of a tile: kDeep whole blocks' loads in flight,
-// then what is left one by one.  store(d) puts set d into an LDS buffer,
-// compute(d) multiplies it; kBuffers LDS buffers alternate.
+// then what is left one by one.  store(d, block) puts set d into the block's
+// LDS buffer, compute(block) multiplies it; kBuffers LDS buffers alternate.
 template <int kDeep, int kBuffers, class FA, class FB, class SA, class SB, class Store, class Compute>
 __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_t k_first, uint64_t k_end, FA& feed_a,
                             FB& feed_b, SA (&sa)[kDeep], SB (&sb)[kDeep], Store&& store, Compute&& compute) {
@@ -482,21 +503,21 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
     for (; block + kDeep <= blocks; block += kDeep) {
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
-        store(d);
+        store(d, block + d);
         __syncthreads();
         sa[d].load(feed_a);
         sb[d].load(feed_b);
         __builtin_amdgcn_sched_barrier(0);
-        compute(d);
+        compute(block + d);
         if constexpr (kBuffers == 1) __syncthreads();
       }
     }
 #pragma unroll
     for (int d = 0; d + 1 < kDeep; ++d) {
       if (block + d < blocks) {
-        store(d);
+        store(d, block + d);
         __syncthreads();
-        compute(d);
+        compute(block + d);
         if constexpr (kBuffers == 1) __syncthreads();
       }
     }
@@ -506,7 +527,7 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
     sa[0].load_edge(feed_a, t.a, m0, k, k_end);
     sb[0].load_edge(feed_b, t.b, n0, k, k_end);
     __syncthreads();
-    store(0);
+    store(0, 0);
     __syncthreads();
     compute(0);
   }
@@ -604,7 +625,6 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
   using SA = Stage<C, kAAlong, kBM, 256>;
   using SB = Stage<C, kBAlong, kBN, 256>;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
-  static_assert(kDeep % 2 == 0, "the LDS buffers alternate");
   const TileAt at(tile, t.tiles_m, t.tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * kBN;
   const int wave = threadIdx.x >> 6;
@@ -623,15 +643,15 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
   SB sb[kDeep];
   Feed<C, kAAlong, kBM, 256, 1> feed_a;
   Feed<C, kBAlong, kBN, 256, 1> feed_b;
-  auto buffer = [&](int d) { return lds + (d & 1) * (SA::kBytes + SB::kBytes); };
+  auto buffer = [&](uint32_t block) { return lds + (block & 1) * (SA::kBytes + SB::kBytes); };
   walk<kDeep, 2>(
       t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
-      [&](int d) {
-        sa[d].store(buffer(d));
-        sb[d].store(buffer(d) + SA::kBytes);
+      [&](int d, uint32_t block) {
+        sa[d].store(buffer(block));
+        sb[d].store(buffer(block) + SA::kBytes);
       },
-      [&](int d) {
-        const char* la = buffer(d);
+      [&](uint32_t block) {
+        const char* la = buffer(block);
         const char* lb = la + SA::kBytes;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -655,7 +675,7 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
       keep_partial<C>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
     }
   } else {
-    finish_all<C>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
+    finish_all<C, !(kAAlong && kBAlong)>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
   }
 }
 
@@ -856,7 +876,7 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   // workgroup's LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-  finish_all<C>(args.e, acc, [&](int p) {
+  finish_all<C, !(kAAlong && kBAlong)>(args.e, acc, [&](int p) {
     return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
   });
 }
@@ -962,11 +982,11 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
   Feed<F32, kBAlong, kBN, 256, 2> feed_b;
   walk<kDeep, 1>(
       t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
-      [&](int d) {
+      [&](int d, uint32_t) {
         sa[d].store(lds);
         sb[d].store(lds + SA::kBytes);
       },
-      [&](int) {
+      [&](uint32_t) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           u32x4 fb[3][kWN];
@@ -1025,7 +1045,7 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
       keep_partial<F32>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
     }
   } else {
-    finish_all<F32>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
+    finish_all<F32, !(kAAlong && kBAlong)>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
   }
 }
 
@@ -1045,7 +1065,8 @@ __device__ inline void any_tile(const TileArgs& t, uint32_t tile, uint32_t share
   if constexpr (C::kElemBytes == 4)
     split_body<kAAlong, kBAlong, kBM, kBN, 1>(t, tile, share, lds);
   else
-    tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 128 ? 2 : 4>(t, tile, share, lds);
+    // what the registers hold: 256 a lane, of which the larger tile's sums are 64
+    tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 64 ? 4 : (kAAlong && kBAlong ? 2 : 1)>(t, tile, share, lds);
 }
 
 // One product: all tiles of the first share of k, then of the next one.
