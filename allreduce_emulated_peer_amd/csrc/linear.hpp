@@ -9,10 +9,20 @@
 // elements is turned while it goes from LDS to registers.
 //
 // The products run on the matrix units: v_mfma_f32_16x16x32_{bf16,f16} for
-// the 16-bit types and v_mfma_f32_16x16x4_f32 for binary32.  The B tile is
-// given as the instruction's first operand, so a lane ends up with four
-// neighbouring columns n of one row m; v_permlane16_swap of two
+// the 16-bit types, and for binary32 too, whose values are split into three
+// bfloat16 parts (with few rows, where memory bounds, v_mfma_f32_16x16x4_f32).
+// The B tile is given as the instruction's first operand, so a lane ends up
+// with four neighbouring columns n of one row m; v_permlane16_swap of two
 // neighbouring tiles makes eight, one 16-byte store of a 16-bit type.
+//
+//   linear_big    256 x 256 tiles of large 16-bit products
+//   linear_tile   64 x 64, 128 x 64 and 128 x 128 tiles of all others, of any
+//                 size, stride and alignment, k split over workgroups where
+//                 the tiles are few (linear_join adds the shares)
+//   linear_pair   both gradients' tiles in one launch
+//   linear_few    up to 32 rows
+//   linear_slope  dz and the bias gradient's partial sums
+//   linear_pack   an operand laid out anew for linear_big
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -194,10 +204,10 @@ __device__ inline void with_activation(int act, Fn&& fn) {
   }
 }
 
-// What the epilogue adds to V neighbouring sums.  A wave fetches all of its
-// tiles' before it finishes the first one: fetched one by one, each would
+// What the epilogue adds to V neighbouring sums.  A wave fetches the residual of
+// many tiles before it finishes the first one: fetched one by one, each would
 // wait a memory latency behind the stores of the one before (8192 x 4096 x
-// 8192 fp16 with a residual: 482 us one by one, 421 us without residual).
+// 8192 fp16 with a residual: 482 us one by one, 441 us ahead).
 template <class C>
 __device__ inline u32x4 fetch_bias(const Epilogue& e, uint64_t n) {
   if (!e.bias || n >= e.n) return u32x4{0u, 0u, 0u, 0u};
@@ -210,31 +220,42 @@ __device__ inline u32x4 fetch_residual(const Epilogue& e, uint64_t m, uint64_t n
                       e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
 }
 
-// Finishes V neighbouring sums of row m from column n on, and stores them.
-template <class C, int kAct>
-__device__ inline void finish(const Epilogue& e, uint64_t m, uint64_t n, float* v, const u32x4& bias,
-                              const u32x4& residual) {
-  constexpr int V = C::V;
-  constexpr bool kFast = C::kElemBytes == 2;
-  if (m >= e.m || n >= e.n) return;
-  const int valid = e.n - n < V ? static_cast<int>(e.n - n) : V;
-  float t[V];
+// V neighbouring sums of row m from column n on: + bias, kept as z if wanted.
+template <class C>
+__device__ inline void keep_preact(const Epilogue& e, uint64_t m, uint64_t n, float* v, const u32x4& bias) {
   if (e.bias) {
+    float t[C::V];
     C::unpack(bias, t);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += t[i];
+    for (int i = 0; i < C::V; ++i) v[i] += t[i];
   }
-  if (e.z) store_upto<C>(e.z + (m * e.z_stride + n) * C::kElemBytes, v, valid);
-  if constexpr (kAct != MSCL_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = activate<kAct, kFast>(v[i]);
-  }
+  if (e.z && m < e.m && n < e.n)
+    store_upto<C>(e.z + (m * e.z_stride + n) * C::kElemBytes, v, e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
+}
+
+// V neighbouring activated values: + residual, stored as y.
+template <class C>
+__device__ inline void keep_result(const Epilogue& e, uint64_t m, uint64_t n, float* v, const u32x4& residual) {
   if (e.residual) {
+    float t[C::V];
     C::unpack(residual, t);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += t[i];
+    for (int i = 0; i < C::V; ++i) v[i] += t[i];
   }
-  store_upto<C>(e.y + (m * e.y_stride + n) * C::kElemBytes, v, valid);
+  if (m < e.m && n < e.n)
+    store_upto<C>(e.y + (m * e.y_stride + n) * C::kElemBytes, v, e.n - n < C::V ? static_cast<int>(e.n - n) : C::V);
+}
+
+// All three steps for one group.
+template <class C>
+__device__ inline void finish(const Epilogue& e, uint64_t m, uint64_t n, float* v) {
+  const u32x4 bias = fetch_bias<C>(e, n), residual = fetch_residual<C>(e, m, n);
+  keep_preact<C>(e, m, n, v, bias);
+  with_activation(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < C::V; ++i) v[i] = activate<decltype(act)::value, C::kElemBytes == 2>(v[i]);
+  });
+  keep_result<C>(e, m, n, v, residual);
 }
 
 // V neighbouring sums of one share of k.  Partial rows are padded to whole
@@ -321,10 +342,13 @@ __device__ inline void finish_all(const Epilogue& e, const f32x4 (&acc)[kParts][
     for (int p = 0; p < kParts; ++p)
 #pragma unroll
       for (int q = 0; q < G::kCount; ++q) {
+        const uint64_t m = G::row(at(p).first, q), n = G::column(at(p).second, q);
         float v[C::V];
         G::sums(acc[p], q, v);
-        finish<C, decltype(act)::value>(e, G::row(at(p).first, q), G::column(at(p).second, q), v,
-                                        bias[p][q % G::kPerRow], residual[p][q]);
+        keep_preact<C>(e, m, n, v, bias[p][q % G::kPerRow]);
+#pragma unroll
+        for (int c = 0; c < C::V; ++c) v[c] = activate<decltype(act)::value, C::kElemBytes == 2>(v[c]);
+        keep_result<C>(e, m, n, v, residual[p][q]);
       }
   });
 }
@@ -694,7 +718,10 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
 // workgroup starts the copy of the half that the phase before has finished
 // with.  So each half is on its way for seven phases (96 KiB in flight per
 // compute unit), every phase waits for all but the 12 newest copies and for
-// its own reads, and one barrier a phase orders both.
+// its own reads, and one barrier a phase orders both.  8192 x 8192 x 4096
+// bf16: 380 to 400 us (1370 to 1450 TFLOP/s, the same as the library's product
+// of these sizes); a wave's LDS reads take 75% of its MFMAs' time, and what is
+// left is the clock that the matrix units hold at this load.
 // The second block of a pair finds its first B half where the block before
 // read it to, so the two B register sets change roles from block to block.
 constexpr int kHalfBytes = 128 * 128;
@@ -752,7 +779,8 @@ struct Copier {
     }
   }
 
-  static constexpr uint32_t kNowhere = 0xf0000000u;
+  // past any range, and with any offset added still below 2^32
+  static constexpr uint32_t kNowhere = 0x80000000u;
 
   static __device__ inline __amdgpu_buffer_rsrc_t range(const char* from, uint64_t bytes) {
     const uint32_t n = bytes >> 31 ? 0x7fffffffu : static_cast<uint32_t>(bytes);
@@ -1123,8 +1151,7 @@ __device__ inline void join_shares(const Epilogue& e, int shares, uint64_t id) {
       for (int c = 0; c < 4; ++c) v[i + c] += q[c];
     }
   }
-  const u32x4 bias = fetch_bias<C>(e, n), residual = fetch_residual<C>(e, m, n);
-  with_activation(e.act, [&](auto act) { finish<C, decltype(act)::value>(e, m, n, v, bias, residual); });
+  finish<C>(e, m, n, v);
 }
 
 // Up to two products' shares: the first `groups` workgroups join a's.
@@ -1264,23 +1291,20 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
     __syncthreads();
   }
   constexpr int kGroups = 16 * kM * 16 * kN / V;
-  with_activation(t.e.act, [&](auto act) {
-    for (int id = threadIdx.x; id < kGroups; id += 512) {
-      const int m = id / (16 * kN / V), n = id % (16 * kN / V) * V;
-      float v[V];
+  for (int id = threadIdx.x; id < kGroups; id += 512) {
+    const int m = id / (16 * kN / V), n = id % (16 * kN / V) * V;
+    float v[V];
 #pragma unroll
-      for (int c = 0; c < V; ++c) v[c] = 0.0f;
+    for (int c = 0; c < V; ++c) v[c] = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
-      if (t.e.partial)
-        keep_partial<C>(t.e, blockIdx.y, m, n0 + n, v);
-      else
-        finish<C, decltype(act)::value>(t.e, m, n0 + n, v, fetch_bias<C>(t.e, n0 + n),
-                                        fetch_residual<C>(t.e, m, n0 + n));
-    }
-  });
+      for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
+    if (t.e.partial)
+      keep_partial<C>(t.e, blockIdx.y, m, n0 + n, v);
+    else
+      finish<C>(t.e, m, n0 + n, v);
+  }
 }
 
 // ------------------------------------------------------------------ operands laid out anew

@@ -308,14 +308,17 @@ mscl_status_t pack(Operand* o, char* to, hipStream_t stream) {
   return launched("linear_pack");
 }
 
-// More dynamic LDS than a kernel gets unasked.
+// More dynamic LDS than a kernel gets unasked, asked for once on each device.
 template <auto kKernel>
 hipError_t allow_lds(int bytes) {
-  static std::atomic<bool> done{false};
-  if (done.load(std::memory_order_acquire)) return hipSuccess;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.store(true, std::memory_order_release);
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << dev;  // current_device() has bounded it
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
 
