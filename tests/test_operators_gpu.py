@@ -189,6 +189,23 @@ def test_binary32_products_of_the_largest_and_smallest_values():
     assert not bool(y[[i for i in range(80) if i not in (3, 4, 5)]].any())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,k,n,form", [(1, 8200, 70, "plain"), (3, 4100, 200, "odd"), (9, 12289, 33, "columns"),
+                                        (17, 8192, 48, "plain"), (32, 5003, 130, "odd"), (12, 640, 8300, "plain"),
+                                        (32, 100, 8200, "columns")])
+def test_few_rows(dtype, m, k, n, form):
+    """Up to 32 rows: k split over workgroups and waves, ends of k inside a step, one and two tiles of rows."""
+    gen = torch.Generator().manual_seed(26)
+    x, w, b, r = linear_case(gen, m, k, n, DTYPES[dtype])
+    note("few rows", dtype, m, k, n, form)
+    args = [placed(v, form) for v in (x, w, b, r)]
+    y, z = M.linear_tensors(*args, "gelu_tanh", return_preact=True)
+    want = O.linear(x, w, b, r, "gelu_tanh")
+    O.assert_within(y, want[0], "y")
+    O.assert_within(z, want[1], "z")
+    assert torch.equal(y, M.linear_tensors(*args, "gelu_tanh"))
+
+
 def test_linear_many_leading_dimensions():
     gen = torch.Generator().manual_seed(13)
     x, w, b, _ = linear_case(gen, 30, 24, 40, torch.bfloat16)
@@ -379,6 +396,19 @@ def test_layer_norm(dtype, params, form):
             need = {f"need_{n}": k == only for k, n in enumerate(("dx", "dw", "db"))}
             one = M.layer_norm_backward_tensors(dyg, xg, mean, rstd, wg, **need)
             O.assert_within(one[only], want[only], f"{only} alone {rows}x{width}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_layer_norm_of_no_rows(dtype):
+    t = DTYPES[dtype]
+    note("layer norm of no rows", dtype)
+    for width in (5, 3000):
+        x = torch.empty(0, width, dtype=t, device="cuda")
+        w = torch.ones(width, dtype=t, device="cuda")
+        y, mean, rstd = M.layer_norm_tensors(x, w, w, return_stats=True)
+        assert y.shape == (0, width) and mean.shape == rstd.shape == (0,)
+        dx, dw, db = M.layer_norm_backward_tensors(x, x, mean, rstd, w)
+        assert dx.shape == (0, width) and dw.shape == db.shape == (width,) and not dw.any() and not db.any()
 
 
 def test_layer_norm_constant_rows_and_far_means():
