@@ -460,11 +460,12 @@ struct BackwardPlan {
 
 // Row groups of a pass that sums columns: enough workgroups for the device,
 // but at least 16 rows each, so that the partial sums stay a small part of
-// the traffic.
+// the traffic, and whole turns of 16 rows (4 waves with 4 rows in flight):
+// 17 rows take as long as 32.
 void plan_groups(uint64_t rows, uint64_t column_blocks, uint32_t* groups, uint32_t* rows_per_group) {
-  uint64_t want = std::max<uint64_t>(1, ceil_div(4 * kCus, std::max<uint64_t>(1, column_blocks)));
-  uint64_t per = std::max<uint64_t>(16, ceil_div(rows, want));
-  per = std::max(per, ceil_div(rows, 65535));
+  const uint64_t want = std::max<uint64_t>(1, ceil_div(4 * kCus, std::max<uint64_t>(1, column_blocks)));
+  uint64_t per = std::max<uint64_t>(16, ceil_div(rows, want) / 16 * 16);
+  per = std::max(per, round_up(ceil_div(rows, 65535), 16));
   *rows_per_group = static_cast<uint32_t>(std::min<uint64_t>(per, 0xffffffffu));
   *groups = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(rows, *rows_per_group)));
 }

@@ -308,11 +308,9 @@ def _need_torch():
     return _torch
 
 
-def _same_kind(like, **tensors):
-    """Checks shared by the operators' tensors: element type, device."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
+def _same_kind(like, name, t):
+    """Checks shared by an operator's tensors: element type, device."""
+    if t is not None:
         if t.device != like.device:
             raise ValueError(f"{name} must be on {like.device}")
         if t.dtype != like.dtype:
@@ -391,7 +389,9 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
         raise ValueError(f"unknown activation {activation!r}")
     if weight.dim() != 2:
         raise ValueError("weight must be a matrix")
-    _same_kind(x, weight=weight, bias=bias, residual=residual)
+    _same_kind(x, "weight", weight)
+    _same_kind(x, "bias", bias)
+    _same_kind(x, "residual", residual)
     if not x.is_cuda:
         raise ValueError("tensors must be on a GPU")
     n, k = weight.shape
@@ -444,7 +444,9 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
         raise ValueError("an activation's gradient needs preact")
     if activation == "none":
         preact = None
-    _same_kind(dy, x=x, weight=weight, preact=preact)
+    _same_kind(dy, "x", x)
+    _same_kind(dy, "weight", weight)
+    _same_kind(dy, "preact", preact)
     if not dy.is_cuda:
         raise ValueError("tensors must be on a GPU")
     n, k = weight.shape
@@ -477,19 +479,19 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
     return dx, dw, db
 
 
-def _param_code(like, **tensors):
-    """The parameters' type: that of the rows, or float32; None entries say nothing."""
-    kind = None
-    for name, t in tensors.items():
+def _param_type(like, weight, bias, width):
+    """The parameters' type: that of the rows, or float32; None says nothing."""
+    if weight is None and bias is None:
+        return like.dtype
+    kind = bias.dtype if weight is None else weight.dtype
+    if kind != like.dtype and kind != _torch.float32 or bias is not None and bias.dtype != kind:
+        raise ValueError(f"parameters must all be of {like.dtype} or all of float32")
+    for name, t in (("weight", weight), ("bias", bias)):
         if t is not None:
-            if kind is None:
-                kind = t.dtype
-            if t.dtype != kind or kind != like.dtype and kind != _torch.float32:
-                raise ValueError(f"parameters must all be of {like.dtype} or all of float32")
             if t.device != like.device:
                 raise ValueError(f"{name} must be on {like.device}")
-            _vector(name, t, like.shape[-1])
-    return kind or like.dtype
+            _vector(name, t, width)
+    return kind
 
 
 def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, stream=None):
@@ -503,12 +505,13 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     codes = _CODES
     if x.dtype not in codes:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    if x.dim() == 0 or x.shape[-1] == 0:
+    shape = x.shape
+    if not shape or shape[-1] == 0:
         raise ValueError("x must have a last dimension of at least 1")
     if not eps >= 0:
         raise ValueError("eps must be at least 0")
-    width = x.shape[-1]
-    param = codes[_param_code(x, weight=weight, bias=bias)]
+    width = shape[-1]
+    param = codes[_param_type(x, weight, bias, width)]
     if not x.is_cuda:
         raise ValueError("tensors must be on a GPU")
     xm = _matrix("x", x, width)
@@ -519,15 +522,17 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
         return _elsewhere(x.device, stream, (x, weight, bias),
                           lambda: layer_norm_tensors(x, weight, bias, eps, return_stats))
     y = torch.empty_like(xm) if xm.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
-    rstd = torch.empty_like(mean) if return_stats else None
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     call = LAYER_NORM.pack(xm.data_ptr(), xm.stride(0), _address(weight), _address(bias), y.data_ptr(), width,
                            _address(mean), _address(rstd), rows, width, eps, codes[x.dtype], param)
     status = lib.mscl_layer_norm(call, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_layer_norm")
-    if x.dim() != 2:
-        y = y.view(x.shape)
+    if xm is not x:
+        y = y.view(shape)
     return (y, mean, rstd) if return_stats else y
 
 
@@ -546,9 +551,9 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
         raise ValueError("dy must have a last dimension of at least 1")
     if x.shape != dy.shape:
         raise ValueError("dy and x must have the same shape")
-    _same_kind(dy, x=x)
+    _same_kind(dy, "x", x)
     width = dy.shape[-1]
-    kind = _param_code(dy, weight=weight)
+    kind = _param_type(dy, weight, None, width)
     if not dy.is_cuda:
         raise ValueError("tensors must be on a GPU")
     for name, t in (("mean", mean), ("rstd", rstd)):

@@ -135,6 +135,28 @@ def test_large_products(dtype, m, k, n, form):
             assert torch.equal(a, b2)
 
 
+def test_large_products_of_far_rows():
+    """Rows almost 2^22 elements apart, where offsets inside a tile come close to 31 bits, and k that ends inside a block."""
+    gen = torch.Generator().manual_seed(27)
+    far, m, k, n = 2 ** 22 - 8, 2304, 520, 4096
+    x, w, _, _ = linear_case(gen, m, k, n, torch.bfloat16)
+    note("large product of far rows: forward")
+    room = torch.empty((m - 1) * far + k, dtype=torch.bfloat16, device="cuda")
+    view = torch.as_strided(room, (m, k), (far, 1))
+    view.copy_(x)
+    c = [v.cuda() for v in (x, w)]
+    O.assert_within(M.linear_tensors(view, c[1]), O.linear(c[0], c[1], None, None, "none")[0], "y")
+    note("large product of far rows: input gradient")
+    dy, wt = normal(gen, m, k, dtype=torch.bfloat16).cuda(), normal(gen, k, n, dtype=torch.bfloat16).cuda()
+    del view
+    view = torch.as_strided(room, (k, n), (far, 1))
+    view.copy_(wt)
+    dx, _, _ = M.linear_backward_tensors(dy, torch.empty(m, n, dtype=torch.bfloat16, device="cuda"), view,
+                                         need_dw=False, need_db=False)
+    O.assert_within(dx, O.linear_backward(dy, torch.zeros(m, n, dtype=torch.bfloat16, device="cuda"), wt, None, "none")[0],
+                    "dx")
+
+
 def test_large_product_keeps_nan_in_its_row_and_column():
     gen = torch.Generator().manual_seed(19)
     m, k, n = 2100, 712, 4100
