@@ -738,7 +738,8 @@ struct BigArgs {
 // 16 bytes a lane from memory to LDS, lane l's to lds + 16 l; past the
 // resource's range zeros arrive.  The wait is the caller's (vmcnt).  The
 // compiler's own form of this instruction makes it wait for every copy under
-// way at the next LDS read.  Nothing else in these kernels uses m0.
+// way at the next LDS read.  The instruction writes no register, so a copy
+// under way cannot go over one, and nothing else in these kernels uses m0.
 __device__ inline void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t lds, uint32_t voffset, uint32_t soffset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voffset),
                "s"(from), "s"(soffset)
