@@ -736,13 +736,16 @@ struct BigArgs {
 };
 
 // 16 bytes a lane from memory to LDS, lane l's to lds + 16 l; past the
-// resource's range zeros arrive.  The wait is the caller's (vmcnt).  The
-// compiler's own form of this instruction makes it wait for every copy under
-// way at the next LDS read.  The instruction writes no register, so a copy
-// under way cannot go over one, and nothing else in these kernels uses m0.
-__device__ inline void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t lds, uint32_t voffset, uint32_t soffset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voffset),
-               "s"(from), "s"(soffset)
+// resource's range zeros arrive.  All of the offset is in `voffset`: that is
+// what the range check compares, while a scalar offset only lowers the range
+// it is compared with, which has no defined meaning once that offset exceeds
+// the range.  The wait is the caller's (vmcnt).  The compiler's own form of
+// this instruction makes it wait for every copy under way at the next LDS
+// read.  The instruction writes no register, so a copy under way cannot go
+// over one, and nothing else in these kernels uses m0.
+__device__ inline void copy_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t lds, uint32_t voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset),
+               "s"(from)
                : "memory");
 }
 
@@ -792,15 +795,15 @@ struct Copier {
     if constexpr (kAlong) {
       const __amdgpu_buffer_rsrc_t from = range(base, left);
       const uint32_t v = t + 1 < blocks ? voffset : (t + 1 == blocks ? last : kNowhere);
+      const uint32_t k = t < blocks ? t * 128 : 0;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        copy_to_lds(from, lds + (q * 8 + wave) * 1024, v, (h * 128 + q * 64) * stride + t * 128);
+      for (int q = 0; q < 2; ++q) copy_to_lds(from, lds + (q * 8 + wave) * 1024, v + (h * 128 + q * 64) * stride + k);
     } else {
       const uint64_t at = static_cast<uint64_t>(t) * (64 * stride);
       const __amdgpu_buffer_rsrc_t from = range(base + at, t < blocks ? left - at : 0);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        copy_to_lds(from, lds + (q * 8 + wave) * 1024, voffset, q * 32 * stride + h * 128 * e);
+        copy_to_lds(from, lds + (q * 8 + wave) * 1024, voffset + q * 32 * stride + h * 128 * e);
     }
   }
 };

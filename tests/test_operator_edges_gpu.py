@@ -1,0 +1,62 @@
+"""The operators on the GPU at the edges of their kernels' ranges, against their formulas in 64 bits."""
+
+import math
+import sys
+
+import pytest
+import torch
+
+import operator_oracle as O
+from allreduce_emulated_peer_amd import mscl as M
+
+pytestmark = pytest.mark.gpu
+DTYPES = O.DTYPES
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a visible GPU"
+    M.load()
+    yield
+
+
+def note(*what):
+    print("[gpu-case]", *what, file=sys.stderr, flush=True)
+
+
+def normal(gen, *shape, scale=1.0, dtype=torch.float32):
+    return (torch.randn(shape, generator=gen) * scale).to(dtype)
+
+
+def guarded(t, rows=256):
+    """t on the GPU with `rows` rows of NaN behind its last one."""
+    room = torch.full((t.shape[0] + rows, t.shape[1]), math.nan, dtype=t.dtype, device="cuda")
+    room[:t.shape[0]] = t.cuda()
+    return room[:t.shape[0]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [193, 320, 321, 337, 351, 352])
+def test_large_weight_gradient_whose_last_block_has_few_rows(dtype, rows):
+    """256 x 256 tiles, 64 rows at a time: rows of the last block that do not exist count as 0, whatever lies there."""
+    gen = torch.Generator().manual_seed(50)
+    t, k, n = DTYPES[dtype], 4096, 2056
+    dy, x = normal(gen, rows, n, dtype=t), normal(gen, rows, k, dtype=t)
+    w, z = normal(gen, n, k, scale=k ** -0.5, dtype=t), normal(gen, rows, n, scale=1.5, dtype=t)
+    for act in ("none", "silu"):
+        note("large weight gradient", dtype, rows, act)
+        got = M.linear_backward_tensors(guarded(dy), guarded(x), guarded(w), guarded(z), act)
+        want = O.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z.cuda(), act)
+        for g, e, name in zip(got, want, ("dx", "dw", "db")):
+            O.assert_within(g, e, f"{name} {act}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k,n", [(2049, 256, 4097), (2052, 328, 3848)])
+def test_large_product_whose_last_tiles_have_few_rows(dtype, m, k, n):
+    """Tile rows that do not exist are not read: what lies there is NaN, and reaches no result."""
+    gen = torch.Generator().manual_seed(51)
+    t = DTYPES[dtype]
+    x, w = normal(gen, m, k, dtype=t), normal(gen, n, k, scale=k ** -0.5, dtype=t)
+    note("large product, few rows in its last tiles", dtype, m, k, n)
+    O.assert_within(M.linear_tensors(guarded(x), guarded(w)), O.linear(x.cuda(), w.cuda(), None, None, "none")[0], "y")
