@@ -916,22 +916,31 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
 // ------------------------------------------------------------------ binary32 products
 
 // A binary32 value is the sum of three bfloat16 values: its nearest, the
-// nearest to what is left, and what is left then (8 bits each, so nothing of
-// the 24 is lost above bfloat16's smallest values).  Of the nine products of
-// two such sums the six largest are taken, on the bfloat16 matrix units; the
-// others are below 2^-26 of the product, less than one binary32 rounding of
-// it.  Six bfloat16 MFMAs take 96 cycles where the binary32 MFMAs of the same
-// 16 x 16 x 32 take 256.
-// Infinities and NaN have no such parts (inf - inf): they make the tile's sums
-// non-finite, and a tile with a non-finite sum is summed again in binary32.
+// nearest to what is left, and what is left then.  They hold all 24 bits as
+// long as the last of them is no smaller than bfloat16's smallest values, so
+// every operand is multiplied by 2^24 first: the last bit of any binary32
+// value, 2^-149 at least, is then 2^-125, a normal bfloat16.  (Unscaled, a
+// value of 2^-120 kept 14 bits.)  Of the nine products of two such sums the six
+// largest are taken, on the bfloat16 matrix units; the others are below 2^-26
+// of the product, less than one binary32 rounding of it.  Six bfloat16 MFMAs
+// take 96 cycles where the binary32 MFMAs of the same 16 x 16 x 32 take 256.
+// Infinities and NaN have no such parts (inf - inf), nor have values from
+// 2^104 on after their scaling: they make the tile's sums non-finite, as do
+// sums from 2^80 on, and a tile with a non-finite sum is summed again in
+// binary32, unscaled.
 struct Parts {
   u32x4 part[3];  // of eight values
 };
+
+constexpr float kSplitScale = 0x1p24f;  // of each operand
+constexpr float kSplitBack = 0x1p-48f;  // of their product
 
 __device__ inline Parts split(const u32x4& lo, const u32x4& hi) {
   float v[8];
   F32::unpack(lo, v);
   F32::unpack(hi, v + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= kSplitScale;
   Parts o;
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
@@ -1067,6 +1076,11 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
         for (int j = 0; j < kWN; ++j)
           acc[0][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[i], acc[0][i][j], 0, 0, 0);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int j = 0; j < kWN; ++j) acc[0][i][j] *= kSplitBack;
   }
   if (t.e.partial) {
     using G = Groups<F32, kWM, kWN>;

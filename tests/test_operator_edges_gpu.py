@@ -60,3 +60,27 @@ def test_large_product_whose_last_tiles_have_few_rows(dtype, m, k, n):
     x, w = normal(gen, m, k, dtype=t), normal(gen, n, k, scale=k ** -0.5, dtype=t)
     note("large product, few rows in its last tiles", dtype, m, k, n)
     O.assert_within(M.linear_tensors(guarded(x), guarded(w)), O.linear(x.cuda(), w.cuda(), None, None, "none")[0], "y")
+
+
+# x 2^low times random mantissas, w 2^high: ordinary results of operands at the bottom of binary32's range, where a
+# value's smaller parts leave bfloat16's range; and at its top, where the scaled parts do.
+@pytest.mark.parametrize("m,k,n", [(1, 300, 70), (32, 130, 90), (33, 130, 90), (300, 1030, 200)])
+@pytest.mark.parametrize("low,high", [(-111, 100), (-115, 100), (-120, 100), (-126, 100), (-135, 100), (-115, 0), (-126, 20),
+                                      (105, -100), (125, -120)])
+def test_binary32_products_at_the_ends_of_the_range(m, k, n, low, high):
+    gen = torch.Generator().manual_seed(52)
+
+    def values(size, *shape):
+        sign = torch.randint(0, 2, shape, generator=gen) * 2.0 - 1
+        return ((1 + torch.rand(shape, generator=gen, dtype=torch.float64)) * sign * 2.0 ** size).float()
+
+    x, w, dy = values(low, m, k), values(high, n, k), values(low, m, n)
+    note("binary32 ends", m, k, n, low, high)
+    c = [v.cuda() for v in (x, w, dy)]
+    O.assert_within(M.linear_tensors(c[0], c[1]), O.linear(c[0], c[1], None, None, "none")[0], "y")
+    dx, _, _ = M.linear_backward_tensors(c[2], c[0], c[1], need_dw=False, need_db=False)
+    O.assert_within(dx, O.linear_backward(c[2], c[0], c[1], None, "none")[0], "dx")
+    xw = values(high, m, k).cuda()  # dw of tiny dy and large x
+    _, dw, _ = M.linear_backward_tensors(c[2], xw, c[1], need_dx=False, need_db=False)
+    O.assert_within(dw, O.linear_backward(c[2], xw, c[1], None, "none")[1], "dw")
+    assert bool((dw != 0).all())
