@@ -916,14 +916,15 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
 // ------------------------------------------------------------------ binary32 products
 
 // A binary32 value is the sum of three bfloat16 values: its nearest, the
-// nearest to what is left, and what is left then.  They hold all 24 bits as
-// long as the last of them is no smaller than bfloat16's smallest values, so
-// every operand is multiplied by 2^24 first: the last bit of any binary32
-// value, 2^-149 at least, is then 2^-125, a normal bfloat16.  (Unscaled, a
-// value of 2^-120 kept 14 bits.)  Of the nine products of two such sums the six
-// largest are taken, on the bfloat16 matrix units; the others are below 2^-26
-// of the product, less than one binary32 rounding of it.  Six bfloat16 MFMAs
-// take 96 cycles where the binary32 MFMAs of the same 16 x 16 x 32 take 256.
+// nearest to what is left (at most 2^-8 of the value's leading power of two),
+// and what is left then (at most 2^-17).  They hold all 24 bits as long as the
+// last of them is no smaller than bfloat16's smallest values, so every operand
+// is multiplied by 2^24 first: the last bit of any binary32 value, 2^-149 at
+// least, is then 2^-125, a normal bfloat16.  (Unscaled, a value of 2^-120 kept
+// 14 bits.)  Of the nine products of two such sums the six largest are taken,
+// on the bfloat16 matrix units; the others are at most 2 * 2^-8 * 2^-17 + 2^-34
+// of the product, what rounding it to binary32 costs.  Six bfloat16 MFMAs take
+// 96 cycles where the binary32 MFMAs of the same 16 x 16 x 32 take 256.
 // Infinities and NaN have no such parts (inf - inf), nor have values from
 // 2^104 on after their scaling: they make the tile's sums non-finite, as do
 // sums from 2^80 on, and a tile with a non-finite sum is summed again in

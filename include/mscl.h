@@ -461,7 +461,7 @@ mscl_status_t mscl_channel_selftest(mscl_channel_t channel, uint32_t rounds, uin
  * activations are binary32 (whatever the element type) and each result is
  * rounded once, to nearest even; the one rounding inside an operator is
  * named at mscl_linear_backward.  Products of binary32 values may be formed
- * from parts of them, to within 2^-26 of each product.  Sums are added in an
+ * from parts of them, to within 2^-24 + 2^-34 of each product.  Sums are added in an
  * order fixed by the sizes and strides alone (no atomics): the same call
  * gives the same bits.
  * Infinities and NaN propagate as in the formulas, except that an activation

@@ -84,3 +84,12 @@ def test_binary32_products_at_the_ends_of_the_range(m, k, n, low, high):
     _, dw, _ = M.linear_backward_tensors(c[2], xw, c[1], need_dx=False, need_db=False)
     O.assert_within(dw, O.linear_backward(c[2], xw, c[1], None, "none")[1], "dw")
     assert bool((dw != 0).all())
+
+
+def test_binary32_products_of_the_largest_smaller_parts():
+    """One product each, of values whose bfloat16 parts leave out most: the stated bound, and the sums' and the result's roundings."""
+    v = torch.tensor([1 + 2.0 ** -8 - 2.0 ** -17 + i * 2.0 ** -23 for i in range(-40, 41)])
+    note("binary32 products of single values")
+    y = M.linear_tensors(v.view(-1, 1).cuda(), v.view(-1, 1).cuda()).cpu().double()
+    exact = v.double().view(-1, 1) @ v.double().view(1, -1)
+    assert float(((y - exact) / exact).abs().max()) <= 2.0 ** -24 + 2.0 ** -34 + 2 * O.U * (1 + 2.0 ** -6)
