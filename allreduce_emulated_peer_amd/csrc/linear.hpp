@@ -20,7 +20,8 @@
 //                 size, stride and alignment, k split over workgroups where
 //                 the tiles are few (linear_join adds the shares)
 //   linear_pair   both gradients' tiles in one launch
-//   linear_few    up to 32 rows
+//   linear_few    up to 32 rows, but for 17 and more of 16-bit types and 65281 or
+//                 more outputs, which linear_big takes
 //   linear_slope  dz and the bias gradient's partial sums
 //   linear_pack   an operand laid out anew for linear_big
 #pragma once

@@ -256,15 +256,35 @@ void choose_shares(ProductPlan* p, uint64_t m, uint64_t n, uint64_t k, uint64_t 
   if (p->shares > 1) p->partial_bytes = round_up(p->shares * m * p->partial_stride * 4, 256);
 }
 
+// Whether a forward product leaves more than half of the rows or columns of
+// its 256 x 256 tiles empty and is better off with other kernels.  What bounds
+// it is the pass over the long operand, so 256 tiles, one on each compute unit,
+// still do (k 8192, us: 17 x 65536 187 against 218 with few rows, 64 x 65536
+// 194 against 200 by small tiles, 65536 x 64 190 against 199), 128 do not (1 x
+// 32768 162 against 89, 32 x 49152 192 against 170, 64 x 32768 157 against 125,
+// 32768 x 64 161 against 126), and up to 16 rows linear_few is faster still (1
+// x 65536 189 against 173).  Input gradients gain nothing (64 x 32768 142
+// against 126, 64 x 49152 153 against 163).
+bool mostly_empty(bool forward, uint64_t m, uint64_t n, uint64_t tiles) {
+  return forward && (m <= 16 || (std::min(m, n) <= 128 && tiles < kCus));
+}
+
 ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool b_along, uint64_t m, uint64_t n,
                          uint64_t k, int dtype) {
   ProductPlan p;
   const uint64_t block = 128 / bytes_of(dtype);
   const uint64_t blocks = ceil_div(k, block);
-  if (dtype != MSCL_FLOAT32 && ceil_div(m, 256) * ceil_div(n, 256) >= kCus / 2 && blocks >= 4 && blocks < (1u << 24)) {
+  const uint64_t big_m = ceil_div(m, 256), big_n = ceil_div(n, 256);
+  if (dtype != MSCL_FLOAT32 && big_m * big_n >= kCus / 2 && blocks >= 4 && blocks < (1u << 24) &&
+      !mostly_empty(a_along && b_along, m, n, big_m * big_n)) {
     p.pack_a = !lies_well(a);
     p.pack_b = !lies_well(b);
-    if (within_reach(p.pack_a ? packed_stride(a.cols) : a.stride, a.cols, a_along) &&
+    // An operand is laid out anew only for at least 4 rows (columns) of tiles
+    // that use it (32768 outputs, k 4096, w at odd addresses, us: 512 rows 270
+    // against 210 by small tiles that take it as it lies, 768 279 against 267,
+    // 1024 294 against 354; k 8192, 1 row: 398 against 89 with few rows).
+    if ((!p.pack_a || big_n >= 4) && (!p.pack_b || big_m >= 4) &&
+        within_reach(p.pack_a ? packed_stride(a.cols) : a.stride, a.cols, a_along) &&
         within_reach(p.pack_b ? packed_stride(b.cols) : b.stride, b.cols, b_along)) {
       p.kind = ProductPlan::kBig;
       p.tile_m = p.tile_n = 256;

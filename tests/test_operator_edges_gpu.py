@@ -93,3 +93,23 @@ def test_binary32_products_of_the_largest_smaller_parts():
     y = M.linear_tensors(v.view(-1, 1).cuda(), v.view(-1, 1).cuda()).cpu().double()
     exact = v.double().view(-1, 1) @ v.double().view(1, -1)
     assert float(((y - exact) / exact).abs().max()) <= 2.0 ** -24 + 2.0 ** -34 + 2 * O.U * (1 + 2.0 ** -6)
+
+
+# A vocabulary's outputs, more than 128 tiles of 256 columns: from one token to more rows than a tile has.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("m", [1, 16, 17, 32, 33, 200, 513, 800])
+@pytest.mark.parametrize("n,offset", [(32776, 0), (32771, 3), (65536, 0), (65400, 3)])
+def test_many_outputs_of_few_rows(dtype, m, n, offset):
+    gen = torch.Generator().manual_seed(53)
+    t, k = DTYPES[dtype], 264
+    x, w = normal(gen, m, k, dtype=t), normal(gen, n, k, scale=k ** -0.5, dtype=t)
+    b, r = normal(gen, n, dtype=t), normal(gen, m, n, dtype=t)
+    room = torch.full((n, k + offset + 1), math.nan, dtype=t, device="cuda")
+    view = room[:, offset:offset + k] if offset else w.cuda()
+    view.copy_(w)
+    note("many outputs", dtype, m, n, offset)
+    y = M.linear_tensors(x.cuda(), view, b.cuda(), r.cuda(), "silu")
+    O.assert_within(y, O.linear(x.cuda(), w.cuda(), b.cuda(), r.cuda(), "silu")[0], "y")
+    # the mirrored product: many rows, few outputs
+    z = M.linear_tensors(view, x.cuda())
+    O.assert_within(z, O.linear(w.cuda(), x.cuda(), None, None, "none")[0], "many rows")
