@@ -222,7 +222,7 @@ struct ProductPlan {
 // Whether linear_big can take an operand as it lies: 16-byte chunks that are
 // aligned and whole, and offsets within a tile that fit 31 bits.
 bool lies_well(const Operand& o) {
-  return reinterpret_cast<uintptr_t>(o.base) % 16 == 0 && (o.rows <= 1 || o.stride % 8 == 0) && o.cols % 8 == 0;
+  return reinterpret_cast<uintptr_t>(o.base) % 16 == 0 && o.stride % 8 == 0 && o.cols % 8 == 0;
 }
 bool within_reach(uint64_t stride, uint64_t cols, bool along) {
   const uint64_t limit = uint64_t(1) << 30;  // elements of 2 bytes
@@ -461,8 +461,15 @@ mscl_status_t check_linear(const mscl_linear_t* c, Spans& s) {
   return s.check();
 }
 
-Operand x_of(const mscl_linear_t& c) { return Operand{bytes_at(c.x), c.x_stride, c.rows, c.in_features}; }
-Operand w_of(const mscl_linear_t& c) { return Operand{bytes_at(c.w), c.w_stride, c.out_features, c.in_features}; }
+// A matrix as a product takes it.  The stride of a single row means nothing to
+// the caller and anything may stand there, but the plans go by it and the
+// kernels' loads of rows past the end are placed by it.
+Operand operand(const void* p, uint64_t stride, uint64_t rows, uint64_t cols) {
+  return Operand{bytes_at(p), rows > 1 ? stride : cols, rows, cols};
+}
+
+Operand x_of(const mscl_linear_t& c) { return operand(c.x, c.x_stride, c.rows, c.in_features); }
+Operand w_of(const mscl_linear_t& c) { return operand(c.w, c.w_stride, c.out_features, c.in_features); }
 
 ProductPlan plan_linear(const mscl_linear_t& c) {
   return plan_product(x_of(c), true, w_of(c), true, c.rows, c.out_features, c.in_features, c.dtype);
@@ -495,9 +502,9 @@ BackwardPlan plan_linear_backward(const mscl_linear_backward_t& c) {
   const size_t e = bytes_of(c.dtype);
   p.slope = c.activation != MSCL_ACT_NONE && (c.dx || c.dw);
   size_t at = 0;
-  p.dz = Operand{bytes_at(c.dy), c.dy_stride, c.rows, c.out_features};
-  p.x = Operand{bytes_at(c.x), c.x_stride, c.rows, c.in_features};
-  p.w = Operand{bytes_at(c.w), c.w_stride, c.out_features, c.in_features};
+  p.dz = operand(c.dy, c.dy_stride, c.rows, c.out_features);
+  p.x = operand(c.x, c.x_stride, c.rows, c.in_features);
+  p.w = operand(c.w, c.w_stride, c.out_features, c.in_features);
   if (p.slope) {
     p.dz = Operand{nullptr, packed_stride(c.out_features), c.rows, round_up(c.out_features, 16 / e)};
     p.dz_at = at;

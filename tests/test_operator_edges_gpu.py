@@ -113,3 +113,17 @@ def test_many_outputs_of_few_rows(dtype, m, n, offset):
     # the mirrored product: many rows, few outputs
     z = M.linear_tensors(view, x.cuda())
     O.assert_within(z, O.linear(w.cuda(), x.cuda(), None, None, "none")[0], "many rows")
+
+
+@pytest.mark.parametrize("stride", [1, 3, 1 << 40])
+def test_the_stride_of_a_single_row_is_ignored(stride):
+    gen = torch.Generator().manual_seed(54)
+    t = torch.bfloat16
+    note("stride of a single row", stride)
+    dy, w, x = normal(gen, 1, 264, dtype=t).cuda(), normal(gen, 264, 32776, dtype=t).cuda(), normal(gen, 1, 32776, dtype=t).cuda()
+    got = M.linear_backward_tensors(torch.as_strided(dy, (1, 264), (stride, 1)), torch.as_strided(x, (1, 32776), (stride, 1)), w)
+    for g, e, name in zip(got, O.linear_backward(dy, x, w, None, "none"), ("dx", "dw", "db")):
+        O.assert_within(g, e, name)
+    many, one = normal(gen, 66000, 264, dtype=t).cuda(), normal(gen, 1, 264, dtype=t).cuda()
+    y = M.linear_tensors(many, torch.as_strided(one, (1, 264), (stride, 1)))
+    O.assert_within(y, O.linear(many, one, None, None, "none")[0], "y")
