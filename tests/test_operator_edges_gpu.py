@@ -127,3 +127,57 @@ def test_the_stride_of_a_single_row_is_ignored(stride):
     many, one = normal(gen, 66000, 264, dtype=t).cuda(), normal(gen, 1, 264, dtype=t).cuda()
     y = M.linear_tensors(many, torch.as_strided(one, (1, 264), (stride, 1)))
     O.assert_within(y, O.linear(many, one, None, None, "none")[0], "y")
+
+
+def in_64_bits(z, act):
+    """An activation and its slope; gelu_tanh by (1 + tanh u) / 2 = sigmoid(2 u), which does not cancel in the tail."""
+    if act != "gelu_tanh":
+        return O.activate(z, act), O.slope(z, act)
+    a = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    da = 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    return z * torch.sigmoid(a), torch.sigmoid(a) + z * torch.sigmoid(a) * torch.sigmoid(-a) * da
+
+
+def relative_error(z, act, fast):
+    """Of an activation (and of its slope's terms): some ten operations, exp's argument, and the fast forms' tail."""
+    if act == "gelu_tanh":
+        return (10 + 6 * (2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)).abs()) * O.U
+    if act == "silu":
+        return (10 + 2 * z.abs()) * O.U
+    return (10 + 2 * z * z) * O.U + (1.2e-5 if fast else 0.0)
+
+
+def slope_terms(z, act):
+    """The sizes of what the slope is a sum of, and what 1 - (a value near 1) is off by in it."""
+    if act == "gelu":
+        return 0.5 * torch.special.erfc(-z * math.sqrt(0.5)) + z.abs() * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi), 0.0
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return s + (z * s * (1 - s)).abs(), 2 * O.U * z.abs() * s
+    du = math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    s = torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+    return s + (2 * z * s * (1 - s) * du).abs(), 4 * O.U * (z * s * du).abs()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_keep_their_relative_accuracy(dtype, act):
+    """Down the negative tail, where results are small, as elsewhere: to the rounding of the result and of exp's argument."""
+    t = DTYPES[dtype]
+    z = torch.cat([torch.linspace(-12, -4, 2048), torch.linspace(-4, 4, 1024), torch.linspace(4, 12, 512),
+                   torch.linspace(-0.01, 0.01, 512)]).to(t).reshape(64, 64)
+    eye, ones = torch.eye(64, dtype=t).cuda(), torch.ones(64, 64, dtype=t).cuda()
+    note("relative accuracy", dtype, act)
+    y, kept = M.linear_tensors(z.cuda(), eye, activation=act, return_preact=True)
+    assert torch.equal(kept.cpu(), z)  # the product with the identity is exact
+    v = z.double()
+    rel = relative_error(v, act, dtype != "fp32")
+    least = torch.finfo(torch.float32).smallest_normal  # a sigmoid or tail below it may be 0
+    floor = 16 * least  # times z
+    want, steep = in_64_bits(v, act)
+    O.assert_within(y, (want, O.rounded(want, rel * want.abs() + floor, t)), f"{act}")
+    dx, _, _ = M.linear_backward_tensors(ones, eye, eye, z.cuda(), act)
+    terms, near = slope_terms(v, act)
+    if act == "gelu_tanh":  # the slope has 2 z u' times the sigmoid
+        floor = least * (1 + 2 * math.sqrt(2 / math.pi) * v.abs() * (1 + 3 * 0.044715 * v * v))
+    O.assert_within(dx, (steep, O.rounded(steep, rel * terms + near + floor, t)), f"slope of {act}")
