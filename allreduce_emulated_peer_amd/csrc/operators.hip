@@ -37,10 +37,28 @@ bool known_dtype(int d) { return d == MSCL_FLOAT32 || d == MSCL_FLOAT16 || d == 
 // writes it, and the buffer that it may be exactly the same as.
 struct Span {
   const char* name;
-  uintptr_t first, bytes;
+  uintptr_t first, bytes;       // from its first byte to its last one
+  uintptr_t rows, pitch, width; // rows of `width` bytes, `pitch` bytes apart
   bool written;
   const char* may_be;
 };
+
+// Whether two buffers share a byte.  Column blocks of one larger matrix (rows
+// equally far apart) and a single row between a matrix's rows are told apart
+// exactly; matrices of different pitches share bytes if their extents do.
+bool meet(const Span& p, const Span& q) {
+  const Span &a = p.first <= q.first ? p : q, &b = p.first <= q.first ? q : p;
+  const uintptr_t d = b.first - a.first;
+  if (d >= a.bytes) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+  if (a.rows == 1 && b.rows == 1) return true;
+  // b's row 0 starts `r` bytes behind the start of a's row `row`, or where that
+  // row would be; all of b's rows lie so to some row of a
+  const uintptr_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  const uintptr_t row = d / pitch, r = d % pitch;
+  if (d - std::min(row, a.rows - 1) * pitch < a.width) return true;
+  return row + 1 < a.rows && pitch - r < b.width;
+}
 
 struct Spans {
   Span s[12];
@@ -85,7 +103,7 @@ struct Spans {
       status = bad(text);
       return;
     }
-    s[n++] = Span{name, a, bytes, written, may_be};
+    s[n++] = Span{name, a, bytes, rows, stride * e, cols * e, written, may_be};
   }
 
   mscl_status_t check() const {
@@ -98,7 +116,7 @@ struct Spans {
   mscl_status_t check_last(int i) const {
     for (int j = 0; j < i; ++j) {
       if (!s[i].written && !s[j].written) continue;
-      if (s[i].first >= s[j].first + s[j].bytes || s[j].first >= s[i].first + s[i].bytes) continue;
+      if (!meet(s[i], s[j])) continue;
       const bool same = s[i].first == s[j].first && s[i].bytes == s[j].bytes;
       const bool allowed = (s[i].may_be && !strcmp(s[i].may_be, s[j].name)) ||
                            (s[j].may_be && !strcmp(s[j].may_be, s[i].name));

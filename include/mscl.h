@@ -473,7 +473,9 @@ mscl_status_t mscl_channel_selftest(mscl_channel_t channel, uint32_t rounds, uin
  * that the operator's *_workspace function gives for the same call (16-byte
  * aligned; NULL when that is 0); it is used until the call has finished on
  * the stream and holds nothing between calls.  Outputs must not overlap
- * inputs, each other or the workspace, except where said.
+ * inputs, each other or the workspace, except where said.  Column blocks of
+ * one larger matrix do not overlap: matrices of the same stride (or of one
+ * row) may interleave.  Matrices of different strides must lie apart.
  * Errors of all of them: INVALID_ARGUMENT (a null pointer that is needed, a
  * stride shorter than its row, an overlap, an unknown dtype or activation,
  * sizes that overflow, a workspace that is too small), MISALIGNED,

@@ -181,3 +181,61 @@ def test_activations_keep_their_relative_accuracy(dtype, act):
     if act == "gelu_tanh":  # the slope has 2 z u' times the sigmoid
         floor = least * (1 + 2 * math.sqrt(2 / math.pi) * v.abs() * (1 + 3 * 0.044715 * v * v))
     O.assert_within(dx, (steep, O.rounded(steep, rel * terms + near + floor, t)), f"slope of {act}")
+
+
+CODES = {"bf16": M.BFLOAT16, "fp16": M.FLOAT16, "fp32": M.FLOAT32}
+
+
+@pytest.mark.parametrize("dtype,m,k,n", [("bf16", 20, 72, 90), ("fp32", 70, 130, 45), ("fp16", 300, 256, 264),
+                                         ("bf16", 2100, 264, 4100)])
+def test_outputs_as_column_blocks_of_one_matrix(dtype, m, k, n):
+    """Through the C ABI: residual, y and preact side by side; dy, x and dx side by side; a norm's y beside its x."""
+    gen = torch.Generator().manual_seed(55)
+    t, lib, stream = DTYPES[dtype], M.load(), torch.cuda.current_stream().cuda_stream
+    x, w = normal(gen, m, k, dtype=t).cuda(), normal(gen, n, k, scale=k ** -0.5, dtype=t).cuda()
+    r, b = normal(gen, m, n, dtype=t).cuda(), normal(gen, n, dtype=t).cuda()
+    note("column blocks", dtype, m, k, n)
+
+    def run(query, entry, call):
+        space, size = M._workspace(query, call, x)
+        M._check(entry(call, M._address(space), size, stream), "column blocks")
+        torch.cuda.synchronize()
+
+    wide = 3 * n + 5
+    room = torch.full((m, wide), 77.0, dtype=t, device="cuda")
+    room[:, 1:1 + n] = r
+    y, z = room[:, 2 + n:2 + 2 * n], room[:, 3 + 2 * n:3 + 3 * n]
+    run(lib.mscl_linear_workspace, lib.mscl_linear,
+        M.LINEAR.pack(x.data_ptr(), k, w.data_ptr(), k, b.data_ptr(), room[:, 1:].data_ptr(), wide, y.data_ptr(), wide,
+                      z.data_ptr(), wide, m, k, n, CODES[dtype], M.ACT_SILU))
+    want = O.linear(x, w, b, r, "silu")
+    O.assert_within(y, want[0], "y")
+    O.assert_within(z, want[1], "preact")
+    assert torch.equal(room[:, 1:1 + n], r)
+    for column in (0, 1 + n, 2 + 2 * n, 3 + 3 * n, 4 + 3 * n):
+        assert bool((room[:, column] == 77).all())
+
+    wide = n + 2 * k + 4
+    room = torch.full((m, wide), 55.0, dtype=t, device="cuda")
+    dy = room[:, 1:1 + n].copy_(r)
+    xs = room[:, 2 + n:2 + n + k].copy_(x)
+    dx = room[:, 3 + n + k:3 + n + 2 * k]
+    dw, db = torch.empty(n, k, dtype=t, device="cuda"), torch.empty(n, dtype=t, device="cuda")
+    run(lib.mscl_linear_backward_workspace, lib.mscl_linear_backward,
+        M.LINEAR_BACKWARD.pack(dy.data_ptr(), wide, xs.data_ptr(), wide, w.data_ptr(), k, 0, 0, dx.data_ptr(), wide,
+                               dw.data_ptr(), k, db.data_ptr(), m, k, n, CODES[dtype], M.ACT_NONE))
+    for g, e, name in zip((dx, dw, db), O.linear_backward(r, x, w, None, "none"), ("dx", "dw", "db")):
+        O.assert_within(g, e, name)
+    assert torch.equal(dy, r) and torch.equal(xs, x)
+    for column in (0, 1 + n, 2 + n + k, 3 + n + 2 * k):
+        assert bool((room[:, column] == 55).all())
+
+    wide = 2 * k + 3
+    room = torch.full((m, wide), 33.0, dtype=t, device="cuda")
+    xs, y = room[:, 1:1 + k].copy_(x), room[:, 2 + k:2 + 2 * k]
+    M._check(lib.mscl_layer_norm(M.LAYER_NORM.pack(xs.data_ptr(), wide, 0, 0, y.data_ptr(), wide, 0, 0, m, k, 1e-5,
+                                                   CODES[dtype], CODES[dtype]), stream), "norm")
+    O.assert_within(y, O.layer_norm(x, None, None, 1e-5)[0], "norm")
+    assert torch.equal(xs, x)
+    for column in (0, 1 + k, 2 + 2 * k):
+        assert bool((room[:, column] == 33).all())
