@@ -293,12 +293,28 @@ def allreduce_tensors(inputs, outputs, algo: int = ALGO_AUTO, stream=None) -> No
 _torch = None
 _CODES = {}  # torch dtype -> element type code
 _raw_stream = None
+_outside_autograd = None
 
 
 def _need_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _outside_autograd
     if _torch is None:
         import torch
+
+        class OutsideAutograd(torch.autograd.Function):
+            """call(), which autograd knows no gradient of: a backward pass through its results raises."""
+
+            @staticmethod
+            def forward(ctx, call, name, *inputs):
+                ctx.name = name
+                return call()
+
+            @staticmethod
+            def backward(ctx, *grads):
+                raise RuntimeError(f"{ctx.name}_tensors is not part of autograd's graph: run {ctx.name}_backward_tensors, and "
+                                   "call it under torch.no_grad() or detach what it takes or returns")
+
+        _outside_autograd = OutsideAutograd.apply
 
         _CODES.update({torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16})
         # the current stream's handle without a Stream object around it (2 us less), where torch has that
@@ -379,7 +395,9 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
     one dtype (float32 / float16 / bfloat16) and device; rows may be strided,
     elements of a row must be contiguous.  activation is a name of
     ACTIVATION_CODES.  Returns y (..., out), or (y, preact) with return_preact:
-    what linear_backward_tensors needs where there is an activation.
+    what linear_backward_tensors needs where there is an activation.  Autograd
+    does not reach through it: where an input requires a gradient, so do the
+    results, and a backward pass through them raises.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
     dtype = _CODES.get(x.dtype)
@@ -409,6 +427,10 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(x.device, stream, (x, weight, bias, residual),
                           lambda: linear_tensors(x, weight, bias, residual, activation, return_preact))
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or bias is not None and bias.requires_grad
+                                    or residual is not None and residual.requires_grad):
+        return _outside_autograd(lambda: linear_tensors(x, weight, bias, residual, activation, return_preact), "linear",
+                                 x, weight, bias, residual)
     y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
     z = torch.empty_like(y) if return_preact else None
     call = LINEAR.pack(xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), _address(bias), _address(rm),
@@ -499,7 +521,8 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
 
     weight and bias have x's dtype or float32.  Returns y, or (y, mean, rstd)
     with return_stats: float32 of x's leading shape, what
-    layer_norm_backward_tensors needs.
+    layer_norm_backward_tensors needs.  Autograd does not reach through it, as
+    through linear_tensors.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
     codes = _CODES
@@ -521,6 +544,10 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(x.device, stream, (x, weight, bias),
                           lambda: layer_norm_tensors(x, weight, bias, eps, return_stats))
+    if torch.is_grad_enabled() and (x.requires_grad or weight is not None and weight.requires_grad
+                                    or bias is not None and bias.requires_grad):
+        return _outside_autograd(lambda: layer_norm_tensors(x, weight, bias, eps, return_stats), "layer_norm", x, weight,
+                                 bias)
     y = torch.empty_like(xm) if xm.is_contiguous() else torch.empty((rows, width), dtype=x.dtype, device=x.device)
     mean = rstd = None
     if return_stats:

@@ -239,3 +239,51 @@ def test_outputs_as_column_blocks_of_one_matrix(dtype, m, k, n):
     assert torch.equal(xs, x)
     for column in (0, 1 + k, 2 + 2 * k):
         assert bool((room[:, column] == 33).all())
+
+
+def test_a_gradient_is_not_lost_unseen():
+    """Autograd does not reach through the operators: a backward pass that would need it raises."""
+    gen = torch.Generator().manual_seed(56)
+    x, w, b = normal(gen, 6, 40).cuda(), normal(gen, 24, 40).cuda(), normal(gen, 24).cuda()
+    g, head = normal(gen, 24).cuda(), normal(gen, 24).cuda().requires_grad_()
+    note("autograd")
+    y, z = M.linear_tensors(x, w, b, None, "gelu", return_preact=True)
+    n, mean, rstd = M.layer_norm_tensors(y, g, return_stats=True)
+    assert not any(t.requires_grad for t in (y, z, n, mean, rstd))
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        for which in range(4):
+            args = [t.clone().requires_grad_(i == which) for i, t in enumerate((x, w, b, y))]
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            got = M.linear_tensors(*args, "gelu", return_preact=True, stream=stream)
+            with torch.no_grad():
+                want = M.linear_tensors(*args, "gelu", return_preact=True)
+            torch.cuda.synchronize()
+            for a, e in zip(got, want):
+                assert torch.equal(a, e) and a.requires_grad and not e.requires_grad
+            for loss in ((got[0] * head).sum(), (got[1] * head).sum()):
+                with pytest.raises(RuntimeError, match="linear_backward_tensors"):
+                    loss.backward()
+        for which in range(3):
+            args = [t.clone().requires_grad_(i == which) for i, t in enumerate((y, g, b))]
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            got = M.layer_norm_tensors(*args, return_stats=True, stream=stream)
+            with torch.no_grad():
+                want = M.layer_norm_tensors(*args, return_stats=True)
+            torch.cuda.synchronize()
+            for a, e in zip(got, want):
+                assert torch.equal(a, e) and a.requires_grad and not e.requires_grad
+            with pytest.raises(RuntimeError, match="layer_norm_backward_tensors"):
+                (got[0] * head).sum().backward()
+    # what only a head on top needs goes through, as does a result that is changed in place
+    h = M.linear_tensors(x.clone().requires_grad_(), w)
+    h.mul_(2)
+    head.grad = None  # the passes that raised had reached it
+    (h.detach() * head).sum().backward()
+    assert torch.allclose(head.grad, h.detach().sum(0))
+    # the gradients' functions run by hand on parameters, outside of any graph
+    p = w.clone().requires_grad_()
+    for t in M.linear_backward_tensors(torch.ones_like(y), x, p, z, "gelu"):
+        assert not t.requires_grad
