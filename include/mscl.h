@@ -461,9 +461,10 @@ mscl_status_t mscl_channel_selftest(mscl_channel_t channel, uint32_t rounds, uin
  * activations are binary32 (whatever the element type) and each result is
  * rounded once, to nearest even; the one rounding inside an operator is
  * named at mscl_linear_backward.  Products of binary32 values may be formed
- * from parts of them, to within 2^-24 + 2^-34 of each product.  Sums are added in an
- * order fixed by the sizes and strides alone (no atomics): the same call
- * gives the same bits.
+ * from parts of them, to within 2^-24 + 2^-34 of each product.  Sums are
+ * added in an order fixed by the sizes, the strides and the pointers'
+ * alignment (no atomics): the same call gives the same bits, as does one on
+ * copies of its buffers that lie equally to 16-byte boundaries.
  * Infinities and NaN propagate as in the formulas, except that an activation
  * (and its slope) at -infinity is its limit.
  *

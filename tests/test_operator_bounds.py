@@ -1,5 +1,7 @@
 """What the operators' contract says about their arithmetic, in 64 bits on the CPU."""
 
+import os
+
 import torch
 
 
@@ -43,10 +45,15 @@ def test_products_of_parts_stay_within_the_stated_bound():
     assert float(left_out(worst, worst).max()) > 0.98 * 2.0 ** -24
 
 
-def test_the_header_states_that_bound():
-    import os
-
+def header():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     with open(os.path.join(root, "include", "mscl.h")) as f:
-        text = " ".join(f.read().replace("*", " ").split())
-    assert "to within 2^-24 + 2^-34 of each product" in text
+        return " ".join(f.read().replace("*", " ").split())
+
+
+def test_the_header_states_that_bound():
+    assert "to within 2^-24 + 2^-34 of each product" in header()
+
+
+def test_the_header_names_what_fixes_the_order_of_sums():
+    assert "order fixed by the sizes, the strides and the pointers' alignment" in header()

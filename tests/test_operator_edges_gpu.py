@@ -287,3 +287,30 @@ def test_a_gradient_is_not_lost_unseen():
     p = w.clone().requires_grad_()
     for t in M.linear_backward_tensors(torch.ones_like(y), x, p, z, "gelu"):
         assert not t.requires_grad
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_copies_that_lie_equally_give_the_same_bits(dtype):
+    """The order of sums may go by the pointers' place between 16-byte boundaries, and by nothing else of an address."""
+    gen = torch.Generator().manual_seed(57)
+    t, rows, width, out = DTYPES[dtype], 40, 1003, 130
+    x, w, dy = normal(gen, rows, width, dtype=t), normal(gen, out, width, dtype=t), normal(gen, rows, out, dtype=t)
+    step = 16 // x.element_size()
+    note("equally placed copies", dtype)
+    for shift in range(0, step, 3):
+        seen = None
+        for far in (0, 5, 64):  # 16-byte steps
+            def at(v):
+                room = torch.full((shift + step * far + v.numel() + step,), math.nan, dtype=t, device="cuda")
+                view = room[shift + step * far:shift + step * far + v.numel()].view(v.shape)
+                return view.copy_(v)
+
+            a = [at(v) for v in (x, w, dy)]
+            y, mean, rstd = M.layer_norm_tensors(a[0], return_stats=True)
+            got = [y, mean, rstd, M.linear_tensors(a[0], a[1]), *M.linear_backward_tensors(a[2], a[0], a[1]),
+                   *M.layer_norm_backward_tensors(a[0], a[0], mean, rstd)]
+            seen = seen or got
+            for g, e in zip(got, seen):
+                assert torch.equal(g, e)
+        for g, e, name in zip(got, O.layer_norm(x, None, None, 1e-5), ("y", "mean", "rstd")):
+            O.assert_within(g, e, name)
