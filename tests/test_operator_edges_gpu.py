@@ -1,6 +1,8 @@
 """The operators on the GPU at the edges of their kernels' ranges, against their formulas in 64 bits."""
 
 import math
+import os
+import subprocess
 import sys
 
 import pytest
@@ -314,3 +316,67 @@ def test_copies_that_lie_equally_give_the_same_bits(dtype):
                 assert torch.equal(g, e)
         for g, e, name in zip(got, O.layer_norm(x, None, None, 1e-5), ("y", "mean", "rstd")):
             O.assert_within(g, e, name)
+
+
+def large_layer(x, w, b, r, dy, z):
+    y, kept = M.linear_tensors(x, w, b, r, "gelu", return_preact=True)
+    return (y, kept) + M.linear_backward_tensors(dy, x, w, z, "silu")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k,n,odd", [(2304, 4096, 4096, False), (2300, 4099, 3907, True)])
+def test_graph_replays_of_large_products(dtype, m, k, n, odd):
+    """256 x 256 tiles, and operands laid out anew, captured; eager work and synchronizations between the replays."""
+    gen = torch.Generator().manual_seed(58)
+    t = DTYPES[dtype]
+    note("graph of large products", dtype, m, k, n, odd)
+    args = [v.cuda() for v in (normal(gen, m, k, dtype=t), normal(gen, n, k, scale=k ** -0.5, dtype=t), normal(gen, n, dtype=t),
+                               normal(gen, m, n, dtype=t), normal(gen, m, n, dtype=t), normal(gen, m, n, dtype=t))]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        large_layer(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = large_layer(*args)
+    for replay in range(4):
+        for i in (0, 4):
+            args[i].copy_(normal(gen, *args[i].shape, dtype=t))
+        graph.replay()
+        got = [o.clone() for o in out]
+        torch.cuda.synchronize()
+        for a, b in zip(got, large_layer(*args)):
+            assert torch.equal(a, b), f"replay {replay}"
+
+
+FIRST_CALL = """
+import torch
+from allreduce_emulated_peer_amd import mscl as M
+x, w = torch.randn(2304, 520, device="cuda").bfloat16(), torch.randn(4099, 520, device="cuda").bfloat16()
+dy = torch.randn(2304, 4099, device="cuda").bfloat16()
+f = torch.randn(200, 300, device="cuda")
+def layer():
+    return (M.linear_tensors(x, w), *M.linear_backward_tensors(dy, x, w), M.linear_tensors(f, f),
+            *M.linear_backward_tensors(f[:, :200].contiguous(), f, f), *M.layer_norm_tensors(x, return_stats=True))
+M.load()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = layer()
+for _ in range(3):
+    x.copy_(torch.randn(2304, 520, device="cuda"))
+    graph.replay()
+    got = [o.clone() for o in out]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, layer()))
+print("replays equal")
+"""
+
+
+def test_the_first_call_of_a_process_can_be_captured():
+    """Whatever is looked up or set once for a device is no work on a stream."""
+    note("first call captured, in a child process")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=110, cwd=root)
+    assert done.returncode == 0 and done.stdout.strip().endswith("replays equal"), done.stdout + done.stderr
