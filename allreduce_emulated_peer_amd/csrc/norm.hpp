@@ -398,7 +398,7 @@ struct TileRows {
     for (int q = 0; q < kTileRows; ++q)
       if (row0 + 4 * q >= end) {
         mean[q] = rstd[q] = 0.0f;
-        dy[q] = u32x4{0u, 0u, 0u, 0u};
+        x[q] = dy[q] = u32x4{0u, 0u, 0u, 0u};  // x too: 0 times an infinity there would be NaN
       }
   }
 };

@@ -380,3 +380,25 @@ def test_the_first_call_of_a_process_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=110, cwd=root)
     assert done.returncode == 0 and done.stdout.strip().endswith("replays equal"), done.stdout + done.stderr
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,width", [(5, 40), (21, 600), (300, 9000), (2100, 96)])
+def test_an_infinite_input_counts_once_in_the_weight_gradient(dtype, rows, width):
+    """With finite statistics, as the formula has it: infinite in its column and nowhere else."""
+    gen = torch.Generator().manual_seed(59)
+    t = DTYPES[dtype]
+    x, dy = normal(gen, rows, width, dtype=t), normal(gen, rows, width, dtype=t)
+    x[rows - 1, 7], x[rows // 2, 30] = math.inf, -math.inf
+    dy[rows - 1, 7], dy[rows // 2, 30] = 2, 3
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    note("infinite input", dtype, rows, width)
+    for need_dx in (True, False):
+        _, dw, db = M.layer_norm_backward_tensors(dy.cuda(), x.cuda(), mean, rstd, need_dx=need_dx)
+        assert dw[7] == math.inf and dw[30] == -math.inf
+        keep = [i for i in range(width) if i not in (7, 30)]
+        clean = x.clone()
+        clean[rows - 1, 7] = clean[rows // 2, 30] = 0
+        _, want_dw, want_db = O.layer_norm_backward(dy, clean, mean.cpu(), rstd.cpu(), None, t)
+        O.assert_within(dw.cpu()[keep], (want_dw[0][keep], want_dw[1][keep]), "dw")
+        O.assert_within(db, want_db, "db")
