@@ -727,9 +727,11 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
 // with.  So each half is on its way for seven phases (96 KiB in flight per
 // compute unit), every phase waits for all but the 12 newest copies and for
 // its own reads, and one barrier a phase orders both.  8192 x 8192 x 4096
-// bf16: 380 to 400 us (1370 to 1450 TFLOP/s, the same as the library's product
-// of these sizes); a wave's LDS reads take 75% of its MFMAs' time, and what is
-// left is the clock that the matrix units hold at this load.
+// bf16 with gelu and z kept: 400 to 420 us from box to box in a run of calls
+// (1310 to 1370 TFLOP/s; 370 to 400 us without them, no more than the library's
+// product of these sizes), 400 at best and 466 at the median under a profiler,
+// where the clock has not settled; a wave's LDS reads take 75% of its MFMAs'
+// time, and what is left is the clock that the matrix units hold at this load.
 // The second block of a pair finds its first B half where the block before
 // read it to, so the two B register sets change roles from block to block.
 constexpr int kHalfBytes = 128 * 128;
@@ -1376,8 +1378,10 @@ struct SlopeArgs {
 // in binary32 from the unrounded products.  A pass over memory: 64 lanes
 // cover 64 V columns, the 4 waves take the rows in turn.
 // dz is rounded to the element type because the matrix units multiply that
-// type: 2^-9 (bf16) of each term, independent from term to term, which adds
-// to a product's error no more than the rounding of its result.
+// type (its two halves would take two products each): up to 2^-8 (bf16) of
+// each term, independent from term to term, which adds to a product's error no
+// more than the rounding of its result (2.4e-3 of dx and dw against 64 bits,
+// with the result's rounding alone 1.7e-3).
 template <class C>
 __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs a) {
   constexpr int V = C::V;
