@@ -297,11 +297,14 @@ ProductPlan plan_product(const Operand& a, bool a_along, const Operand& b, bool 
       !mostly_empty(a_along && b_along, m, n, big_m * big_n)) {
     p.pack_a = !lies_well(a);
     p.pack_b = !lies_well(b);
-    // An operand is laid out anew only for at least 4 rows (columns) of tiles
-    // that use it (32768 outputs, k 4096, w at odd addresses, us: 512 rows 270
-    // against 210 by small tiles that take it as it lies, 768 279 against 267,
-    // 1024 294 against 354; k 8192, 1 row: 398 against 89 with few rows).
-    if ((!p.pack_a || big_n >= 4) && (!p.pack_b || big_m >= 4) &&
+    // An operand is laid out anew only for enough rows (columns) of tiles that
+    // use it; small tiles take it as it lies (32768 outputs, k 4096, w at odd
+    // addresses, us: 512 rows 212 with the copy, 182 without; 600 267 and 219;
+    // 1000 291 and 340; k 8192, 1 row: 398 against 164 with few rows).  Small
+    // tiles read both operands of a weight gradient down their columns, whose
+    // edges cost them more (16384 x 600, 8192 rows: 262 and 344).
+    const uint64_t enough = a_along ? 4 : 3;
+    if ((!p.pack_a || big_n >= enough) && (!p.pack_b || big_m >= enough) &&
         within_reach(p.pack_a ? packed_stride(a.cols) : a.stride, a.cols, a_along) &&
         within_reach(p.pack_b ? packed_stride(b.cols) : b.stride, b.cols, b_along)) {
       p.kind = ProductPlan::kBig;
