@@ -1,0 +1,298 @@
+"""Cases for timing and checking the gated feed-forward block and the 8-bit products of a tensor-parallel layer.
+
+Five operators: ``gated_linear`` (two projections of one input, an activation
+of the first and their product in one call) and its backward pass;
+``quantize`` (rows to 8-bit integers with a scale for each), ``linear_int8``
+(a product of such rows with a weight that has a scale for each output) and
+``gated_linear_int8``.  Where ``own`` is false, ``run`` computes them from
+elementary torch operations in binary32; where it is true, it calls the
+package's operators.  ``exact`` computes them in binary64 from torch's own
+definitions (autograd for the gradients).
+"""
+
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+BYTES = {"bf16": 2, "fp16": 2, "fp32": 4}
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+LEAST = 2.0 ** -100  # a row's largest size counts as at least this much when its scale is chosen
+
+
+def _gated(name, rows, k, n, dtype, act="silu", bias=False, preacts=False):
+    return {"name": name, "op": "gated", "rows": rows, "in": k, "out": n, "dtype": dtype, "act": act, "bias": bias,
+            "preacts": preacts}
+
+
+def _gated_bwd(name, rows, k, n, dtype, act="silu"):
+    return {"name": name, "op": "gated_bwd", "rows": rows, "in": k, "out": n, "dtype": dtype, "act": act}
+
+
+def _quantize(name, rows, width, dtype):
+    return {"name": name, "op": "quantize", "rows": rows, "width": width, "dtype": dtype}
+
+
+def _int8(name, rows, k, n, dtype, act="none", bias=False, residual=False):
+    return {"name": name, "op": "int8", "rows": rows, "in": k, "out": n, "dtype": dtype, "act": act, "bias": bias,
+            "residual": residual}
+
+
+def _gated_int8(name, rows, k, n, dtype, act="silu", bias=False):
+    return {"name": name, "op": "gated_int8", "rows": rows, "in": k, "out": n, "dtype": dtype, "act": act,
+            "bias": bias}
+
+
+def listed():
+    return [
+        # One token through a rank's gate and up projections (hidden 8192): latency and the weights' bytes.
+        _gated("gated_token", 1, 8192, 4096, "bf16"),
+        # The 8192-token prompt through them, training form (both pre-activations kept).
+        _gated("gated_prompt", 8192, 8192, 4096, "bf16", preacts=True),
+        # Odd sizes in binary32: rows that start at no 16-byte boundary.
+        _gated("gated_ragged", 1001, 2047, 1537, "fp32", act="gelu_tanh", bias=True),
+        # Backward pass over the prompt: input gradient, both weights' and both biases'.
+        _gated_bwd("gated_bwd_prompt", 8192, 8192, 4096, "bf16"),
+        # Odd sizes in binary16.
+        _gated_bwd("gated_bwd_ragged", 515, 1025, 770, "fp16", act="gelu"),
+        # The decode step's 32 tokens to 8 bits: latency.
+        _quantize("quantize_decode", 32, 8192, "bf16"),
+        # The 8192-token prompt to 8 bits: memory.
+        _quantize("quantize_prompt", 8192, 8192, "bf16"),
+        # One token through a column-parallel projection with an 8-bit weight.
+        _int8("int8_token", 1, 8192, 4096, "bf16", act="gelu", bias=True),
+        # The prompt through the row-parallel projection: partial sums with a residual on this rank.
+        _int8("int8_prompt", 8192, 4096, 8192, "bf16", residual=True),
+        # Odd sizes, binary16 results: rows that start at no 16-byte boundary.
+        _int8("int8_ragged", 1001, 2047, 1537, "fp16", act="silu", bias=True, residual=True),
+        # The decode step's 32 tokens through 8-bit gate and up projections.
+        _gated_int8("gated_int8_decode", 32, 8192, 4096, "bf16"),
+        # The prompt through them.
+        _gated_int8("gated_int8_prompt", 8192, 8192, 4096, "bf16"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    n = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    n = min(max(n, lo), hi)
+    # half of the sizes are multiples of 64 where they are large enough, as a model's are
+    return n // 64 * 64 if n >= 256 and rng.random() < 0.5 else n
+
+
+def draw(rng):
+    dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+    op = rng.choice(["gated", "gated", "gated_bwd", "quantize", "int8", "int8", "gated_int8"])
+    if op == "quantize":
+        rows, width = _log_int(rng, 1, 8192), _log_int(rng, 16, 20000)
+        while rows * width * BYTES[dtype] > 8192 * 8192 * 2:
+            rows = max(1, rows // 2)
+        case = _quantize("", rows, width, dtype)
+    else:
+        rows = _log_int(rng, 1, 8192)
+        k, n = _log_int(rng, 16, 8192), _log_int(rng, 16, 8192)
+        most = 8192 * 8192 * 4096 // (8 if dtype == "fp32" and op in ("gated", "gated_bwd") else 1)
+        while rows * k * n > most:
+            rows = max(1, rows // 2)
+        act, bias = rng.choice(ACTIVATIONS), rng.random() < 0.5
+        if op == "gated":
+            case = _gated("", rows, k, n, dtype, act, bias, rng.random() < 0.4)
+        elif op == "gated_bwd":
+            case = _gated_bwd("", rows, k, n, dtype, act)
+        elif op == "int8":
+            case = _int8("", rows, k, n, dtype, act, bias, rng.random() < 0.5)
+        else:
+            case = _gated_int8("", rows, k, n, dtype, act, bias)
+    del case["name"]
+    return case
+
+
+def _to_8_bits(x):
+    """Rows of x as 8-bit integers and binary32 scales; divisions go through 64 bits, so that they are rounded once."""
+    x = x.float()
+    most = x.abs().amax(1).clamp_min(LEAST).double()
+    q = torch.round(x * (127.0 / most).float()[:, None]).to(torch.int8)
+    return q, (most / 127.0).float()
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    t = DTYPES[case["dtype"]]
+
+    def normal(*shape, scale=1.0, dtype=t):
+        return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32).mul_(scale).to(dtype)
+
+    def rows_of(rows, width):
+        # what a layer norm hands on: unit size, a few columns several times larger
+        wide = torch.rand(width, generator=g, device="cuda")
+        return normal(rows, width, dtype=torch.float32) * torch.where(wide < 0.01, 6.0, 1.0)
+
+    s = {"case": case}
+    if case["op"] == "quantize":
+        s["x"] = rows_of(case["rows"], case["width"]).to(t)
+        return s
+    rows, k, n = case["rows"], case["in"], case["out"]
+    if case["op"] in ("int8", "gated_int8"):
+        s["q"], s["scale"] = _to_8_bits(rows_of(rows, k))
+        s["b"] = normal(n, scale=0.5) if case["bias"] else None
+        s["w"], s["w_scale"] = _to_8_bits(normal(n, k, scale=k ** -0.5, dtype=torch.float32))
+        if case["op"] == "int8":
+            s["r"] = normal(rows, n) if case["residual"] else None
+        else:
+            s["up"], s["up_scale"] = _to_8_bits(normal(n, k, scale=k ** -0.5, dtype=torch.float32))
+            s["up_b"] = normal(n, scale=0.5) if case["bias"] else None
+        return s
+    s["x"] = normal(rows, k)
+    s["w"], s["up"] = normal(n, k, scale=k ** -0.5), normal(n, k, scale=k ** -0.5)
+    if case["op"] == "gated":
+        s["b"] = normal(n, scale=0.5) if case["bias"] else None
+        s["up_b"] = normal(n, scale=0.5) if case["bias"] else None
+    else:
+        s["dy"] = normal(rows, n)
+        # what the forward pass kept: both pre-activations, in the activations' type
+        s["z"], s["v"] = s["x"] @ s["w"].t(), s["x"] @ s["up"].t()
+    return s
+
+
+def _act(z, act):
+    if act == "relu":
+        return torch.where(z > 0, z, torch.zeros_like(z))
+    if act == "gelu":
+        return 0.5 * z * (1.0 + torch.erf(z * math.sqrt(0.5)))
+    if act == "gelu_tanh":
+        return 0.5 * z * (1.0 + torch.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z * z * z)))
+    if act == "silu":
+        return z / (1.0 + torch.exp(-z))
+    return z
+
+
+def _act_slope(z, act):
+    if act == "relu":
+        return (z > 0).to(z.dtype)
+    if act == "gelu":
+        return 0.5 * (1.0 + torch.erf(z * math.sqrt(0.5))) + z * torch.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    if act == "gelu_tanh":
+        c = math.sqrt(2.0 / math.pi)
+        t = torch.tanh(c * (z + 0.044715 * z * z * z))
+        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * c * (1.0 + 3.0 * 0.044715 * z * z)
+    if act == "silu":
+        q = 1.0 / (1.0 + torch.exp(-z))
+        return q * (1.0 + z * (1.0 - q))
+    return torch.ones_like(z)
+
+
+def _plain(s):
+    case = s["case"]
+    t = DTYPES[case["dtype"]]
+    if case["op"] == "quantize":
+        q, scale = _to_8_bits(s["x"])
+        return {"q": q, "scale": scale}
+    if case["op"] in ("int8", "gated_int8"):
+        q = s["q"].float()
+        z = (q @ s["w"].float().t()) * s["scale"][:, None] * s["w_scale"]
+        if s["b"] is not None:
+            z = z + s["b"].float()
+        y = _act(z, case["act"])
+        if case["op"] == "int8":
+            if s["r"] is not None:
+                y = y + s["r"].float()
+            return {"y": y.to(t)}
+        v = (q @ s["up"].float().t()) * s["scale"][:, None] * s["up_scale"]
+        if s["up_b"] is not None:
+            v = v + s["up_b"].float()
+        return {"y": (y * v).to(t)}
+    x, w, up = s["x"].float(), s["w"].float(), s["up"].float()
+    if case["op"] == "gated":
+        z, v = x @ w.t(), x @ up.t()
+        if s["b"] is not None:
+            z, v = z + s["b"].float(), v + s["up_b"].float()
+        y = (_act(z, case["act"]) * v).to(t)
+        return {"y": y, "z": z.to(t), "v": v.to(t)} if case["preacts"] else {"y": y}
+    dy, z = s["dy"].float(), s["z"].float()
+    dz = dy * s["v"].float() * _act_slope(z, case["act"])
+    dv = dy * _act(z, case["act"])
+    return {"dx": (dz @ w + dv @ up).to(t), "dw": (dz.t() @ x).to(t), "dup": (dv.t() @ x).to(t),
+            "db": dz.sum(0).to(t), "dup_b": dv.sum(0).to(t)}
+
+
+def _framework(s):
+    from allreduce_emulated_peer_amd import mscl
+
+    case = s["case"]
+    if case["op"] == "quantize":
+        q, scale = mscl.quantize_tensors(s["x"])
+        return {"q": q, "scale": scale}
+    if case["op"] == "int8":
+        return {"y": mscl.linear_int8_tensors(s["q"], s["scale"], s["w"], s["w_scale"], bias=s["b"], residual=s["r"],
+                                              activation=case["act"], dtype=DTYPES[case["dtype"]])}
+    if case["op"] == "gated_int8":
+        return {"y": mscl.gated_linear_int8_tensors(s["q"], s["scale"], s["w"], s["w_scale"], s["up"], s["up_scale"],
+                                                    gate_bias=s["b"], up_bias=s["up_b"], activation=case["act"],
+                                                    dtype=DTYPES[case["dtype"]])}
+    if case["op"] == "gated":
+        out = mscl.gated_linear_tensors(s["x"], s["w"], s["up"], gate_bias=s["b"], up_bias=s["up_b"],
+                                        activation=case["act"], return_preacts=case["preacts"])
+        return {"y": out[0], "z": out[1], "v": out[2]} if case["preacts"] else {"y": out}
+    dx, dw, dup, db, dup_b = mscl.gated_linear_backward_tensors(s["dy"], s["x"], s["w"], s["up"], s["z"], s["v"],
+                                                                activation=case["act"])
+    return {"dx": dx, "dw": dw, "dup": dup, "db": db, "dup_b": dup_b}
+
+
+def run(state):
+    if own:
+        return _framework(state)
+    return _plain(state)
+
+
+def work(case):
+    e = BYTES[case["dtype"]]
+    if case["op"] == "quantize":
+        rows, width = case["rows"], case["width"]
+        return {"bytes": rows * width * (e + 1) + 4 * rows, "flops": 3 * rows * width}
+    m, k, n = case["rows"], case["in"], case["out"]
+    if case["op"] == "int8":
+        moved = m * k + n * k + 4 * (m + n) + e * ((n if case["bias"] else 0) + m * n * (1 + int(case["residual"])))
+        return {"bytes": moved, "flops": 2 * m * n * k}
+    if case["op"] == "gated_int8":
+        moved = m * k + 2 * n * k + 4 * (m + 2 * n) + e * ((2 * n if case["bias"] else 0) + m * n)
+        return {"bytes": moved, "flops": 4 * m * n * k}
+    if case["op"] == "gated":
+        moved = m * k + 2 * n * k + (2 * n if case["bias"] else 0) + m * n * (3 if case["preacts"] else 1)
+        return {"bytes": moved * e, "flops": 4 * m * n * k}
+    # dy, z and v; x and dx; both weights and their gradients; both biases' gradients
+    return {"bytes": (3 * m * n + 2 * m * k + 4 * n * k + 2 * n) * e, "flops": 8 * m * n * k}
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    F = torch.nn.functional
+    acts = {"none": lambda z: z, "relu": F.relu, "gelu": F.gelu, "silu": F.silu,
+            "gelu_tanh": lambda z: F.gelu(z, approximate="tanh")}
+    act = acts.get(case.get("act"))
+    if case["op"] == "quantize":
+        # q is defined by the binary32 product of x and the binary32 quotient 127 / largest; both roundings of a
+        # 64-bit value are those of the exact one
+        x = s["x"].double()
+        most = torch.linalg.vector_norm(x, math.inf, dim=1).clamp(min=LEAST)
+        by = torch.full_like(most, 127).div(most).to(torch.float32).double()
+        q = torch.mul(x, by.unsqueeze(1)).to(torch.float32).double().round_()
+        return {"q": q.to(torch.int8), "scale": most / 127}
+    d = {name: (v.double() if isinstance(v, torch.Tensor) else v) for name, v in s.items()}
+    if case["op"] in ("int8", "gated_int8"):
+        x = d["q"].mul_(d["scale"].unsqueeze(1))
+        y = act(F.linear(x, d["w"].mul_(d["w_scale"].unsqueeze(1)), d["b"]))
+        if case["op"] == "gated_int8":
+            return {"y": y.mul_(F.linear(x, d["up"].mul_(d["up_scale"].unsqueeze(1)), d["up_b"]))}
+        return {"y": y if d["r"] is None else torch.add(y, d["r"])}
+    if case["op"] == "gated":
+        z, v = F.linear(d["x"], d["w"], d["b"]), F.linear(d["x"], d["up"], d["up_b"])
+        y = torch.mul(act(z), v)
+        return {"y": y, "z": z, "v": v} if case["preacts"] else {"y": y}
+    z, v = d["z"].requires_grad_(), d["v"].requires_grad_()
+    dz, dv = torch.autograd.grad(act(z) * v, (z, v), d["dy"])
+    return {"dx": torch.addmm(torch.mm(dz, d["w"]), dv, d["up"]),
+            "dw": torch.mm(dz.t().contiguous(), d["x"]), "dup": torch.mm(dv.t().contiguous(), d["x"]),
+            "db": torch.ones(1, dz.shape[0], dtype=dz.dtype, device=dz.device).mm(dz)[0],
+            "dup_b": torch.ones(1, dv.shape[0], dtype=dv.dtype, device=dv.device).mm(dv)[0]}
