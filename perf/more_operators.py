@@ -2,9 +2,9 @@
 
 Five operators: ``gated_linear`` (two projections of one input, an activation
 of the first and their product in one call) and its backward pass;
-``quantize`` (rows to 8-bit integers with a scale for each), ``linear_int8``
+``quantize`` (rows to 8-bit integers with a scale for each), ``linear_quantized``
 (a product of such rows with a weight that has a scale for each output) and
-``gated_linear_int8``.  Where ``own`` is false, ``run`` computes them from
+``gated_linear_quantized``.  Where ``own`` is false, ``run`` computes them from
 elementary torch operations in binary32; where it is true, it calls the
 package's operators.  ``exact`` computes them in binary64 from torch's own
 definitions (autograd for the gradients).
@@ -225,10 +225,10 @@ def _framework(s):
         q, scale = mscl.quantize_tensors(s["x"])
         return {"q": q, "scale": scale}
     if case["op"] == "int8":
-        return {"y": mscl.linear_int8_tensors(s["q"], s["scale"], s["w"], s["w_scale"], bias=s["b"], residual=s["r"],
+        return {"y": mscl.linear_quantized_tensors(s["q"], s["scale"], s["w"], s["w_scale"], bias=s["b"], residual=s["r"],
                                               activation=case["act"], dtype=DTYPES[case["dtype"]])}
     if case["op"] == "gated_int8":
-        return {"y": mscl.gated_linear_int8_tensors(s["q"], s["scale"], s["w"], s["w_scale"], s["up"], s["up_scale"],
+        return {"y": mscl.gated_linear_quantized_tensors(s["q"], s["scale"], s["w"], s["w_scale"], s["up"], s["up_scale"],
                                                     gate_bias=s["b"], up_bias=s["up_b"], activation=case["act"],
                                                     dtype=DTYPES[case["dtype"]])}
     if case["op"] == "gated":
