@@ -1,9 +1,12 @@
 """Build the HIP library libmscl.so in-tree for gfx950.
 
-Two translation units: csrc/mscl.hip (the collectives' C ABI, including the
-kernels of csrc/kernels.hpp) and csrc/operators.hip (the linear layer and
-layer norm), compiled side by side with hipcc: -O3, no fast-math, no FP
-contraction, packed-FP32 instructions disabled.
+The translation units are csrc/mscl.hip (the collectives' C ABI, including the
+kernels of csrc/kernels.hpp), csrc/operators.hip (the linear layer and layer
+norm), csrc/gated.hip (the gated feed-forward block, forward and backward),
+csrc/quantized.hip (rows to 8 bits, the 8-bit product) and
+csrc/gated_quantized.hip (the gated block of 8-bit weights), compiled side by
+side with hipcc: -O3, no fast-math, no FP contraction, packed-FP32 instructions
+disabled.
 """
 
 from __future__ import annotations
@@ -15,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SRC = os.path.join(CSRC, "mscl.hip")
-UNITS = ("mscl", "operators")
+UNITS = ("mscl", "operators", "gated", "quantized", "gated_quantized")
 LIB = os.path.join(HERE, "libmscl.so")
 ARCH = "gfx950"
 

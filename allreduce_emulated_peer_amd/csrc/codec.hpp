@@ -201,6 +201,13 @@ __device__ inline u32x4 load_partial_scoped(const void* base, uint64_t vi, int n
   return v;
 }
 
+// 8-bit integers, as operands of integer products only: nothing rounds to them
+// through a codec.
+struct I8 {
+  static constexpr int kElemBytes = 1;
+  static constexpr int V = 16;
+};
+
 // First `nvalid` (< V) elements of vector `vi`; the rest read as zero bits.
 template <class C>
 __device__ inline u32x4 load_partial(const void* base, uint64_t vi, int nvalid) {
@@ -210,6 +217,11 @@ __device__ inline u32x4 load_partial(const void* base, uint64_t vi, int nvalid) 
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k < nvalid) v[k] = p[k];
+  } else if constexpr (C::kElemBytes == 1) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + vi * 16;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k < nvalid) v[k >> 2] |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
   } else {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + vi * 8;
 #pragma unroll

@@ -1,0 +1,370 @@
+// Host side of the gated feed-forward block, forward and backward
+// (include/mscl.h).  Every entry point returns a status code; nothing here
+// aborts or allocates.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "../../include/mscl.h"
+#include "failure.hpp"
+#include "feedforward.hpp"
+#include "forward.hpp"
+#include "launch.hpp"
+#include "linear.hpp"
+
+namespace {
+
+using namespace mscl;
+using namespace mscl::launch;
+
+mscl_status_t check_gated(const mscl_gated_linear_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  mscl_status_t st = check_kinds(c->dtype, c->activation);
+  if (st == MSCL_SUCCESS) st = check_sizes(c->rows, c->in_features, c->out_features);
+  if (st != MSCL_SUCCESS) return st;
+  const size_t e = bytes_of(c->dtype), m = c->rows, k = c->in_features, n = c->out_features;
+  s.add("x", c->x, m, k, c->x_stride, e, false, n != 0);
+  s.add("gate_w", c->gate_w, n, k, c->gate_w_stride, e, false, m != 0);
+  s.add("up_w", c->up_w, n, k, c->up_w_stride, e, false, m != 0);
+  s.add("gate_bias", c->gate_bias, 1, n, 0, e, false, false);
+  s.add("up_bias", c->up_bias, 1, n, 0, e, false, false);
+  s.add("y", c->y, m, n, c->y_stride, e, true, true);
+  s.add("gate", c->gate, m, n, c->gate_stride, e, true, false);
+  s.add("up", c->up, m, n, c->up_stride, e, true, false);
+  return s.check();
+}
+
+PairOperand weights_of(const mscl_gated_linear_t& c) {
+  return pair_of(c.gate_w, c.gate_w_stride, c.up_w, c.up_w_stride, c.out_features, c.in_features);
+}
+ForwardPlan plan_gated(const mscl_gated_linear_t& c) {
+  return plan_forward(operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c).half, 2, c.rows, c.out_features,
+                      c.in_features, bytes_of(c.dtype));
+}
+
+// ------------------------------------------------------------------ backward pass
+
+// Parts of a backward call's workspace, each from a 256-byte boundary.
+struct GatedBackwardPlan {
+  uint64_t half = 0;     // columns of dz and of dv in the workspace
+  bool products = false; // dx or a weight's gradient is wanted
+  bool dx_big = false, pack_w = false, dw_big = false;
+  ProductPlan dx, dw;    // dx as tiles: of one weight's half
+  uint32_t groups = 0, rows_per_group = 0;  // of the bias gradients' partial sums
+  PairOperand w;
+  Operand x;
+  size_t w_bytes = 0;    // of one weight laid out anew
+  size_t d_at = 0, sums_at = 0, dx_at = 0, dw_at = 0, bytes = 0;
+};
+
+GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
+  GatedBackwardPlan p;
+  const size_t e = bytes_of(c.dtype);
+  const uint64_t m = c.rows, k = c.in_features, n = c.out_features;
+  const bool want_dw = c.dgate_w || c.dup_w;
+  p.products = c.dx || want_dw;
+  p.half = packed_stride(n);
+  size_t at = 0;
+  if (p.products) at = round_up(m * 2 * p.half * e, 256);
+  plan_groups(m, ceil_div(p.half, 64 * (16 / e)), &p.groups, &p.rows_per_group);
+  p.sums_at = at;
+  if (c.dgate_bias || c.dup_bias) at = round_up(at + size_t(p.groups) * 2 * n * 4, 256);
+  // The plans go by sizes and layouts, not by which gradients are wanted: a
+  // gradient has the same bits alone.
+  const Operand none{nullptr, k, n, k};
+  p.w = c.dx ? pair_of(c.gate_w, c.gate_w_stride, c.up_w, c.up_w_stride, n, k) : PairOperand{{none, none}};
+  p.x = want_dw ? operand(c.x, c.x_stride, m, k) : Operand{nullptr, k, m, k};
+  const Operand d{nullptr, 2 * p.half, m, 2 * p.half};
+  const uint64_t big_m = ceil_div(m, 256), big_n = ceil_div(k, 256), turn = p.half / 64;
+  if (e == 2 && big_m * big_n >= kCus / 2 && turn >= 2) {
+    p.pack_w = !lies_well(p.w.half[0]) || !lies_well(p.w.half[1]) || p.w.half[0].stride != p.w.half[1].stride;
+    p.dx_big = (!p.pack_w || big_m >= 4) && within_reach(d.stride, d.cols, true) &&
+               within_reach(p.pack_w ? packed_stride(k) : p.w.half[0].stride, k, false);
+    if (!p.dx_big) p.pack_w = false;
+  }
+  if (m && n && k) {
+    p.dw = plan_product(Operand{nullptr, 2 * p.half, m, round_up(n, 8)}, false, p.x, false, n, k, m, c.dtype);
+    p.dw_big = p.dw.kind == ProductPlan::kBig;
+  }
+  // what runs as tiles runs in one launch
+  const uint64_t across = ceil_div(k, 128);
+  const uint64_t large = 2 * across * ((p.dx_big ? 0 : ceil_div(m, 128)) + (p.dw_big ? 0 : ceil_div(n, 128)));
+  choose_tile(&p.dx, large, c.dtype);
+  const uint64_t steps = 2 * ((p.dx_big ? 0 : ceil_div(m, p.dx.tile_m) * turn) +
+                              (p.dw_big ? 0 : ceil_div(n, p.dx.tile_m) * ceil_div(m, 64))) * ceil_div(k, p.dx.tile_n);
+  if (!p.dw_big) {
+    const ProductPlan shape = p.dx;
+    p.dw = shape;
+    choose_shares(&p.dw, n, k, m, steps);
+  }
+  if (!p.dx_big) choose_shares(&p.dx, m, k, n, steps);
+  p.dx_at = at;
+  if (c.dx) {
+    if (p.pack_w) p.w_bytes = packed_bytes(p.w.half[0]);
+    at += p.dx_big ? 2 * p.w_bytes : round_up(2 * size_t(p.dx.shares) * m * p.dx.partial_stride * 4, 256);
+  }
+  p.dw_at = at;
+  if (want_dw) at += p.dw_big ? p.dw.bytes() : 2 * p.dw.partial_bytes;
+  p.bytes = at;
+  return p;
+}
+
+mscl_status_t check_gated_backward(const mscl_gated_linear_backward_t* c, Spans& s) {
+  if (!c) return bad("call is null");
+  mscl_status_t st = check_kinds(c->dtype, c->activation);
+  if (st == MSCL_SUCCESS) st = check_sizes(c->rows, c->in_features, c->out_features);
+  if (st != MSCL_SUCCESS) return st;
+  const size_t e = bytes_of(c->dtype), m = c->rows, k = c->in_features, n = c->out_features;
+  const bool dw = c->dgate_w || c->dup_w, some = c->dx || dw || c->dgate_bias || c->dup_bias;
+  s.add("dy", c->dy, m, n, c->dy_stride, e, false, some);
+  if (dw) s.add("x", c->x, m, k, c->x_stride, e, false, n != 0);
+  if (c->dx) {
+    s.add("gate_w", c->gate_w, n, k, c->gate_w_stride, e, false, m != 0);
+    s.add("up_w", c->up_w, n, k, c->up_w_stride, e, false, m != 0);
+  }
+  s.add("gate", c->gate, m, n, c->gate_stride, e, false, some);
+  s.add("up", c->up, m, n, c->up_stride, e, false, some);
+  s.add("dx", c->dx, m, k, c->dx_stride, e, true, false);
+  s.add("dgate_w", c->dgate_w, n, k, c->dgate_w_stride, e, true, false);
+  s.add("dup_w", c->dup_w, n, k, c->dup_w_stride, e, true, false);
+  s.add("dgate_bias", c->dgate_bias, 1, n, 0, e, true, false);
+  s.add("dup_bias", c->dup_bias, 1, n, 0, e, true, false);
+  return s.check();
+}
+
+template <class C, int kBM, int kBN>
+mscl_status_t launch_gated_back(const GatedBackArgs& a, uint32_t groups, hipStream_t stream) {
+  constexpr int kLds = std::max(tile_lds<C, true, false, kBM, kBN>(), tile_lds<C, false, false, kBM, kBN>());
+  const hipError_t err = allow_lds<&gated_back<C, kBM, kBN>>(kLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  gated_back<C, kBM, kBN><<<groups, 256, kLds, stream>>>(a);
+  return launched("gated_back");
+}
+
+Epilogue results(void* y, uint64_t stride, uint64_t m, uint64_t n) {
+  Epilogue e;
+  memset(&e, 0, sizeof e);
+  e.y = bytes_at(y);
+  e.y_stride = stride;
+  e.m = m;
+  e.n = n;
+  return e;
+}
+
+template <class C>
+mscl_status_t dx_by_large_tiles(const GatedBackwardPlan& p, const Operand& d, const Epilogue& e, int dtype, char* ws,
+                                hipStream_t s) {
+  PairOperand w = p.w;
+  if (p.pack_w) {
+    mscl_status_t st = pack_operand(dtype, &w.half[0], ws + p.dx_at, s);
+    if (st == MSCL_SUCCESS) st = pack_operand(dtype, &w.half[1], ws + p.dx_at + p.w_bytes, s);
+    if (st != MSCL_SUCCESS) return st;
+  }
+  const uint64_t tm = ceil_div(e.m, 256), tn = ceil_div(e.n, 256);
+  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  const hipError_t err = allow_lds<&gated_dx_big<C>>(kBigLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  const GatedDxArgs a{d, w, e, static_cast<uint32_t>(p.half / 64), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
+  gated_dx_big<C><<<static_cast<uint32_t>(tm * tn), 512, kBigLds, s>>>(a);
+  return launched("gated_dx_big");
+}
+
+// dx, both weights' gradients and the bias gradients' last sums, as far as they
+// run as tiles.
+template <class C>
+mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c, bool dx, bool dw, bool db,
+                            const Operand& d, const JoinArgs& join, char* ws, hipStream_t s) {
+  const uint64_t m = c.rows, k = c.in_features, n = c.out_features;
+  constexpr size_t e = C::kElemBytes;
+  GatedBackArgs a;
+  GatedJoinArgs j;
+  memset(&a, 0, sizeof a);
+  memset(&j, 0, sizeof j);
+  a.db = join;
+  const uint64_t dx_tiles = ceil_div(m, p.dx.tile_m) * ceil_div(k, p.dx.tile_n);
+  const uint64_t dw_tiles = ceil_div(n, p.dx.tile_m) * ceil_div(k, p.dx.tile_n);
+  uint64_t groups = 0;
+  for (int h = 0; h < 2; ++h) {
+    const Operand side{d.base + h * p.half * e, d.stride, m, round_up(n, C::V)};
+    if (dx) {
+      a.dx[h] = tile_args(p.dx, side, p.w.half[h], n, results(c.dx, c.dx_stride, m, k), nullptr);
+      a.dx[h].e.partial = reinterpret_cast<float*>(ws + p.dx_at) + h * p.dx.shares * m * p.dx.partial_stride;
+    }
+    void* to = h ? c.dup_w : c.dgate_w;
+    const uint64_t stride = h ? c.dup_w_stride : c.dgate_w_stride;
+    if (dw) {
+      a.dw[h] = tile_args(p.dw, side, p.x, m, results(to, stride, to ? n : 0, k), ws + p.dw_at + h * p.dw.partial_bytes);
+      // a gradient that is not wanted has no rows, but takes its place in the launch
+      a.dw[h].tiles_m = static_cast<uint32_t>(ceil_div(n, p.dw.tile_m));
+    }
+  }
+  if (dx_tiles * p.dx.shares > kMostGroups / 8 || dw_tiles * p.dw.shares > kMostGroups / 8)
+    return bad("the matrices have too many tiles");
+  if (dx) {
+    a.dx_tiles = static_cast<uint32_t>(dx_tiles);
+    a.dx_groups = static_cast<uint32_t>(dx_tiles * p.dx.shares);
+    j.e[0] = a.dx[0].e;
+    j.shares[0] = 2 * p.dx.shares;
+  }
+  if (dw) {
+    a.dw_tiles = static_cast<uint32_t>(dw_tiles);
+    a.dw_groups = static_cast<uint32_t>(dw_tiles * p.dw.shares);
+    for (int h = 0; h < 2; ++h) {
+      j.e[1 + h] = a.dw[h].e;
+      j.shares[1 + h] = p.dw.shares;
+    }
+  }
+  groups = 2 * (uint64_t(a.dx_groups) + a.dw_groups);
+  a.db_blocks = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(n, 32)));
+  if (db) groups += 2 * uint64_t(a.db_blocks);
+  if (groups == 0) return MSCL_SUCCESS;
+  mscl_status_t st;
+  if (p.dx.tile_m == 128)
+    st = launch_gated_back<C, 128, e == 4 ? 64 : 128>(a, static_cast<uint32_t>(groups), s);
+  else
+    st = launch_gated_back<C, 64, 64>(a, static_cast<uint32_t>(groups), s);
+  if (st != MSCL_SUCCESS) return st;
+  uint64_t joins = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!(i == 0 ? dx : dw) || j.shares[i] < 2) continue;
+    const uint64_t of_it = ceil_div(ceil_div(j.e[i].n, C::V) * j.e[i].m, 256);
+    joins += of_it;
+    if (joins > kMostGroups) return bad("the matrices have too many tiles");
+    j.groups[i] = static_cast<uint32_t>(of_it);
+  }
+  if (joins == 0) return MSCL_SUCCESS;
+  gated_join<C><<<static_cast<uint32_t>(joins), 256, 0, s>>>(j);
+  return launched("gated_join");
+}
+
+}  // namespace
+
+extern "C" {
+
+mscl_status_t mscl_gated_linear_workspace(const mscl_gated_linear_t* call, size_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  Spans spans;
+  const mscl_status_t st = check_gated(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  *bytes = call->rows && call->out_features ? plan_gated(*call).bytes : 0;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace, size_t workspace_bytes, void* stream) {
+  Spans spans;
+  mscl_status_t st = check_gated(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_gated_linear_t& c = *call;
+  if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
+  const ForwardPlan p = plan_gated(c);
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  return with_codec(c.dtype, [&](auto t) {
+    Gated<decltype(t)> e;
+    memset(&e, 0, sizeof e);
+    e.bias[0] = bytes_at(c.gate_bias);
+    e.bias[1] = bytes_at(c.up_bias);
+    e.y = bytes_at(c.y);
+    e.y_stride = c.y_stride;
+    e.z[0] = bytes_at(c.gate);
+    e.z[1] = bytes_at(c.up);
+    e.z_stride[0] = c.gate_stride;
+    e.z_stride[1] = c.up_stride;
+    e.m = c.rows;
+    e.n = c.out_features;
+    e.act = c.activation;
+    return forward<decltype(t)>(p, operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c), c.in_features, e,
+                                bytes_at(workspace), static_cast<hipStream_t>(stream));
+  });
+}
+
+mscl_status_t mscl_gated_linear_backward_workspace(const mscl_gated_linear_backward_t* call, size_t* bytes) {
+  if (!bytes) return bad("bytes is null");
+  Spans spans;
+  const mscl_status_t st = check_gated_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  *bytes = plan_gated_backward(*call).bytes;
+  return MSCL_SUCCESS;
+}
+
+mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* call, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  Spans spans;
+  mscl_status_t st = check_gated_backward(call, spans);
+  if (st != MSCL_SUCCESS) return st;
+  const mscl_gated_linear_backward_t& c = *call;
+  const GatedBackwardPlan p = plan_gated_backward(c);
+  if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
+  const bool dx = c.dx && c.rows && c.in_features;
+  const bool dw = (c.dgate_w || c.dup_w) && c.out_features && c.in_features;
+  const bool db = (c.dgate_bias || c.dup_bias) && c.out_features;
+  if (!dx && !dw && !db) return MSCL_SUCCESS;
+  int cus = 0;
+  if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = bytes_at(workspace);
+  const size_t e = bytes_of(c.dtype);
+
+  GatedSlopeArgs g;
+  g.dy = bytes_at(c.dy);
+  g.z = bytes_at(c.gate);
+  g.v = bytes_at(c.up);
+  g.d = dx || dw ? ws + p.d_at : nullptr;
+  g.sums = db ? reinterpret_cast<float*>(ws + p.sums_at) : nullptr;
+  g.dy_stride = c.dy_stride;
+  g.z_stride = c.gate_stride;
+  g.v_stride = c.up_stride;
+  g.half = p.half;
+  g.rows = c.rows;
+  g.cols = c.out_features;
+  g.rows_per_group = p.rows_per_group;
+  g.act = c.activation;
+  const uint64_t blocks = ceil_div(p.half, 64 * (16 / e));
+  if (blocks > kMostGroups) return bad("the matrices have too many tiles");
+  if (blocks) {
+    st = with_codec(c.dtype, [&](auto t) {
+      gated_slope<decltype(t)><<<dim3(static_cast<uint32_t>(blocks), p.groups), 256, 0, s>>>(g);
+      return launched("gated_slope");
+    });
+    if (st != MSCL_SUCCESS) return st;
+  }
+  const JoinArgs join =
+      join_args(g.sums, c.out_features, c.out_features, p.groups, c.dgate_bias, c.dup_bias, 2);
+  const Operand d{ws + p.d_at, 2 * p.half, c.rows, 2 * p.half};
+  const bool dx_tiles = dx && !p.dx_big, dw_tiles = dw && !p.dw_big;
+  const bool db_with_tiles = db && (dx_tiles || dw_tiles);
+  if (db && !db_with_tiles && (st = join_columns(c.dtype, join, 2, s)) != MSCL_SUCCESS) return st;
+  if (dx && p.dx_big) {
+    const Epilogue ex = results(c.dx, c.dx_stride, c.rows, c.in_features);
+    st = c.dtype == MSCL_FLOAT16 ? dx_by_large_tiles<F16>(p, d, ex, c.dtype, ws, s)
+                                 : dx_by_large_tiles<BF16>(p, d, ex, c.dtype, ws, s);
+    if (st != MSCL_SUCCESS) return st;
+  }
+  if (dw && p.dw_big) {
+    ProductPlan dw_plan = p.dw;
+    Operand x = p.x;
+    char* at = ws + p.dw_at;
+    if (dw_plan.pack_b) {  // once for both
+      if ((st = pack_operand(c.dtype, &x, at, s)) != MSCL_SUCCESS) return st;
+      dw_plan.pack_b = false;
+    }
+    for (int h = 0; h < 2; ++h) {
+      void* to = h ? c.dup_w : c.dgate_w;
+      if (!to) continue;
+      const Operand side{d.base + h * p.half * e, d.stride, c.rows, round_up(c.out_features, 8)};
+      st = weight_gradient(c.dtype, dw_plan, side, x, c.rows,
+                           results(to, h ? c.dup_w_stride : c.dgate_w_stride, c.out_features, c.in_features), at, s);
+      if (st != MSCL_SUCCESS) return st;
+    }
+  }
+  if (!dx_tiles && !dw_tiles) return MSCL_SUCCESS;
+  return with_codec(c.dtype, [&](auto t) {
+    return back_by_tiles<decltype(t)>(p, c, dx_tiles, dw_tiles, db_with_tiles, d, join, ws, s);
+  });
+}
+
+}  // extern "C"

@@ -37,6 +37,7 @@
 namespace mscl {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -45,12 +46,14 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // 16 bytes at the alignment of one element: gfx950 loads and stores them at
 // any element's address with one instruction.
+typedef u32x4 u32x4_by1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_by4 __attribute__((aligned(4)));
 
 template <class C>
 __device__ inline u32x4 load_loose(const char* p) {
   if constexpr (C::kElemBytes == 4) return *reinterpret_cast<const u32x4_by4*>(p);
+  if constexpr (C::kElemBytes == 1) return *reinterpret_cast<const u32x4_by1*>(p);
   return *reinterpret_cast<const u32x4_by2*>(p);
 }
 template <class C>
@@ -88,6 +91,13 @@ __device__ inline void with_edges(bool full, Fn&& fn) {
   else
     fn(std::false_type{});
 }
+
+// Four neighbouring sums of products of C's elements: binary32, or 32-bit
+// integers for 8-bit ones.
+template <class C>
+using Sums = std::conditional_t<C::kElemBytes == 1, i32x4, f32x4>;
+template <class C>
+using SumOf = std::conditional_t<C::kElemBytes == 1, int32_t, float>;
 
 // ------------------------------------------------------------------ activations
 
@@ -300,15 +310,20 @@ struct Groups {
     if constexpr (C::V == 4) return n0 + 16 * j + 4 * g;
     return n0 + 16 * (2 * j + (g & 1)) + 8 * (g >> 1);
   }
-  static __device__ inline void sums(const f32x4 (&acc)[kM][kN], int q, float* v) {
+  static __device__ inline float value(float v) { return v; }
+  static __device__ inline float value(int32_t v) { return __builtin_bit_cast(float, v); }
+
+  // Integer sums come out as their bits.
+  template <class S>
+  static __device__ inline void sums(const S (&acc)[kM][kN], int q, float* v) {
     const int i = q / kPerRow, j = q % kPerRow;
     if constexpr (C::V == 4) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = acc[i][j][c];
+      for (int c = 0; c < 4; ++c) v[c] = value(acc[i][j][c]);
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float a = acc[i][2 * j][c], b = acc[i][2 * j + 1][c];
+        float a = value(acc[i][2 * j][c]), b = value(acc[i][2 * j + 1][c]);
         swap_rows16(a, b);
         v[c] = a;
         v[4 + c] = b;
@@ -364,6 +379,23 @@ __device__ inline void finish_all(const Epilogue& e, const f32x4 (&acc)[kParts][
 struct Corner {
   uint64_t first, second;
 };
+
+// A wave's block of tiles at (m0, n0) of one share of k.
+template <class C, bool kPlain, int kM, int kN>
+__device__ inline void finish_tile(const Epilogue& e, uint64_t share, const f32x4 (&acc)[1][kM][kN], uint64_t m0,
+                                   uint64_t n0) {
+  if (e.partial) {
+    using G = Groups<C, kM, kN>;
+#pragma unroll
+    for (int q = 0; q < G::kCount; ++q) {
+      float v[C::V];
+      G::sums(acc[0], q, v);
+      keep_partial<C>(e, share, G::row(m0, q), G::column(n0, q), v);
+    }
+  } else {
+    finish_all<C, kPlain>(e, acc, [&](int) { return Corner{m0, n0}; });
+  }
+}
 
 // ------------------------------------------------------------------ column sums
 
@@ -423,22 +455,37 @@ struct TileAt {
 };
 
 struct Operand {
+  static constexpr int kParts = 1;
   const char* base;
   uint64_t stride;  // elements between memory rows
   uint64_t rows;    // memory rows: m or n (kAlong), k (kDown)
   uint64_t cols;    // elements of a memory row: k (kAlong), m or n (kDown)
+  __device__ inline const Operand& part(int) const { return *this; }
 };
 
-struct TileArgs {
-  Operand a, b;
-  Epilogue e;
+// Two weights of one size whose products with the same rows are wanted: the
+// first half of a tile's rows comes from the one, the second from the other,
+// and column n of both lies in one lane.
+struct PairOperand {
+  static constexpr int kParts = 2;
+  Operand half[2];
+  __device__ inline const Operand& part(int p) const { return half[p]; }
+};
+
+template <class B, class E>
+struct TileArgsOf {
+  Operand a;
+  B b;
+  E e;
   uint64_t k;
   uint32_t tiles_m, tiles_n;
   uint32_t blocks_per_share;  // blocks of k that one share sums
 };
+using TileArgs = TileArgsOf<Operand, Epilogue>;
 
-// Where one operand's kT x (64 k) tiles of a run of k come from: a thread's
-// 8-element chunks, block after block, kParts 16-byte loads each.  Rows
+// Where one operand's kT x (64 k; 128 of 8 bits) tiles of a run of k come from:
+// a thread's 8-element (16-element) chunks, block after block, kParts 16-byte
+// loads each.  Rows
 // (kAlong) and columns (kDown) past the matrix meet only results that are not
 // stored: a row past the end repeats the last one.
 // The whole blocks' loads hang on no branch, or the compiler could not count
@@ -449,6 +496,9 @@ struct Feed {
   static constexpr int kChunks = kT * 8 / kThreads;
   static constexpr int kPerRow = kAlong ? 8 : kT / 8;  // chunks per LDS row
   static constexpr int e = C::kElemBytes;
+  static constexpr int kChunk = kParts * C::V;  // elements
+  static constexpr int kBlock = 8 * kChunk;     // k
+  static_assert(kAlong || kChunk == 8, "8-bit operands lie along k");
   // kAlong: each chunk's address; kDown: the first one's, the others lie `apart`
   const char* p[kAlong ? kChunks : 1];
   uint64_t apart;
@@ -456,17 +506,23 @@ struct Feed {
   uint64_t cols;      // kDown: columns from the tile's first on
   uint32_t left = 0;  // whole blocks not yet loaded
 
-  __device__ inline void init(const Operand& o, uint64_t first, uint64_t k) {
-    step = kAlong ? 64 * e : 64 * o.stride * e;
-    cols = kAlong ? 0 : o.cols - first;
-    apart = kThreads / kPerRow * o.stride * e;
+  // O: Operand, or PairOperand for a kAlong tile of both its parts' rows from
+  // `first` on.
+  template <class O>
+  __device__ inline void init(const O& both, uint64_t first, uint64_t k) {
+    static_assert(O::kParts == 1 || (kAlong && kChunks % 2 == 0), "a chunk's rows are of one part");
+    step = kAlong ? kBlock * e : kBlock * both.part(0).stride * e;
+    cols = kAlong ? 0 : both.part(0).cols - first;
+    apart = kThreads / kPerRow * both.part(0).stride * e;
 #pragma unroll
     for (int i = 0; i < (kAlong ? kChunks : 1); ++i) {
-      const int id = i * kThreads + threadIdx.x;
+      constexpr int kOfPart = kChunks / O::kParts;
+      const Operand& o = both.part(i / kOfPart);
+      const int id = (O::kParts == 1 ? i : i % kOfPart) * kThreads + threadIdx.x;
       const int r = id / kPerRow, c = id % kPerRow;
       uint64_t row = (kAlong ? first : k) + r;
       if (kAlong && row >= o.rows) row = o.rows - 1;
-      p[i] = o.base + (row * o.stride + (kAlong ? k : first) + static_cast<uint64_t>(c) * 8) * e;
+      p[i] = o.base + (row * o.stride + (kAlong ? k : first) + static_cast<uint64_t>(c) * kChunk) * e;
     }
   }
   __device__ inline const char* chunk(int i) const {
@@ -490,10 +546,10 @@ struct Feed {
     for (int i = 0; i < (kAlong ? kChunks : 1); ++i) p[i] += by;
   }
 
-  // The same for a block at k of which k_end - k may be less than 64, or
+  // The same for a block at k of which k_end - k may be less than a block, or
   // whose columns may end.
-  template <class Fn>
-  __device__ inline void edge(const Operand& o, uint64_t first, uint64_t k, uint64_t k_end, Fn&& fn) {
+  template <class O, class Fn>
+  __device__ inline void edge(const O& o, uint64_t first, uint64_t k, uint64_t k_end, Fn&& fn) {
     init(o, first, k);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -501,10 +557,10 @@ struct Feed {
       const int r = id / kPerRow, c = id % kPerRow;
       int64_t valid;
       if constexpr (kAlong)
-        valid = static_cast<int64_t>(k_end - k) - c * 8;
+        valid = static_cast<int64_t>(k_end - k) - c * kChunk;
       else
-        valid = k + r < k_end ? static_cast<int64_t>(cols) - c * 8 : 0;
-      const int n = valid < 0 ? 0 : (valid > 8 ? 8 : static_cast<int>(valid));
+        valid = k + r < k_end ? static_cast<int64_t>(cols) - c * kChunk : 0;
+      const int n = valid < 0 ? 0 : (valid > kChunk ? kChunk : static_cast<int>(valid));
 #pragma unroll
       for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, n - q * C::V);
     }
@@ -514,14 +570,15 @@ struct Feed {
 // Walks over the blocks of k of a tile: kDeep whole blocks' loads in flight,
 // then what is left one by one.  store(d, block) puts set d into the block's
 // LDS buffer, compute(block) multiplies it; kBuffers LDS buffers alternate.
-template <int kDeep, int kBuffers, class FA, class FB, class SA, class SB, class Store, class Compute>
-__device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_t k_first, uint64_t k_end, FA& feed_a,
+template <int kDeep, int kBuffers, class Args, class FA, class FB, class SA, class SB, class Store, class Compute>
+__device__ inline void walk(const Args& t, uint64_t m0, uint64_t n0, uint64_t k_first, uint64_t k_end, FA& feed_a,
                             FB& feed_b, SA (&sa)[kDeep], SB (&sb)[kDeep], Store&& store, Compute&& compute) {
+  constexpr int kBlock = FA::kBlock;
   feed_a.init(t.a, m0, k_first);
   feed_b.init(t.b, n0, k_first);
   uint64_t k = k_first;
   const uint32_t blocks =
-      k_end > k_first && feed_a.whole() && feed_b.whole() ? static_cast<uint32_t>((k_end - k_first) / 64) : 0;
+      k_end > k_first && feed_a.whole() && feed_b.whole() ? static_cast<uint32_t>((k_end - k_first) / kBlock) : 0;
   if (blocks > 0) {
     feed_a.left = feed_b.left = blocks;
 #pragma unroll
@@ -553,9 +610,9 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
         if constexpr (kBuffers == 1) __syncthreads();
       }
     }
-    k += static_cast<uint64_t>(blocks) * 64;
+    k += static_cast<uint64_t>(blocks) * kBlock;
   }
-  for (; k < k_end; k += 64) {
+  for (; k < k_end; k += kBlock) {
     sa[0].load_edge(feed_a, t.a, m0, k, k_end);
     sb[0].load_edge(feed_b, t.b, n0, k, k_end);
     __syncthreads();
@@ -565,8 +622,8 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
   }
 }
 
-// One operand's kT x (64 k) tile of a 16-bit type, from memory through
-// registers into LDS.  kAlong: kT rows of 128 bytes, 16-byte chunk c of row r
+// One operand's kT x (64 k) tile of a 16-bit type, or kT x (128 k) of 8-bit
+// integers (kAlong only), from memory through registers into LDS.  kAlong: kT rows of 128 bytes, 16-byte chunk c of row r
 // at chunk c ^ (r % 8), so that eight neighbouring rows' equal chunks lie in
 // different banks.  kDown: one row of kT elements for each k, read
 // transposed; 32-byte segments are xored with bits of k so that the rows that
@@ -574,8 +631,8 @@ __device__ inline void walk(const TileArgs& t, uint64_t m0, uint64_t n0, uint64_
 template <class C, bool kAlong, int kT, int kThreads>
 struct Stage {
   static constexpr int V = C::V;
-  static_assert(V == 8, "binary32 operands are split first");
-  static constexpr int kBlock = 64;  // k
+  static_assert(V == 8 || (V == 16 && kAlong), "binary32 operands are split first");
+  static constexpr int kBlock = 8 * V;  // k
   static constexpr int kChunks = kT * 8 / kThreads;  // 16-byte chunks per thread
   static constexpr int kBytes = kT * 128;
   static constexpr int kPerRow = kAlong ? 8 : kT / V;  // chunks per LDS row
@@ -592,7 +649,8 @@ struct Stage {
   __device__ inline void load(Feed<C, kAlong, kT, kThreads, 1>& f) {
     f.next([&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
   }
-  __device__ inline void load_edge(Feed<C, kAlong, kT, kThreads, 1>& f, const Operand& o, uint64_t first, uint64_t k,
+  template <class O>
+  __device__ inline void load_edge(Feed<C, kAlong, kT, kThreads, 1>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
     f.edge(o, first, k, k_end, [&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
   }
@@ -634,8 +692,10 @@ struct Stage {
 
 // acc += (16 rows of b) x (16 rows of a) over the k of one fragment.
 template <class C>
-__device__ inline f32x4 multiply(const u32x4& b, const u32x4& a, f32x4 acc) {
-  if constexpr (C::kElemBytes == 4) {
+__device__ inline Sums<C> multiply(const u32x4& b, const u32x4& a, Sums<C> acc) {
+  if constexpr (C::kElemBytes == 1) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), acc, 0, 0, 0);
+  } else if constexpr (C::kElemBytes == 4) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t x = b[j], y = a[j];
@@ -652,24 +712,28 @@ __device__ inline f32x4 multiply(const u32x4& b, const u32x4& a, f32x4 acc) {
 // Any sizes, strides and alignments of a 16-bit type: kBM x kBN tiles by 4
 // waves in a square, 64 k at a time, two LDS buffers.  The next kDeep blocks'
 // loads are in flight in registers.
-template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep>
-__device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
+// Of a pair of weights a tile has kBN / 2 columns of each.
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
+__device__ inline void tile_body(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
   using SA = Stage<C, kAAlong, kBM, 256>;
   using SB = Stage<C, kBAlong, kBN, 256>;
-  constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
+  constexpr int kParts = B::kParts;
+  constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
-  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * kBN;
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * (kBN / kParts);
   const int wave = threadIdx.x >> 6;
-  const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
+  const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * SA::kBlock;
   uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * SA::kBlock;
   if (k_end > t.k) k_end = t.k;
 
-  f32x4 acc[1][kWM][kWN];
+  Sums<C> acc[kParts][kWM][kWN];
 #pragma unroll
-  for (int i = 0; i < kWM; ++i)
+  for (int p = 0; p < kParts; ++p)
 #pragma unroll
-    for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int j = 0; j < kWN; ++j) acc[p][i][j] = Sums<C>{0, 0, 0, 0};
 
   SA sa[kDeep];
   SB sb[kDeep];
@@ -687,28 +751,22 @@ __device__ inline void tile_body(const TileArgs& t, uint32_t tile, uint32_t shar
         const char* lb = la + SA::kBytes;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          u32x4 fa[kWM], fb[kWN];
+          u32x4 fa[kWM], fb[kParts][kWN];
 #pragma unroll
           for (int i = 0; i < kWM; ++i) fa[i] = SA::fragment(la, wm + 16 * i, s);
 #pragma unroll
-          for (int j = 0; j < kWN; ++j) fb[j] = SB::fragment(lb, wn + 16 * j, s);
+          for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lb, p * (kBN / 2) + wn + 16 * j, s);
 #pragma unroll
           for (int i = 0; i < kWM; ++i)
 #pragma unroll
-            for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<C>(fb[j], fa[i], acc[0][i][j]);
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int j = 0; j < kWN; ++j) acc[p][i][j] = multiply<C>(fb[p][j], fa[i], acc[p][i][j]);
         }
       });
-  if (t.e.partial) {
-    using G = Groups<C, kWM, kWN>;
-#pragma unroll
-    for (int q = 0; q < G::kCount; ++q) {
-      float v[C::V];
-      G::sums(acc[0], q, v);
-      keep_partial<C>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
-    }
-  } else {
-    finish_all<C, !(kAAlong && kBAlong)>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
-  }
+  finish_tile<C, !(kAAlong && kBAlong)>(t.e, share, acc, m0 + wm, n0 + wn);
 }
 
 // ------------------------------------------------------------------ large products of 16-bit types
@@ -738,12 +796,15 @@ constexpr int kHalfBytes = 128 * 128;
 constexpr int kBlockBytes = 4 * kHalfBytes;
 constexpr int kBigLds = 2 * kBlockBytes;
 
-struct BigArgs {
-  Operand a, b;
-  Epilogue e;
+template <class B, class E>
+struct BigArgsOf {
+  Operand a;
+  B b;
+  E e;
   uint64_t k;
   uint32_t tiles_m, tiles_n;
 };
+using BigArgs = BigArgsOf<Operand, Epilogue>;
 
 // 16 bytes a lane from memory to LDS, lane l's to lds + 16 l; past the
 // resource's range zeros arrive.  All of the offset is in `voffset`: that is
@@ -785,7 +846,7 @@ struct Copier {
     if constexpr (kAlong) {
       const int chunk = (lane & 7) ^ (lane >> 3);
       voffset = (wave * 8 + (lane >> 3)) * stride + chunk * 16;
-      last = static_cast<uint64_t>(blocks - 1) * 64 + chunk * C::V < k ? voffset : kNowhere;
+      last = static_cast<uint64_t>(blocks - 1) * (8 * C::V) + chunk * C::V < k ? voffset : kNowhere;
     } else {
       const int row = wave * 4 + (lane >> 4);
       voffset = row * stride + Stage<C, false, 128, 512>::swizzle(row, lane & 15) * 16;
@@ -818,35 +879,24 @@ struct Copier {
   }
 };
 
-template <class C, bool kAAlong, bool kBAlong>
-__global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
+// The sums of one tile: acc[2 i + j] is a wave's part of quarter (i, j).
+template <class C, bool kAAlong, bool kBAlong, class CA, class CB>
+__device__ inline void big_sums(const CA& ca, const CB& cb, uint32_t blocks, char* lds, int wave, Sums<C> (&acc)[4][4][2]) {
   using SA = Stage<C, kAAlong, 128, 512>;
   using SB = Stage<C, kBAlong, 128, 512>;
-  extern __shared__ __align__(16) char lds[];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-
-  const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
-  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
-
-  Copier<C, kAAlong> ca;
-  Copier<C, kBAlong> cb;
-  const uint32_t blocks = static_cast<uint32_t>((args.k + 63) / 64);
-  ca.init(args.a, m0, args.k, blocks, wave);
-  cb.init(args.b, n0, args.k, blocks, wave);
 
   // Halves of block t: A0, A1, B0, B1.  Both blocks' A halves come first, so
   // that one address register and the instruction's offset reach them all.
   auto region = [](uint32_t t, int which) { return (which >> 1) * (4 * kHalfBytes) + (t & 1) * (2 * kHalfBytes) + (which & 1) * kHalfBytes; };
 
-  f32x4 acc[4][4][2];  // quarter (i, j) is 2 i + j
 #pragma unroll
   for (int p = 0; p < 4; ++p)
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) acc[p][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int y = 0; y < 2; ++y) acc[p][x][y] = Sums<C>{0, 0, 0, 0};
   u32x4 fa[2][2][4], fb[2][2][2];  // [set][step][tile]
 
   ca.copy(lds0 + region(0, 0), 0, 0, wave);
@@ -917,7 +967,23 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   // zeros that copies past the last block still bring must not meet the next
   // workgroup's LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
+template <class C, bool kAAlong, bool kBAlong>
+__global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
+  extern __shared__ __align__(16) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
+
+  Copier<C, kAAlong> ca;
+  Copier<C, kBAlong> cb;
+  const uint32_t blocks = static_cast<uint32_t>((args.k + 63) / 64);
+  ca.init(args.a, m0, args.k, blocks, wave);
+  cb.init(args.b, n0, args.k, blocks, wave);
+  f32x4 acc[4][4][2];
+  big_sums<C, kAAlong, kBAlong>(ca, cb, blocks, lds, wave, acc);
   finish_all<C, !(kAAlong && kBAlong)>(args.e, acc, [&](int p) {
     return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
   });
@@ -977,7 +1043,8 @@ struct SplitStage {
   __device__ inline void load(Feed<F32, kAlong, kT, 256, 2>& f) {
     f.next([&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
   }
-  __device__ inline void load_edge(Feed<F32, kAlong, kT, 256, 2>& f, const Operand& o, uint64_t first, uint64_t k,
+  template <class O>
+  __device__ inline void load_edge(Feed<F32, kAlong, kT, 256, 2>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
     f.edge(o, first, k, k_end, [&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
   }
@@ -1009,24 +1076,27 @@ __device__ inline float value_at(const Operand& o, uint64_t i, uint64_t k, uint6
 // three planes of it let two workgroups share a compute unit: one splits and
 // stores while the other multiplies.  kDeep blocks' loads are in flight, as in
 // linear_tile.
-template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep>
-__device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
+template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
+__device__ inline void split_body(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
   using SA = SplitStage<kAAlong, kBM>;
   using SB = SplitStage<kBAlong, kBN>;
-  constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16;
+  constexpr int kParts = B::kParts;
+  constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
-  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * kBN;
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * (kBN / kParts);
   const int wave = threadIdx.x >> 6;
-  const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2);
+  const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * 64;
   uint64_t k_end = k_first + static_cast<uint64_t>(t.blocks_per_share) * 64;
   if (k_end > t.k) k_end = t.k;
 
-  f32x4 acc[1][kWM][kWN];
+  f32x4 acc[kParts][kWM][kWN];
 #pragma unroll
-  for (int i = 0; i < kWM; ++i)
+  for (int p = 0; p < kParts; ++p)
 #pragma unroll
-    for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int j = 0; j < kWN; ++j) acc[p][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   SA sa[kDeep];
   SB sb[kDeep];
@@ -1041,69 +1111,74 @@ __device__ inline void split_body(const TileArgs& t, uint32_t tile, uint32_t sha
       [&](uint32_t) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          u32x4 fb[3][kWN];
+          u32x4 fb[3][kParts][kWN];
 #pragma unroll
-          for (int p = 0; p < 3; ++p)
+          for (int l = 0; l < 3; ++l)
 #pragma unroll
-            for (int j = 0; j < kWN; ++j) fb[p][j] = SB::fragment(lds + SA::kBytes, p, wn + 16 * j, s);
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int j = 0; j < kWN; ++j)
+                fb[l][p][j] = SB::fragment(lds + SA::kBytes, l, p * (kBN / 2) + wn + 16 * j, s);
 #pragma unroll
           for (int i = 0; i < kWM; ++i) {
             u32x4 fa[3];
 #pragma unroll
-            for (int p = 0; p < 3; ++p) fa[p] = SA::fragment(lds, p, wm + 16 * i, s);
+            for (int l = 0; l < 3; ++l) fa[l] = SA::fragment(lds, l, wm + 16 * i, s);
             // the smaller products first
 #pragma unroll
             for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-              for (int p = 0; p <= sum; ++p)
+              for (int l = 0; l <= sum; ++l)
 #pragma unroll
-                for (int j = 0; j < kWN; ++j) acc[0][i][j] = multiply<BF16>(fb[sum - p][j], fa[p], acc[0][i][j]);
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                  for (int j = 0; j < kWN; ++j) acc[p][i][j] = multiply<BF16>(fb[sum - l][p][j], fa[l], acc[p][i][j]);
           }
         }
       });
 
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < kWM; ++i)
+  for (int p = 0; p < kParts; ++p)
 #pragma unroll
-    for (int j = 0; j < kWN; ++j)
+    for (int i = 0; i < kWM; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) odd |= !(fabsf(acc[0][i][j][c]) < INFINITY);
+      for (int j = 0; j < kWN; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) odd |= !(fabsf(acc[p][i][j][c]) < INFINITY);
   if (__any(odd)) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int i = 0; i < kWM; ++i)
-#pragma unroll
-      for (int j = 0; j < kWN; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (uint64_t k = k_first; k < k_end; k += 4) {
-      float a[kWM], b[kWN];
-#pragma unroll
-      for (int i = 0; i < kWM; ++i) a[i] = value_at<kAAlong>(t.a, m0 + wm + 16 * i + r, k + g, k_end);
-#pragma unroll
-      for (int j = 0; j < kWN; ++j) b[j] = value_at<kBAlong>(t.b, n0 + wn + 16 * j + r, k + g, k_end);
+    for (int p = 0; p < kParts; ++p)
 #pragma unroll
       for (int i = 0; i < kWM; ++i)
 #pragma unroll
-        for (int j = 0; j < kWN; ++j)
-          acc[0][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[i], acc[0][i][j], 0, 0, 0);
+        for (int j = 0; j < kWN; ++j) acc[p][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (uint64_t k = k_first; k < k_end; k += 4) {
+      float a[kWM], b[kParts][kWN];
+#pragma unroll
+      for (int i = 0; i < kWM; ++i) a[i] = value_at<kAAlong>(t.a, m0 + wm + 16 * i + r, k + g, k_end);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int j = 0; j < kWN; ++j) b[p][j] = value_at<kBAlong>(t.b.part(p), n0 + wn + 16 * j + r, k + g, k_end);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+#pragma unroll
+          for (int j = 0; j < kWN; ++j)
+            acc[p][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[p][j], a[i], acc[p][i][j], 0, 0, 0);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kWM; ++i)
+    for (int p = 0; p < kParts; ++p)
 #pragma unroll
-      for (int j = 0; j < kWN; ++j) acc[0][i][j] *= kSplitBack;
-  }
-  if (t.e.partial) {
-    using G = Groups<F32, kWM, kWN>;
+      for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int q = 0; q < G::kCount; ++q) {
-      float v[4];
-      G::sums(acc[0], q, v);
-      keep_partial<F32>(t.e, share, G::row(m0 + wm, q), G::column(n0 + wn, q), v);
-    }
-  } else {
-    finish_all<F32, !(kAAlong && kBAlong)>(t.e, acc, [&](int) { return Corner{m0 + wm, n0 + wn}; });
+        for (int j = 0; j < kWN; ++j) acc[p][i][j] *= kSplitBack;
   }
+  finish_tile<F32, !(kAAlong && kBAlong)>(t.e, share, acc, m0 + wm, n0 + wn);
 }
 
 // ------------------------------------------------------------------ launches of tiles
@@ -1117,8 +1192,8 @@ constexpr int tile_lds() {
     return 2 * (Stage<C, kAAlong, kBM, 256>::kBytes + Stage<C, kBAlong, kBN, 256>::kBytes);
 }
 
-template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN>
-__device__ inline void any_tile(const TileArgs& t, uint32_t tile, uint32_t share, char* lds) {
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, class B, class E>
+__device__ inline void any_tile(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
   if constexpr (C::kElemBytes == 4)
     split_body<kAAlong, kBAlong, kBM, kBN, 1>(t, tile, share, lds);
   else
@@ -1195,6 +1270,28 @@ __global__ __launch_bounds__(256) void linear_join(const Epilogue a, int a_share
 
 // ------------------------------------------------------------------ few rows
 
+// The products of up to 16 kM rows and 16 kN columns from column n0 on, the sums of 4 waves.
+template <class C, int kM, int kN, int kSize>
+__device__ inline void finish_few(const Epilogue& e, const float (&sums)[4][kSize], uint64_t n0) {
+  constexpr int V = C::V;
+  constexpr int kPitch = 16 * kN + 4;
+  constexpr int kGroups = 16 * kM * 16 * kN / V;
+  for (int id = threadIdx.x; id < kGroups; id += 512) {
+    const int m = id / (16 * kN / V), n = id % (16 * kN / V) * V;
+    float v[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) v[c] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
+    if (e.partial)
+      keep_partial<C>(e, blockIdx.y, m, n0 + n, v);
+    else
+      finish<C>(e, m, n0 + n, v);
+  }
+}
+
 // Products of up to 32 rows, where the pass over w bounds: 8 waves share
 // 16 kN rows of w (columns of y) and split k between them, each streams its
 // part of w straight into the MFMA operand registers (no LDS on the way,
@@ -1204,32 +1301,35 @@ __global__ __launch_bounds__(256) void linear_join(const Epilogue a, int a_share
 // the loads of the next kDeep steps are in flight while kDeep are multiplied.
 // 1 x 8192 x 4096 bf16: 12.6 us (5.3 TB/s); 32 x 4096 x 8192: 18.8 us, where
 // reading x, as many bytes a workgroup as its part of w, takes the rest.
-template <class C, int kM, int kN, int kDeep>
-__global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
+// Of a pair of weights a workgroup has 8 kN rows of each.
+template <class C, int kM, int kN, int kDeep, class B, class E>
+__device__ inline void few_body(const TileArgsOf<B, E>& t) {
   constexpr int V = C::V;
   constexpr int kStep = 8 * V;
   constexpr int kPitch = 16 * kN + 4;  // floats; rows 16 apart lie 4 banks apart
-  __shared__ __align__(16) float sums[4][16 * kM * kPitch];
+  constexpr int kOfPart = kN / B::kParts;
+  __shared__ __align__(16) SumOf<C> sums[4][16 * kM * kPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * (16 * kN);
+  const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * (16 * kOfPart);
   const char* w[kN];
   const char* x[kM];
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    const uint64_t n = n0 + 16 * j + r;
-    w[j] = t.b.base + ((n < t.b.rows ? n : t.b.rows - 1) * t.b.stride + g * V) * C::kElemBytes;
+    const Operand& b = t.b.part(j / kOfPart);
+    const uint64_t n = n0 + 16 * (j % kOfPart) + r;
+    w[j] = b.base + ((n < b.rows ? n : b.rows - 1) * b.stride + g * V) * C::kElemBytes;
   }
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     const uint64_t m = 16 * i + r;
     x[i] = t.a.base + ((m < t.a.rows ? m : t.a.rows - 1) * t.a.stride + g * V) * C::kElemBytes;
   }
-  f32x4 acc[kM][kN];
+  Sums<C> acc[kM][kN];
 #pragma unroll
   for (int i = 0; i < kM; ++i)
 #pragma unroll
-    for (int j = 0; j < kN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < kN; ++j) acc[i][j] = Sums<C>{0, 0, 0, 0};
 
   // this wave's whole steps of this share of k: [step, end)
   const uint64_t whole = t.k / kStep;
@@ -1315,26 +1415,17 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
       for (int i = 0; i < kM; ++i)
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          f32x4& at = *reinterpret_cast<f32x4*>(&sums[wave & 3][(16 * i + r) * kPitch + 16 * j + 4 * g]);
+          Sums<C>& at = *reinterpret_cast<Sums<C>*>(&sums[wave & 3][(16 * i + r) * kPitch + 16 * j + 4 * g]);
           at = turn ? acc[i][j] : at + acc[i][j];
         }
     __syncthreads();
   }
-  constexpr int kGroups = 16 * kM * 16 * kN / V;
-  for (int id = threadIdx.x; id < kGroups; id += 512) {
-    const int m = id / (16 * kN / V), n = id % (16 * kN / V) * V;
-    float v[V];
-#pragma unroll
-    for (int c = 0; c < V; ++c) v[c] = 0.0f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int c = 0; c < V; ++c) v[c] += sums[q][m * kPitch + n + c];
-    if (t.e.partial)
-      keep_partial<C>(t.e, blockIdx.y, m, n0 + n, v);
-    else
-      finish<C>(t.e, m, n0 + n, v);
-  }
+  finish_few<C, kM, kN>(t.e, sums, n0);
+}
+
+template <class C, int kM, int kN, int kDeep>
+__global__ __launch_bounds__(512) void linear_few(const TileArgs t) {
+  few_body<C, kM, kN, kDeep>(t);
 }
 
 // ------------------------------------------------------------------ operands laid out anew

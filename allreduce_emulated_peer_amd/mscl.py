@@ -1,7 +1,7 @@
 """Thin ctypes binding over libmscl.so (C ABI in include/mscl.h).
 
-Argument marshalling only: every step of the AllReduce, of the linear layer
-and of layer norm runs in the HIP library.  Names mirror the C entry points without the ``mscl_`` prefix.
+Argument marshalling only: every step of the AllReduce and of the operators
+around it runs in the HIP library.  Names mirror the C entry points without the ``mscl_`` prefix.
 There is no fallback: if the library is missing, loading raises.
 
 Pointers are plain integers (device addresses, e.g. ``tensor.data_ptr()``),
@@ -52,6 +52,9 @@ EXPORTS = (
     "mscl_reduce_scatter", "mscl_allgather", "mscl_channel_selftest", "mscl_allreduce_noalloc",
     "mscl_linear", "mscl_linear_workspace", "mscl_linear_backward", "mscl_linear_backward_workspace",
     "mscl_layer_norm", "mscl_layer_norm_backward", "mscl_layer_norm_backward_workspace",
+    "mscl_gated_linear", "mscl_gated_linear_workspace", "mscl_gated_linear_backward",
+    "mscl_gated_linear_backward_workspace", "mscl_quantize", "mscl_linear_quantized", "mscl_linear_quantized_workspace",
+    "mscl_gated_linear_quantized", "mscl_gated_linear_quantized_workspace",
 )
 
 # the argument records of include/mscl.h, field by field: pointers and sizes
@@ -60,6 +63,11 @@ LINEAR = struct.Struct("14Nii")
 LINEAR_BACKWARD = struct.Struct("16Nii")
 LAYER_NORM = struct.Struct("10Ndii")
 LAYER_NORM_BACKWARD = struct.Struct("13Nii")
+GATED_LINEAR = struct.Struct("17Nii")
+GATED_LINEAR_BACKWARD = struct.Struct("23Nii")
+QUANTIZE = struct.Struct("7Ni0N")
+LINEAR_QUANTIZED = struct.Struct("14Nii")
+GATED_LINEAR_QUANTIZED = struct.Struct("16Nii")
 
 
 class MsclError(RuntimeError):
@@ -124,13 +132,15 @@ def load(path: str = LIB_PATH):
     lib.mscl_channel_set_fault_controls.argtypes = [vp, ctypes.c_uint64, c_int]
     lib.mscl_channel_set_checks.restype = c_int
     lib.mscl_channel_set_checks.argtypes = [vp, c_int, c_int]
-    for name in ("mscl_linear", "mscl_linear_backward", "mscl_layer_norm_backward"):
+    for name in ("mscl_linear", "mscl_linear_backward", "mscl_layer_norm_backward", "mscl_gated_linear",
+                 "mscl_gated_linear_backward", "mscl_linear_quantized", "mscl_gated_linear_quantized"):
         getattr(lib, name).restype = c_int
         getattr(lib, name).argtypes = [ctypes.c_char_p, vp, c_size, vp]
         getattr(lib, name + "_workspace").restype = c_int
         getattr(lib, name + "_workspace").argtypes = [ctypes.c_char_p, ctypes.POINTER(c_size)]
-    lib.mscl_layer_norm.restype = c_int
-    lib.mscl_layer_norm.argtypes = [ctypes.c_char_p, vp]
+    for name in ("mscl_layer_norm", "mscl_quantize"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
     _lib = lib
     return lib
 
@@ -311,6 +321,9 @@ def _need_torch():
 
             @staticmethod
             def backward(ctx, *grads):
+                if "quantize" in ctx.name:
+                    raise RuntimeError(f"{ctx.name}_tensors has no gradient: call it under torch.no_grad() or detach what "
+                                       "it takes or returns")
                 raise RuntimeError(f"{ctx.name}_tensors is not part of autograd's graph: run {ctx.name}_backward_tensors, and "
                                    "call it under torch.no_grad() or detach what it takes or returns")
 
@@ -606,3 +619,270 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
     if need_dx and dy.dim() != 2:
         dx = dx.view(dy.shape)
     return dx, dw, db
+
+
+# ---------------------------------------------------------------- the gated feed-forward block and 8-bit products
+
+def _needs_grad(*tensors):
+    return _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _pair_of_weights(like, k, gate_weight, up_weight):
+    """Both weights as matrices, after their checks."""
+    if gate_weight.dim() != 2 or up_weight.dim() != 2:
+        raise ValueError("gate_weight and up_weight must be matrices")
+    if gate_weight.shape != up_weight.shape:
+        raise ValueError("gate_weight and up_weight must have the same shape")
+    _same_kind(like, "gate_weight", gate_weight)
+    _same_kind(like, "up_weight", up_weight)
+    return _matrix("gate_weight", gate_weight, k), _matrix("up_weight", up_weight, k)
+
+
+def gated_linear_tensors(x, gate_weight, up_weight, gate_bias=None, up_bias=None, activation="silu",
+                         return_preacts=False, stream=None):
+    """mscl_gated_linear on torch tensors: activation(x @ gate_weight.T + gate_bias) * (x @ up_weight.T + up_bias).
+
+    x is (..., in), the weights (out, in), the biases (out), all of one dtype
+    (float32 / float16 / bfloat16) and device; rows may be strided, elements of
+    a row must be contiguous.  activation is a name of ACTIVATION_CODES.
+    Returns y (..., out), or (y, gate, up) with return_preacts: both products
+    with their biases, what gated_linear_backward_tensors needs.  Autograd does
+    not reach through it, as through linear_tensors.
+    """
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = _CODES.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
+    gm, um = _pair_of_weights(x, k, gate_weight, up_weight)
+    for name, bias in (("gate_bias", gate_bias), ("up_bias", up_bias)):
+        if bias is not None:
+            _same_kind(x, name, bias)
+            _vector(name, bias, n)
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    xm = _matrix("x", x, k)
+    rows = xm.shape[0]
+
+    inputs = (x, gate_weight, up_weight, gate_bias, up_bias)
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, inputs, lambda: gated_linear_tensors(*inputs, activation, return_preacts))
+    if _needs_grad(*inputs):
+        return _outside_autograd(lambda: gated_linear_tensors(*inputs, activation, return_preacts), "gated_linear", *inputs)
+    y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    gate, up = (torch.empty_like(y), torch.empty_like(y)) if return_preacts else (None, None)
+    call = GATED_LINEAR.pack(xm.data_ptr(), xm.stride(0), gm.data_ptr(), gm.stride(0), um.data_ptr(), um.stride(0),
+                             _address(gate_bias), _address(up_bias), y.data_ptr(), n, _address(gate), n, _address(up), n,
+                             rows, k, n, dtype, ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_gated_linear_workspace, call, x)
+    status = lib.mscl_gated_linear(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_gated_linear")
+    out = (y, gate, up) if return_preacts else (y,)
+    if x.dim() != 2:
+        out = tuple(t.view(x.shape[:-1] + (n,)) for t in out)
+    return out if return_preacts else out[0]
+
+
+def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activation="silu", need_dx=True, need_dw=True,
+                                  need_db=True, stream=None):
+    """mscl_gated_linear_backward on torch tensors: (dx, dgate_weight, dup_weight, dgate_bias, dup_bias).
+
+    dy is the gradient of y (..., out); gate and up are what
+    gated_linear_tensors returned with return_preacts.  Gradients that are not
+    needed are None (need_dw: both weights', need_db: both biases').
+    """
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = _CODES.get(dy.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {dy.dtype}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
+    wm, vm = _pair_of_weights(dy, k, gate_weight, up_weight)
+    for name, t in (("x", x), ("gate", gate), ("up", up)):
+        _same_kind(dy, name, t)
+    if not dy.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    gm, xm = _matrix("dy", dy, n), _matrix("x", x, k)
+    rows = gm.shape[0]
+    if x.shape[:-1] != dy.shape[:-1]:
+        raise ValueError("dy and x must have the same rows")
+    if gate.shape != dy.shape or up.shape != dy.shape:
+        raise ValueError("gate and up must have dy's shape")
+    zm, um = _matrix("gate", gate, n), _matrix("up", up, n)
+
+    index = dy.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(dy.device, stream, (dy, x, gate_weight, up_weight, gate, up),
+                          lambda: gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activation,
+                                                                need_dx, need_dw, need_db))
+    like = {"dtype": dy.dtype, "device": dy.device}
+    dx = torch.empty((rows, k), **like) if need_dx else None
+    dgw, duw = (torch.empty((n, k), **like), torch.empty((n, k), **like)) if need_dw else (None, None)
+    dgb, dub = (torch.empty((n,), **like), torch.empty((n,), **like)) if need_db else (None, None)
+    call = GATED_LINEAR_BACKWARD.pack(
+        gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), vm.data_ptr(), vm.stride(0),
+        zm.data_ptr(), zm.stride(0), um.data_ptr(), um.stride(0), _address(dx), k, _address(dgw), k, _address(duw), k,
+        _address(dgb), _address(dub), rows, k, n, dtype, ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_gated_linear_backward_workspace, call, dy)
+    status = lib.mscl_gated_linear_backward(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_gated_linear_backward")
+    if need_dx and x.dim() != 2:
+        dx = dx.view(x.shape)
+    return dx, dgw, duw, dgb, dub
+
+
+def quantize_tensors(x, stream=None):
+    """mscl_quantize on a torch tensor: rows (the last dimension) as 8-bit integers and a scale for each.
+
+    Returns (q, scale): int8 of x's shape and float32 of its leading shape, x ~
+    q * scale[..., None].  For a weight (out, in) the scales are those of its
+    outputs.  Autograd does not reach through it.
+    """
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = _CODES.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    shape = x.shape
+    if not shape or shape[-1] == 0:
+        raise ValueError("x must have a last dimension of at least 1")
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    width = shape[-1]
+    xm = _matrix("x", x, width)
+    rows = xm.shape[0]
+
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, (x,), lambda: quantize_tensors(x))
+    if _needs_grad(x):
+        return _outside_autograd(lambda: quantize_tensors(x), "quantize", x)
+    q = torch.empty(shape, dtype=torch.int8, device=x.device)
+    scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    call = QUANTIZE.pack(xm.data_ptr(), xm.stride(0), q.data_ptr(), width, scale.data_ptr(), rows, width, dtype)
+    status = lib.mscl_quantize(call, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_quantize")
+    return q, scale
+
+
+def _int8_rows(name, q, scale, like, shape):
+    """Checks of an 8-bit matrix and its scales, one for each row."""
+    if q.dtype != _torch.int8:
+        raise ValueError(f"{name} must be of torch.int8")
+    if q.device != like.device or scale.device != like.device:
+        raise ValueError(f"{name} and its scales must be on {like.device}")
+    if scale.dtype != _torch.float32 or scale.shape != shape or not scale.is_contiguous():
+        raise ValueError(f"{name}'s scales must be contiguous, float32 and {tuple(shape)}")
+
+
+def _result_type(dtype, tensors):
+    """The code of an 8-bit product's result type, which its biases and residual share."""
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    for name, t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be of {dtype}")
+    return code
+
+
+def linear_quantized_tensors(x, x_scale, weight, weight_scale, bias=None, residual=None, activation="none", dtype=None,
+                        stream=None):
+    """mscl_linear_quantized on torch tensors: activation((x @ weight.T) * x_scale * weight_scale + bias) + residual.
+
+    x (..., in) and weight (out, in) are int8 with in at most 131071, x_scale
+    (...) and weight_scale (out) float32, as quantize_tensors returns them; bias
+    (out), residual (..., out) and the result have `dtype` (float32, float16 or
+    bfloat16, the default).  Rows may be strided, elements of a row must be
+    contiguous.  It has no gradient.
+    """
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = _result_type(dtype, (("bias", bias), ("residual", residual)))
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    if weight.dim() != 2:
+        raise ValueError("weight must be a matrix")
+    n, k = weight.shape
+    _int8_rows("x", x, x_scale, x, x.shape[:-1])
+    _int8_rows("weight", weight, weight_scale, x, (n,))
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    xm, wm = _matrix("x", x, k), _matrix("weight", weight, k)
+    rows = xm.shape[0]
+    if bias is not None:
+        _vector("bias", bias, n)
+        if bias.device != x.device:
+            raise ValueError(f"bias must be on {x.device}")
+    rm = None
+    if residual is not None:
+        if residual.shape != x.shape[:-1] + (n,) or residual.device != x.device:
+            raise ValueError(f"residual must be {tuple(x.shape[:-1]) + (n,)} on {x.device}")
+        rm = _matrix("residual", residual, n)
+
+    inputs = (x, x_scale, weight, weight_scale, bias, residual)
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, inputs, lambda: linear_quantized_tensors(*inputs, activation, dtype))
+    if _needs_grad(*inputs):
+        return _outside_autograd(lambda: linear_quantized_tensors(*inputs, activation, dtype), "linear_quantized", *inputs)
+    y = torch.empty((rows, n), dtype=dtype, device=x.device)
+    call = LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), wm.data_ptr(), wm.stride(0),
+                            weight_scale.data_ptr(), _address(bias), _address(rm), _row_stride(rm), y.data_ptr(), n, rows,
+                            k, n, code, ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_linear_quantized_workspace, call, x)
+    status = lib.mscl_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_linear_quantized")
+    return y if x.dim() == 2 else y.view(x.shape[:-1] + (n,))
+
+
+def gated_linear_quantized_tensors(x, x_scale, gate_weight, gate_scale, up_weight, up_scale, gate_bias=None, up_bias=None,
+                              activation="silu", dtype=None, stream=None):
+    """mscl_gated_linear_quantized on torch tensors: gated_linear_tensors with 8-bit rows and weights.
+
+    Arguments and result are as for linear_quantized_tensors, with two weights of one
+    shape and their scales.  It has no gradient.
+    """
+    torch, lib = _torch or _need_torch(), _lib or load()
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = _result_type(dtype, (("gate_bias", gate_bias), ("up_bias", up_bias)))
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}")
+    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
+    _int8_rows("x", x, x_scale, x, x.shape[:-1])
+    gm, um = _pair_of_weights(x, k, gate_weight, up_weight)
+    _int8_rows("gate_weight", gate_weight, gate_scale, x, (n,))
+    _int8_rows("up_weight", up_weight, up_scale, x, (n,))
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    for name, bias in (("gate_bias", gate_bias), ("up_bias", up_bias)):
+        if bias is not None:
+            _vector(name, bias, n)
+            if bias.device != x.device:
+                raise ValueError(f"{name} must be on {x.device}")
+    xm = _matrix("x", x, k)
+    rows = xm.shape[0]
+
+    inputs = (x, x_scale, gate_weight, gate_scale, up_weight, up_scale, gate_bias, up_bias)
+    index = x.device.index
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(x.device, stream, inputs, lambda: gated_linear_quantized_tensors(*inputs, activation, dtype))
+    if _needs_grad(*inputs):
+        return _outside_autograd(lambda: gated_linear_quantized_tensors(*inputs, activation, dtype), "gated_linear_quantized", *inputs)
+    y = torch.empty((rows, n), dtype=dtype, device=x.device)
+    call = GATED_LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), gm.data_ptr(), gm.stride(0),
+                                  gate_scale.data_ptr(), um.data_ptr(), um.stride(0), up_scale.data_ptr(),
+                                  _address(gate_bias), _address(up_bias), y.data_ptr(), n, rows, k, n, code,
+                                  ACTIVATION_CODES[activation])
+    space, size = _workspace(lib.mscl_gated_linear_quantized_workspace, call, x)
+    status = lib.mscl_gated_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
+    if status:
+        _check(status, "mscl_gated_linear_quantized")
+    return y if x.dim() == 2 else y.view(x.shape[:-1] + (n,))

@@ -596,6 +596,157 @@ mscl_status_t mscl_layer_norm_backward(const mscl_layer_norm_backward_t* call, v
                                        size_t workspace_bytes, void* stream);
 mscl_status_t mscl_layer_norm_backward_workspace(const mscl_layer_norm_backward_t* call, size_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * The gated feed-forward block of a tensor-parallel layer, and the 8-bit
+ * integer products by which such layers are served.  What is said above of
+ * the operators' matrices, sums, streams, workspaces and errors holds here too.
+ */
+typedef struct {
+  const void* x;         /* [rows][in_features] */
+  size_t x_stride;
+  const void* gate_w;    /* [out_features][in_features] */
+  size_t gate_w_stride;
+  const void* up_w;      /* [out_features][in_features] */
+  size_t up_w_stride;
+  const void* gate_bias; /* [out_features], or NULL */
+  const void* up_bias;   /* [out_features], or NULL */
+  void* y;               /* [rows][out_features] */
+  size_t y_stride;
+  void* gate;            /* [rows][out_features]: receives x gate_w^T + gate_bias, or NULL */
+  size_t gate_stride;
+  void* up;              /* [rows][out_features]: receives x up_w^T + up_bias, or NULL */
+  size_t up_stride;
+  size_t rows, in_features, out_features;
+  int dtype;             /* mscl_dtype_t of every matrix */
+  int activation;        /* mscl_activation_t */
+} mscl_gated_linear_t;
+
+/*
+ * y = activation(x gate_w^T + gate_bias) * (x up_w^T + up_bias), of the
+ * unrounded sums, also where `gate` and `up` keep them rounded.  The weights
+ * may be halves of one matrix.  rows or out_features 0: nothing to do;
+ * in_features 0: the sums are 0.
+ */
+mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace, size_t workspace_bytes,
+                                void* stream);
+mscl_status_t mscl_gated_linear_workspace(const mscl_gated_linear_t* call, size_t* bytes);
+
+typedef struct {
+  const void* dy;        /* [rows][out_features] */
+  size_t dy_stride;
+  const void* x;         /* [rows][in_features]; needed for the weights' gradients */
+  size_t x_stride;
+  const void* gate_w;    /* [out_features][in_features]; needed for dx */
+  size_t gate_w_stride;
+  const void* up_w;      /* [out_features][in_features]; needed for dx */
+  size_t up_w_stride;
+  const void* gate;      /* [rows][out_features]: what mscl_gated_linear kept */
+  size_t gate_stride;
+  const void* up;        /* [rows][out_features]: what mscl_gated_linear kept */
+  size_t up_stride;
+  void* dx;              /* [rows][in_features], or NULL */
+  size_t dx_stride;
+  void* dgate_w;         /* [out_features][in_features], or NULL */
+  size_t dgate_w_stride;
+  void* dup_w;           /* [out_features][in_features], or NULL */
+  size_t dup_w_stride;
+  void* dgate_bias;      /* [out_features], or NULL */
+  void* dup_bias;        /* [out_features], or NULL */
+  size_t rows, in_features, out_features;
+  int dtype;
+  int activation;
+} mscl_gated_linear_backward_t;
+
+/*
+ * With dg = dy up activation'(gate) and du = dy activation(gate):
+ *   dx = dg gate_w + du up_w,  dgate_w = dg^T x,  dup_w = du^T x,
+ *   dgate_bias and dup_bias = the columns' sums of dg and du.
+ * dg and du are rounded to the element type before the matrix products, as
+ * the matrix units take that type (the biases' gradients are summed from the
+ * unrounded values): a binary16 value above 65504 becomes infinite.  At gate =
+ * 0 the slope of RELU is 0.  rows 0: the weights' and biases' gradients are 0;
+ * out_features 0: dx is 0.
+ */
+mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* call, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+mscl_status_t mscl_gated_linear_backward_workspace(const mscl_gated_linear_backward_t* call, size_t* bytes);
+
+typedef struct {
+  const void* x;        /* [rows][width] of dtype */
+  size_t x_stride;
+  int8_t* q;            /* [rows][width] */
+  size_t q_stride;
+  float* scale;         /* [rows] */
+  size_t rows, width;
+  int dtype;            /* mscl_dtype_t of x */
+} mscl_quantize_t;
+
+/*
+ * Each row as 8-bit integers and one scale, x ~ q scale.  With size = the
+ * largest |x| of the row, but at least 2^-100:
+ *   q = x (127 / size) rounded to the nearest integer, ties to even;
+ *   scale = size / 127,
+ * each operation in binary32, so q is -127..127.  A row with an infinity or a
+ * NaN has q = 0 and the scale NaN, which makes its products NaN.  It serves a
+ * layer's activations (a scale for each token) and its weights (a scale for
+ * each output).  width must be at least 1; rows 0: nothing to do.  No workspace.
+ */
+mscl_status_t mscl_quantize(const mscl_quantize_t* call, void* stream);
+
+typedef struct {
+  const int8_t* x;       /* [rows][in_features] */
+  size_t x_stride;
+  const float* x_scale;  /* [rows] */
+  const int8_t* w;       /* [out_features][in_features] */
+  size_t w_stride;
+  const float* w_scale;  /* [out_features] */
+  const void* bias;      /* [out_features], or NULL */
+  const void* residual;  /* [rows][out_features], or NULL */
+  size_t residual_stride;
+  void* y;               /* [rows][out_features] */
+  size_t y_stride;
+  size_t rows, in_features, out_features;
+  int dtype;             /* mscl_dtype_t of bias, residual and y */
+  int activation;        /* mscl_activation_t */
+} mscl_linear_quantized_t;
+
+/*
+ * y = activation((x w^T) x_scale w_scale + bias) + residual.  The sums of
+ * products are exact integers, which in_features of at most 131071 keeps
+ * within 32 bits; from there on binary32: the sum (rounded to it) times the
+ * row's scale, times the output's.  `y` may be `residual` (same pointer and
+ * stride).  rows or out_features 0: nothing to do; in_features 0: the sums are 0.
+ */
+mscl_status_t mscl_linear_quantized(const mscl_linear_quantized_t* call, void* workspace, size_t workspace_bytes, void* stream);
+mscl_status_t mscl_linear_quantized_workspace(const mscl_linear_quantized_t* call, size_t* bytes);
+
+typedef struct {
+  const int8_t* x;          /* [rows][in_features] */
+  size_t x_stride;
+  const float* x_scale;     /* [rows] */
+  const int8_t* gate_w;     /* [out_features][in_features] */
+  size_t gate_w_stride;
+  const float* gate_scale;  /* [out_features] */
+  const int8_t* up_w;       /* [out_features][in_features] */
+  size_t up_w_stride;
+  const float* up_scale;    /* [out_features] */
+  const void* gate_bias;    /* [out_features], or NULL */
+  const void* up_bias;      /* [out_features], or NULL */
+  void* y;                  /* [rows][out_features] */
+  size_t y_stride;
+  size_t rows, in_features, out_features;
+  int dtype;                /* mscl_dtype_t of the biases and y */
+  int activation;           /* mscl_activation_t */
+} mscl_gated_linear_quantized_t;
+
+/*
+ * y = activation((x gate_w^T) x_scale gate_scale + gate_bias)
+ *     * ((x up_w^T) x_scale up_scale + up_bias), computed as in mscl_linear_quantized.
+ */
+mscl_status_t mscl_gated_linear_quantized(const mscl_gated_linear_quantized_t* call, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+mscl_status_t mscl_gated_linear_quantized_workspace(const mscl_gated_linear_quantized_t* call, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif
