@@ -12,6 +12,7 @@
 #include "failure.hpp"
 #include "feedforward.hpp"
 #include "forward.hpp"
+#include "gated.hpp"
 #include "launch.hpp"
 #include "linear.hpp"
 
@@ -40,9 +41,68 @@ mscl_status_t check_gated(const mscl_gated_linear_t* c, Spans& s) {
 PairOperand weights_of(const mscl_gated_linear_t& c) {
   return pair_of(c.gate_w, c.gate_w_stride, c.up_w, c.up_w_stride, c.out_features, c.in_features);
 }
-ForwardPlan plan_gated(const mscl_gated_linear_t& c) {
-  return plan_forward(operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c).half, 2, c.rows, c.out_features,
-                      c.in_features, bytes_of(c.dtype));
+// A binary32 operand's parts in a workspace.
+size_t part_bytes(const Operand& o) { return packed_bytes(o); }
+Operand parts_at(const Operand& o, const char* at) {
+  return Operand{at, packed_stride(o.cols), o.rows, round_up(o.cols, 8)};
+}
+mscl_status_t split_operand(const Operand& o, char* to, hipStream_t s) {
+  const SplitArgs a{o, to, packed_stride(o.cols), part_bytes(o)};
+  const uint64_t groups = std::min<uint64_t>(ceil_div(ceil_div(o.cols, 8) * o.rows, 256), 16 * kCus);
+  split_parts<<<static_cast<uint32_t>(groups), 256, 0, s>>>(a);
+  return launched("split_parts");
+}
+// Whether a product of binary32 operands, m x n of `tiles` tiles of 256 x 256,
+// is large enough for its operands to be taken into parts first.
+bool by_parts(int dtype, uint64_t tiles, uint64_t k, uint64_t a_stride, uint64_t b_stride) {
+  const uint64_t limit = uint64_t(1) << 22;  // elements of 2 bytes within a tile's 31-bit offsets
+  return dtype == MSCL_FLOAT32 && tiles >= kCus / 2 && k >= 256 && a_stride < limit && b_stride < limit;
+}
+
+struct GatedPlan {
+  bool parts = false;
+  ForwardPlan tiles;
+  size_t a_part = 0, b_part = 0;  // bytes of one part of x, of a weight
+  size_t bytes = 0;
+};
+
+GatedPlan plan_gated(const mscl_gated_linear_t& c) {
+  GatedPlan p;
+  const Operand x = operand(c.x, c.x_stride, c.rows, c.in_features);
+  const PairOperand w = weights_of(c);
+  const uint64_t stride = packed_stride(c.in_features);
+  p.parts = by_parts(c.dtype, ceil_div(c.rows, 256) * ceil_div(c.out_features, 128), c.in_features, stride, stride);
+  if (p.parts) {
+    p.a_part = part_bytes(x);
+    p.b_part = part_bytes(w.half[0]);
+    p.bytes = 3 * p.a_part + 6 * p.b_part;
+    return p;
+  }
+  p.tiles = plan_forward(x, w.half, 2, c.rows, c.out_features, c.in_features, bytes_of(c.dtype));
+  p.bytes = p.tiles.bytes;
+  return p;
+}
+
+mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, const Gated<F32>& e, char* ws, hipStream_t s) {
+  const Operand x = operand(c.x, c.x_stride, c.rows, c.in_features);
+  const PairOperand w = weights_of(c);
+  char* w_at = ws + 3 * p.a_part;
+  mscl_status_t st = split_operand(x, ws, s);
+  for (int h = 0; h < 2 && st == MSCL_SUCCESS; ++h) st = split_operand(w.half[h], w_at + 3 * h * p.b_part, s);
+  if (st != MSCL_SUCCESS) return st;
+  const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.out_features, 128);
+  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  const hipError_t err = allow_lds<&gated_parts_big>(kBigLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  GatedPartsArgs a;
+  a.parts = {parts_at(x, ws), PairOperand{{parts_at(w.half[0], w_at), parts_at(w.half[1], w_at + 3 * p.b_part)}}, e,
+             round_up(c.in_features, 8), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
+  a.of = {p.a_part, p.b_part};
+  a.a = x;
+  a.b = w;
+  a.k = c.in_features;
+  gated_parts_big<<<static_cast<uint32_t>(tm * tn), 512, kBigLds, s>>>(a);
+  return launched("gated_parts_big");
 }
 
 // ------------------------------------------------------------------ backward pass
@@ -56,8 +116,11 @@ struct GatedBackwardPlan {
   uint32_t groups = 0, rows_per_group = 0;  // of the bias gradients' partial sums
   PairOperand w;
   Operand x;
-  size_t w_bytes = 0;    // of one weight laid out anew
-  size_t d_at = 0, sums_at = 0, dx_at = 0, dw_at = 0, bytes = 0;
+  size_t w_bytes = 0;    // of one weight laid out anew, or of one part of it
+  // large binary32 products: bytes of one part of d and of x
+  bool parts = false;
+  size_t d_part = 0, x_part = 0;
+  size_t d_at = 0, sums_at = 0, parts_at = 0, dx_at = 0, dw_at = 0, bytes = 0;
 };
 
 GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
@@ -66,7 +129,7 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   const uint64_t m = c.rows, k = c.in_features, n = c.out_features;
   const bool want_dw = c.dgate_w || c.dup_w;
   p.products = c.dx || want_dw;
-  p.half = packed_stride(n);
+  p.half = round_up(n, 128);  // whole tiles of the weights' gradients, whatever their size
   size_t at = 0;
   if (p.products) at = round_up(m * 2 * p.half * e, 256);
   plan_groups(m, ceil_div(p.half, 64 * (16 / e)), &p.groups, &p.rows_per_group);
@@ -89,6 +152,12 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
     p.dw = plan_product(Operand{nullptr, 2 * p.half, m, round_up(n, 8)}, false, p.x, false, n, k, m, c.dtype);
     p.dw_big = p.dw.kind == ProductPlan::kBig;
   }
+  if (c.dtype == MSCL_FLOAT32 && m && n && k) {
+    const uint64_t big_of_dw = 2 * ceil_div(n, 256) * big_n, stride = packed_stride(k);
+    p.dx_big = by_parts(c.dtype, big_m * big_n, 2 * n, d.stride, stride);
+    p.dw_big = by_parts(c.dtype, big_of_dw, m, d.stride, stride);
+    p.parts = (p.dx_big && c.dx) || (p.dw_big && want_dw);
+  }
   // what runs as tiles runs in one launch
   const uint64_t across = ceil_div(k, 128);
   const uint64_t large = 2 * across * ((p.dx_big ? 0 : ceil_div(m, 128)) + (p.dw_big ? 0 : ceil_div(n, 128)));
@@ -101,13 +170,29 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
     choose_shares(&p.dw, n, k, m, steps);
   }
   if (!p.dx_big) choose_shares(&p.dx, m, k, n, steps);
+  if (p.parts) {
+    p.parts_at = at;
+    p.d_part = part_bytes(d);
+    at += 3 * p.d_part;
+  }
   p.dx_at = at;
-  if (c.dx) {
+  if (c.dx && p.dx_big && e == 4) {
+    p.w_bytes = part_bytes(p.w.half[0]);
+    at += 6 * p.w_bytes;
+  } else if (c.dx) {
     if (p.pack_w) p.w_bytes = packed_bytes(p.w.half[0]);
-    at += p.dx_big ? 2 * p.w_bytes : round_up(2 * size_t(p.dx.shares) * m * p.dx.partial_stride * 4, 256);
+    if (p.dx_big)
+      at += 2 * p.w_bytes;
+    else if (p.dx.shares > 1)
+      at += round_up(2 * size_t(p.dx.shares) * m * p.dx.partial_stride * 4, 256);
   }
   p.dw_at = at;
-  if (want_dw) at += p.dw_big ? p.dw.bytes() : 2 * p.dw.partial_bytes;
+  if (want_dw && p.dw_big && e == 4) {
+    p.x_part = part_bytes(p.x);
+    at += 3 * p.x_part;
+  } else if (want_dw) {
+    at += p.dw_big ? p.dw.bytes() : 2 * p.dw.partial_bytes;
+  }
   p.bytes = at;
   return p;
 }
@@ -144,6 +229,18 @@ mscl_status_t launch_gated_back(const GatedBackArgs& a, uint32_t groups, hipStre
   return launched("gated_back");
 }
 
+FittedArgs fitted(const TileArgs& t) {
+  FittedArgs f;
+  f.a = t.a;
+  f.b = t.b;
+  static_cast<Epilogue&>(f.e) = t.e;
+  f.k = t.k;
+  f.tiles_m = t.tiles_m;
+  f.tiles_n = t.tiles_n;
+  f.blocks_per_share = t.blocks_per_share;
+  return f;
+}
+
 Epilogue results(void* y, uint64_t stride, uint64_t m, uint64_t n) {
   Epilogue e;
   memset(&e, 0, sizeof e);
@@ -172,6 +269,58 @@ mscl_status_t dx_by_large_tiles(const GatedBackwardPlan& p, const Operand& d, co
   return launched("gated_dx_big");
 }
 
+// dx of binary32 operands; d's parts are there.
+mscl_status_t dx_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c, const Operand& d, char* ws,
+                          hipStream_t s) {
+  char* w_at = ws + p.dx_at;
+  for (int h = 0; h < 2; ++h) {
+    const mscl_status_t st = split_operand(p.w.half[h], w_at + 3 * h * p.w_bytes, s);
+    if (st != MSCL_SUCCESS) return st;
+  }
+  const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.in_features, 256);
+  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  const hipError_t err = allow_lds<&gated_dx_parts_big>(kBigLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  GatedDxPartsArgs a;
+  a.parts = {parts_at(d, ws + p.parts_at),
+             PairOperand{{parts_at(p.w.half[0], w_at), parts_at(p.w.half[1], w_at + 3 * p.w_bytes)}},
+             results(c.dx, c.dx_stride, c.rows, c.in_features), static_cast<uint32_t>(p.half / 64),
+             static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
+  a.of = {p.d_part, p.w_bytes};
+  for (int h = 0; h < 2; ++h) a.a[h] = Operand{d.base + h * p.half * 4, d.stride, c.rows, c.out_features};
+  a.b = p.w;
+  a.k = c.out_features;
+  gated_dx_parts_big<<<static_cast<uint32_t>(tm * tn), 512, kBigLds, s>>>(a);
+  return launched("gated_dx_parts_big");
+}
+
+// Both weights' gradients; d's parts are there.
+mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c, const Operand& d, char* ws,
+                          hipStream_t s) {
+  const mscl_status_t st = split_operand(p.x, ws + p.dw_at, s);
+  if (st != MSCL_SUCCESS) return st;
+  const uint64_t tm = ceil_div(c.out_features, 256), tn = ceil_div(c.in_features, 256);
+  if (tm > kMostGroups / 2 / tn) return bad("the matrices have too many tiles");
+  const hipError_t err = allow_lds<&gated_dw_parts_big>(kBigLds);
+  if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  GatedDwPartsArgs a;
+  for (int h = 0; h < 2; ++h) {
+    a.a[h] = Operand{ws + p.parts_at + h * p.half * 2, 2 * p.half, c.rows, round_up(c.out_features, 8)};
+    a.a32[h] = Operand{d.base + h * p.half * 4, d.stride, c.rows, c.out_features};
+    void* to = h ? c.dup_w : c.dgate_w;
+    // a gradient that is not wanted has no rows
+    a.e[h] = results(to, h ? c.dup_w_stride : c.dgate_w_stride, to ? c.out_features : 0, c.in_features);
+  }
+  a.b = parts_at(p.x, ws + p.dw_at);
+  a.b32 = p.x;
+  a.of = {p.d_part, p.x_part};
+  a.k = c.rows;
+  a.tiles_m = static_cast<uint32_t>(tm);
+  a.tiles_n = static_cast<uint32_t>(tn);
+  gated_dw_parts_big<<<static_cast<uint32_t>(2 * tm * tn), 512, kBigLds, s>>>(a);
+  return launched("gated_dw_parts_big");
+}
+
 // dx, both weights' gradients and the bias gradients' last sums, as far as they
 // run as tiles.
 template <class C>
@@ -187,16 +336,22 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
   const uint64_t dx_tiles = ceil_div(m, p.dx.tile_m) * ceil_div(k, p.dx.tile_n);
   const uint64_t dw_tiles = ceil_div(n, p.dx.tile_m) * ceil_div(k, p.dx.tile_n);
   uint64_t groups = 0;
+  const bool chained = p.dx.shares == 1;
+  a.dx_parts = chained ? 1 : 2;
   for (int h = 0; h < 2; ++h) {
-    const Operand side{d.base + h * p.half * e, d.stride, m, round_up(n, C::V)};
     if (dx) {
-      a.dx[h] = tile_args(p.dx, side, p.w.half[h], n, results(c.dx, c.dx_stride, m, k), nullptr);
-      a.dx[h].e.partial = reinterpret_cast<float*>(ws + p.dx_at) + h * p.dx.shares * m * p.dx.partial_stride;
+      const Operand side{d.base + h * p.half * e, d.stride, m, round_up(n, C::V)};
+      a.dx[h] = fitted(tile_args(p.dx, side, p.w.half[h], n, results(c.dx, c.dx_stride, m, k), nullptr));
+      a.dx[h].e.partial =
+          chained ? nullptr : reinterpret_cast<float*>(ws + p.dx_at) + h * p.dx.shares * m * p.dx.partial_stride;
     }
     void* to = h ? c.dup_w : c.dgate_w;
     const uint64_t stride = h ? c.dup_w_stride : c.dgate_w_stride;
     if (dw) {
-      a.dw[h] = tile_args(p.dw, side, p.x, m, results(to, stride, to ? n : 0, k), ws + p.dw_at + h * p.dw.partial_bytes);
+      // whole tiles of columns: those past the last one meet only rows that are not stored
+      const Operand side{d.base + h * p.half * e, d.stride, m, p.half};
+      a.dw[h] = fitted(
+          tile_args(p.dw, side, p.x, m, results(to, stride, to ? n : 0, k), ws + p.dw_at + h * p.dw.partial_bytes));
       // a gradient that is not wanted has no rows, but takes its place in the launch
       a.dw[h].tiles_m = static_cast<uint32_t>(ceil_div(n, p.dw.tile_m));
     }
@@ -207,7 +362,7 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
     a.dx_tiles = static_cast<uint32_t>(dx_tiles);
     a.dx_groups = static_cast<uint32_t>(dx_tiles * p.dx.shares);
     j.e[0] = a.dx[0].e;
-    j.shares[0] = 2 * p.dx.shares;
+    j.shares[0] = chained ? 1 : 2 * p.dx.shares;
   }
   if (dw) {
     a.dw_tiles = static_cast<uint32_t>(dw_tiles);
@@ -217,7 +372,7 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
       j.shares[1 + h] = p.dw.shares;
     }
   }
-  groups = 2 * (uint64_t(a.dx_groups) + a.dw_groups);
+  groups = uint64_t(a.dx_parts) * a.dx_groups + 2 * uint64_t(a.dw_groups);
   a.db_blocks = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(n, 32)));
   if (db) groups += 2 * uint64_t(a.db_blocks);
   if (groups == 0) return MSCL_SUCCESS;
@@ -259,7 +414,7 @@ mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace
   if (st != MSCL_SUCCESS) return st;
   const mscl_gated_linear_t& c = *call;
   if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
-  const ForwardPlan p = plan_gated(c);
+  const GatedPlan p = plan_gated(c);
   if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
   int cus = 0;
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
@@ -277,7 +432,9 @@ mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace
     e.m = c.rows;
     e.n = c.out_features;
     e.act = c.activation;
-    return forward<decltype(t)>(p, operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c), c.in_features, e,
+    if constexpr (std::is_same<decltype(t), F32>::value)
+      if (p.parts) return gated_by_parts(p, c, e, bytes_at(workspace), static_cast<hipStream_t>(stream));
+    return forward<decltype(t)>(p.tiles, operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c), c.in_features, e,
                                 bytes_at(workspace), static_cast<hipStream_t>(stream));
   });
 }
@@ -338,13 +495,18 @@ mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* cal
   const bool dx_tiles = dx && !p.dx_big, dw_tiles = dw && !p.dw_big;
   const bool db_with_tiles = db && (dx_tiles || dw_tiles);
   if (db && !db_with_tiles && (st = join_columns(c.dtype, join, 2, s)) != MSCL_SUCCESS) return st;
-  if (dx && p.dx_big) {
+  if (p.parts && (dx || dw) && (st = split_operand(d, ws + p.parts_at, s)) != MSCL_SUCCESS) return st;
+  if (dx && p.dx_big && e == 4) {
+    if ((st = dx_by_parts(p, c, d, ws, s)) != MSCL_SUCCESS) return st;
+  } else if (dx && p.dx_big) {
     const Epilogue ex = results(c.dx, c.dx_stride, c.rows, c.in_features);
     st = c.dtype == MSCL_FLOAT16 ? dx_by_large_tiles<F16>(p, d, ex, c.dtype, ws, s)
                                  : dx_by_large_tiles<BF16>(p, d, ex, c.dtype, ws, s);
     if (st != MSCL_SUCCESS) return st;
   }
-  if (dw && p.dw_big) {
+  if (dw && p.dw_big && e == 4) {
+    if ((st = dw_by_parts(p, c, d, ws, s)) != MSCL_SUCCESS) return st;
+  } else if (dw && p.dw_big) {
     ProductPlan dw_plan = p.dw;
     Operand x = p.x;
     char* at = ws + p.dw_at;

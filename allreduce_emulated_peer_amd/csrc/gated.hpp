@@ -1,0 +1,428 @@
+// Kernels of the gated feed-forward block alone: its backward pass, and large
+// binary32 products.  The other forward kernels are feedforward.hpp's.
+//
+//   gated_slope        both sums' gradients, side by side in the workspace, and
+//                      the bias gradients' partial sums
+//   gated_dx_big       input gradient, one product over both weights
+//   gated_back         tiles of all three products in one launch
+//   gated_join         adds their shares of k
+//   split_parts        a binary32 operand as three of bfloat16
+//   gated_parts_big, gated_dx_parts_big, gated_dw_parts_big
+//                      large products of binary32 operands in parts
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mscl.h"
+#include "codec.hpp"
+#include "feedforward.hpp"
+#include "linear.hpp"
+
+namespace mscl {
+
+// ------------------------------------------------------------------ large binary32 products
+
+// A binary32 operand as linear.hpp's three bfloat16 parts, each a matrix of its
+// own in the workspace.  The parts are taken apart once and not in every tile
+// that uses them, and a product is then one of 16 bits whose k is six times as
+// long: block t is block t / 6 of k, of the parts that pair t % 6 names, the
+// smaller products first.
+constexpr int kPairs = 6;
+constexpr uint32_t kPartsOfA = 0 | 1 << 2 | 2 << 4 | 0 << 6 | 1 << 8 | 0 << 10;
+constexpr uint32_t kPartsOfB = 2 | 1 << 2 | 0 << 4 | 1 << 6 | 0 << 8 | 0 << 10;
+
+struct SplitArgs {
+  Operand from;
+  char* to;            // three parts, `part_bytes` apart
+  uint64_t to_stride;  // elements: rows at 128-byte boundaries
+  uint64_t part_bytes;
+};
+
+// 8 values a thread, past the row's end zeros up to a whole vector.  A pass
+// over memory: 4 bytes read and 6 written for each value.
+__global__ __launch_bounds__(256) void split_parts(const SplitArgs a) {
+  const uint64_t per_row = (a.from.cols + 7) / 8, total = per_row * a.from.rows;
+  for (uint64_t id = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; id < total;
+       id += static_cast<uint64_t>(gridDim.x) * 256) {
+    const uint64_t row = id / per_row, col = id % per_row * 8;
+    const int valid = a.from.cols - col < 8 ? static_cast<int>(a.from.cols - col) : 8;
+    const char* p = a.from.base + (row * a.from.stride + col) * 4;
+    const u32x4 lo = load_upto<F32>(p, valid), hi = load_upto<F32>(p + 16, valid - 4);
+    const Parts o = split(lo, hi);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      *reinterpret_cast<u32x4*>(a.to + i * a.part_bytes + (row * a.to_stride + col) * 2) = o.part[i];
+  }
+}
+
+// The copies of an operand that lies in parts.
+template <class Inner>
+struct PartCopier {
+  Inner in;
+  uint64_t part_bytes;
+  uint32_t parts;  // 2 bits for each pair
+  __device__ inline void copy(uint32_t lds, int h, uint32_t t, int wave) const {
+    const uint32_t block = t / kPairs, pair = t - block * kPairs;
+    Inner from = in;
+    from.shift((parts >> (2 * pair) & 3) * part_bytes);
+    from.copy(lds, h, block, wave);
+  }
+};
+
+// A wave's sums of parts to those of the values; where one of the m x n is not
+// finite, all of them again in binary32 from the `chain` products' operands
+// themselves.  What lies past the matrix may be anything and is not looked at.
+// at(p) is where quarter p begins, a_of(h) and b_of(h, p) its operands.
+template <bool kAAlong, bool kBAlong, class At, class OfA, class OfB>
+__device__ inline void finish_parts(f32x4 (&acc)[4][4][2], uint64_t m, uint64_t n, uint64_t k_end, int chain, At&& at,
+                                    OfA&& a_of, OfB&& b_of) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  bool odd = false;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const Corner c = at(p);
+    const int rows = c.first >= m ? 0 : (m - c.first < 64 ? static_cast<int>(m - c.first) : 64);
+    const int cols = c.second >= n ? 0 : (n - c.second < 32 ? static_cast<int>(n - c.second) : 32);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * x + r < rows && 16 * y + 4 * g + i < cols) odd |= !(fabsf(acc[p][x][y][i]) < INFINITY);
+        acc[p][x][y] *= kSplitBack;
+      }
+  }
+  if (!__any(odd)) return;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) acc[p][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const Corner c = at(p);
+    for (int h = 0; h < chain; ++h)
+      for (uint64_t k = 0; k < k_end; k += 4) {
+        float a[4], b[2];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) a[x] = value_at<kAAlong>(a_of(h), c.first + 16 * x + r, k + g, k_end);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) b[y] = value_at<kBAlong>(b_of(h, p), c.second + 16 * y + r, k + g, k_end);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) acc[p][x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[y], a[x], acc[p][x][y], 0, 0, 0);
+      }
+  }
+}
+
+struct PartsOf {
+  uint64_t a_bytes, b_bytes;  // of one part
+};
+
+// forward_big of a pair of binary32 weights in parts; a and b are the operands
+// themselves.
+struct GatedPartsArgs {
+  BigArgsOf<PairOperand, Gated<F32>> parts;
+  PartsOf of;
+  Operand a;
+  PairOperand b;
+  uint64_t k;
+};
+
+__global__ __launch_bounds__(512, 2) void gated_parts_big(const GatedPartsArgs args) {
+  extern __shared__ __align__(16) char lds[];
+  const auto& t = args.parts;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const TileAt at(xcd_run(blockIdx.x, t.tiles_m * t.tiles_n), t.tiles_m, t.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 128;
+  const uint32_t blocks = static_cast<uint32_t>((t.k + 63) / 64);
+  PartCopier<Copier<BF16, true>> ca;
+  PartCopier<PairCopier<BF16>> cb;
+  ca.in.init(t.a, m0, t.k, blocks, wave);
+  cb.in.init(t.b, n0, t.k, blocks, wave);
+  ca.part_bytes = args.of.a_bytes;
+  cb.part_bytes = args.of.b_bytes;
+  ca.parts = kPartsOfA;
+  cb.parts = kPartsOfB;
+  f32x4 acc[4][4][2];
+  big_sums<BF16, true, true>(ca, cb, kPairs * blocks, lds, wave, acc);
+  finish_parts<true, true>(
+      acc, t.e.m, t.e.n, args.k, 1, [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + wn * 32}; },
+      [&](int) -> const Operand& { return args.a; }, [&](int, int p) -> const Operand& { return args.b.half[p & 1]; });
+  finish_blocks<F32, 4, 2, 2>(
+      t.e, [&](int b, int p) -> const f32x4(&)[4][2] { return acc[2 * b + p]; },
+      [&](int b) { return Corner{m0 + b * 128 + wm * 64, n0 + wn * 32}; });
+}
+
+// ------------------------------------------------------------------ backward pass
+
+struct GatedSlopeArgs {
+  const char *dy, *z, *v;  // z: the gate's sums, v: the other's
+  char* d;      // null: not wanted; else rows of dz and dv, `half` columns each
+  float* sums;  // null: no bias gradients; else [gridDim.y][2][cols]
+  uint64_t dy_stride, z_stride, v_stride, half;
+  uint64_t rows, cols;
+  uint32_t rows_per_group;
+  int act;
+};
+
+// dz = dy v act'(z) and dv = dy act(z), and each column's sums of both over
+// this workgroup's rows, in binary32 from the unrounded values: a pass over
+// memory as linear_slope.  Both are rounded to the element type, which is what
+// the matrix units multiply; columns from the last one to `half` become 0.
+template <class C>
+__global__ __launch_bounds__(256) void gated_slope(const GatedSlopeArgs a) {
+  constexpr int V = C::V;
+  constexpr bool kFast = C::kElemBytes == 2;
+  __shared__ float part[2][4][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t n = (static_cast<uint64_t>(blockIdx.x) * 64 + lane) * V;
+  const uint64_t first = static_cast<uint64_t>(blockIdx.y) * a.rows_per_group;
+  uint64_t end = first + a.rows_per_group;
+  if (end > a.rows) end = a.rows;
+  const int valid = n >= a.cols ? 0 : (a.cols - n < V ? static_cast<int>(a.cols - n) : V);
+  float sum[2][V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[0][i] = sum[1][i] = 0.0f;
+  with_activation(a.act, [&](auto act) {
+    with_edges(n - lane * V + 64 * V <= a.cols, [&](auto full) {
+      constexpr int kAct = decltype(act)::value;
+      constexpr bool kFull = decltype(full)::value;
+      constexpr int kRows = 4;  // in flight
+      for (uint64_t m0 = first + wave; m0 < end; m0 += 4 * kRows) {
+        u32x4 dy[kRows], z[kRows], v[kRows];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          const uint64_t m = m0 + 4 * q < end ? m0 + 4 * q : end - 1;
+          const int there = kFull ? V : valid;
+          dy[q] = load_upto<C>(a.dy + (m * a.dy_stride + n) * C::kElemBytes, there);
+          z[q] = load_upto<C>(a.z + (m * a.z_stride + n) * C::kElemBytes, there);
+          v[q] = load_upto<C>(a.v + (m * a.v_stride + n) * C::kElemBytes, there);
+        }
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          if (m0 + 4 * q >= end) continue;
+          float g[V], t[V], w[V];
+          C::unpack(dy[q], g);
+          C::unpack(z[q], t);
+          C::unpack(v[q], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float dz = g[i] * w[i] * slope<kAct, kFast>(t[i]);
+            w[i] = g[i] * activate<kAct, kFast>(t[i]);
+            g[i] = dz;
+            sum[0][i] += g[i];
+            sum[1][i] += w[i];
+          }
+          if (a.d && (kFull || n < a.half)) {
+            char* to = a.d + ((m0 + 4 * q) * 2 * a.half + n) * C::kElemBytes;
+            *reinterpret_cast<u32x4*>(to) = C::pack(g);
+            *reinterpret_cast<u32x4*>(to + a.half * C::kElemBytes) = C::pack(w);
+          }
+        }
+      }
+    });
+  });
+  if (!a.sums) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    part[0][wave][lane * V + i] = sum[0][i];
+    part[1][wave][lane * V + i] = sum[1][i];
+  }
+  __syncthreads();
+  float* out = a.sums + static_cast<uint64_t>(blockIdx.y) * 2 * a.cols;
+  for (int c = threadIdx.x; c < 2 * 64 * V; c += 256) {
+    const int p = c / (64 * V), i = c % (64 * V);
+    const uint64_t col = static_cast<uint64_t>(blockIdx.x) * 64 * V + i;
+    if (col < a.cols) out[p * a.cols + col] = (part[p][0][i] + part[p][1][i]) + (part[p][2][i] + part[p][3][i]);
+  }
+}
+
+// The copies of two weights as one operand whose k runs down the first's rows
+// and then the second's, `turn` blocks each: rows past a weight's end, and whole
+// blocks of them, read as 0.
+template <class C>
+struct ChainCopier {
+  Copier<C, false> first;
+  const char* base;  // of the second weight's tile
+  uint64_t left;
+  uint32_t turn;
+
+  __device__ inline void init(const PairOperand& b, uint64_t n, uint32_t turn_, int wave) {
+    first.init(b.half[0], n, 0, static_cast<uint32_t>((b.half[0].rows + 63) / 64), wave);
+    turn = turn_;
+    const Operand& o = b.half[1];
+    const uint64_t at = n * C::kElemBytes;
+    base = o.base + at;
+    left = (o.rows - 1) * o.stride * C::kElemBytes + o.cols * C::kElemBytes - at;
+  }
+  __device__ inline void shift(uint64_t bytes) {
+    first.base += bytes;
+    base += bytes;
+  }
+  __device__ inline void copy(uint32_t lds, int h, uint32_t t, int wave) const {
+    Copier<C, false> from = first;
+    const bool second = t >= turn;
+    from.base = second ? base : first.base;
+    from.left = second ? left : first.left;
+    from.copy(lds, h, second ? t - turn : t, wave);
+  }
+};
+
+struct GatedDxArgs {
+  Operand a;      // dz and dv side by side
+  PairOperand b;  // the weights, rows equally far apart
+  Epilogue e;
+  uint32_t turn;  // blocks of 64 of one weight's rows
+  uint32_t tiles_m, tiles_n;
+};
+
+// dx = dz wg + dv wu: one product whose k runs over both.
+template <class C>
+__global__ __launch_bounds__(512, 2) void gated_dx_big(const GatedDxArgs args) {
+  extern __shared__ __align__(16) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
+  Copier<C, true> ca;
+  ChainCopier<C> cb;
+  ca.init(args.a, m0, args.a.cols, 2 * args.turn, wave);
+  cb.init(args.b, n0, args.turn, wave);
+  f32x4 acc[4][4][2];
+  big_sums<C, true, false>(ca, cb, 2 * args.turn, lds, wave, acc);
+  finish_all<C, true>(args.e, acc, [&](int p) {
+    return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
+  });
+}
+
+// The same of binary32 operands in parts; a[h] and b are the operands themselves.
+struct GatedDxPartsArgs {
+  GatedDxArgs parts;
+  PartsOf of;
+  Operand a[2];
+  PairOperand b;
+  uint64_t k;  // of one weight
+};
+
+__global__ __launch_bounds__(512, 2) void gated_dx_parts_big(const GatedDxPartsArgs args) {
+  extern __shared__ __align__(16) char lds[];
+  const auto& t = args.parts;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const TileAt at(xcd_run(blockIdx.x, t.tiles_m * t.tiles_n), t.tiles_m, t.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
+  PartCopier<Copier<BF16, true>> ca;
+  PartCopier<ChainCopier<BF16>> cb;
+  ca.in.init(t.a, m0, t.a.cols, 2 * t.turn, wave);
+  cb.in.init(t.b, n0, t.turn, wave);
+  ca.part_bytes = args.of.a_bytes;
+  cb.part_bytes = args.of.b_bytes;
+  ca.parts = kPartsOfA;
+  cb.parts = kPartsOfB;
+  f32x4 acc[4][4][2];
+  big_sums<BF16, true, false>(ca, cb, 2 * kPairs * t.turn, lds, wave, acc);
+  auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
+  finish_parts<true, false>(
+      acc, t.e.m, t.e.n, args.k, 2, corner, [&](int h) -> const Operand& { return args.a[h]; },
+      [&](int h, int) -> const Operand& { return args.b.half[h]; });
+  finish_all<F32, true>(t.e, acc, corner);
+}
+
+// Both weights' gradients of binary32 operands in parts.
+struct GatedDwPartsArgs {
+  Operand a[2], b;    // parts of dz, dv and x
+  Epilogue e[2];
+  PartsOf of;
+  Operand a32[2], b32;
+  uint64_t k;
+  uint32_t tiles_m, tiles_n;  // of one gradient
+};
+
+__global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsArgs args) {
+  extern __shared__ __align__(16) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles;
+  const TileAt at(id % tiles, args.tiles_m, args.tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
+  const uint32_t blocks = static_cast<uint32_t>((args.k + 63) / 64);
+  PartCopier<Copier<BF16, false>> ca, cb;
+  ca.in.init(args.a[h], m0, args.k, blocks, wave);
+  cb.in.init(args.b, n0, args.k, blocks, wave);
+  ca.part_bytes = args.of.a_bytes;
+  cb.part_bytes = args.of.b_bytes;
+  ca.parts = kPartsOfA;
+  cb.parts = kPartsOfB;
+  f32x4 acc[4][4][2];
+  big_sums<BF16, false, false>(ca, cb, kPairs * blocks, lds, wave, acc);
+  auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
+  finish_parts<false, false>(
+      acc, args.e[h].m, args.e[h].n, args.k, 1, corner, [&](int) -> const Operand& { return args.a32[h]; },
+      [&](int, int) -> const Operand& { return args.b32; });
+  finish_all<F32, true>(args.e[h], acc, corner);
+}
+
+// A gradient's sums, whose last tile of columns ends where the matrix does.
+struct Fitted : Epilogue {
+  static constexpr bool kFit = true;
+};
+using FittedArgs = TileArgsOf<Operand, Fitted>;
+
+template <class C, bool kPlain, int kM, int kN>
+__device__ inline void finish_tile(const Fitted& e, uint64_t share, const f32x4 (&acc)[1][kM][kN], uint64_t m0,
+                                   uint64_t n0) {
+  finish_tile<C, kPlain>(static_cast<const Epilogue&>(e), share, acc, m0, n0);
+}
+
+// Tiles of the three products and the bias gradients' last sums in one launch.
+// A tile of dx walks over both weights, or, where there are few tiles, over a
+// share of one of them: dx[h] then writes shares of its own.
+struct GatedBackArgs {
+  FittedArgs dx[2], dw[2];
+  JoinArgs db;
+  uint32_t dx_tiles, dx_groups;  // groups of one of the two: tiles x shares
+  uint32_t dw_tiles, dw_groups;
+  uint32_t db_blocks;
+  uint32_t dx_parts;  // 2; 1: both weights in one tile
+};
+
+template <class C, int kBM, int kBN>
+__global__ __launch_bounds__(256, 2) void gated_back(const GatedBackArgs p) {
+  extern __shared__ __align__(16) char lds[];
+  uint32_t id = blockIdx.x;
+  if (id < p.dx_parts * p.dx_groups) {
+    id = xcd_run(id, p.dx_parts * p.dx_groups);
+    const uint32_t h = id / p.dx_groups, r = id % p.dx_groups;
+    any_tile<C, true, false, kBM, kBN>(p.dx[h], r % p.dx_tiles, r / p.dx_tiles, lds, 3 - static_cast<int>(p.dx_parts));
+    return;
+  }
+  id -= p.dx_parts * p.dx_groups;
+  if (id < 2 * p.dw_groups) {
+    id = xcd_run(id, 2 * p.dw_groups);
+    const uint32_t h = id / p.dw_groups, r = id % p.dw_groups;
+    any_tile<C, false, false, kBM, kBN>(p.dw[h], r % p.dw_tiles, r / p.dw_tiles, lds);
+    return;
+  }
+  id -= 2 * p.dw_groups;
+  join_block<C>(p.db, id % p.db_blocks, id / p.db_blocks);
+}
+
+struct GatedJoinArgs {
+  Epilogue e[3];
+  uint32_t shares[3];
+  uint32_t groups[3];  // workgroups of each; 0: nothing to join
+};
+
+template <class C>
+__global__ __launch_bounds__(256) void gated_join(const GatedJoinArgs p) {
+  uint32_t id = blockIdx.x;
+  int i = 0;
+  while (i < 2 && id >= p.groups[i]) id -= p.groups[i++];
+  join_shares<C>(p.e[i], static_cast<int>(p.shares[i]), static_cast<uint64_t>(id) * 256 + threadIdx.x);
+}
+
+}  // namespace mscl

@@ -49,6 +49,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef u32x4 u32x4_by1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_by4 __attribute__((aligned(4)));
+typedef f32x4 f32x4_by4 __attribute__((aligned(4)));
 
 template <class C>
 __device__ inline u32x4 load_loose(const char* p) {
@@ -70,6 +71,30 @@ __device__ inline u32x4 load_upto(const char* p, int valid) {
   if (valid >= C::V) return load_loose<C>(p);
   u32x4 v = {0u, 0u, 0u, 0u};
   if (valid > 0) v = load_partial<C>(p, 0, valid);
+  return v;
+}
+
+// The same where at least `room` bytes of the row lie before `p`: the vector
+// that ends with the last element, moved down, in place of a load an element.
+template <class C>
+__device__ inline u32x4 load_within(const char* p, int valid, uint64_t room) {
+  if (valid >= C::V) return load_loose<C>(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (valid <= 0) return v;
+  const uint32_t back = (C::V - valid) * C::kElemBytes;
+  if (room < back) return load_partial<C>(p, 0, valid);
+  const u32x4 w = load_loose<C>(p - back);
+  const uint32_t words = back >> 2, bytes = back & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + words == j) lo = w[j];
+      if (i + words + 1 == j) hi = w[j];
+    }
+    v[i] = __builtin_amdgcn_alignbyte(hi, lo, bytes);
+  }
   return v;
 }
 
@@ -283,7 +308,7 @@ __device__ inline void keep_partial(const Epilogue& e, uint64_t share, uint64_t 
   if (m >= e.m || n >= e.n) return;
   float* p = e.partial + (share * e.m + m) * e.partial_stride + n;
 #pragma unroll
-  for (int i = 0; i < C::V; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  for (int i = 0; i < C::V; i += 4) *reinterpret_cast<f32x4_by4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
 }
 
 // Swaps lanes 16..31 (48..63) of a with lanes 0..15 (32..47) of b.
@@ -532,14 +557,14 @@ struct Feed {
   // Whether all of the tile's columns exist.
   __device__ inline bool whole() const { return kAlong || cols >= kT; }
 
-  // fn(chunk, part, address, how many of the part's elements exist) for the
-  // next whole block.
+  // fn(chunk, part, address, how many of the part's elements exist, bytes of the
+  // row before it) for the next whole block.
   template <class Fn>
   __device__ inline void next(Fn&& fn) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, C::V);
+      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, C::V, uint64_t(0));
     const uint64_t by = left > 1 ? step : 0;
     if (left > 1) --left;
 #pragma unroll
@@ -562,7 +587,8 @@ struct Feed {
         valid = k + r < k_end ? static_cast<int64_t>(cols) - c * kChunk : 0;
       const int n = valid < 0 ? 0 : (valid > kChunk ? kChunk : static_cast<int>(valid));
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, n - q * C::V);
+      for (int q = 0; q < kParts; ++q)
+        fn(i, q, chunk(i) + q * 16, n - q * C::V, ((kAlong ? k : first) + c * kChunk + q * C::V) * e);
     }
   }
 };
@@ -647,12 +673,15 @@ struct Stage {
   }
 
   __device__ inline void load(Feed<C, kAlong, kT, kThreads, 1>& f) {
-    f.next([&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
+    f.next([&](int i, int, const char* p, int, uint64_t) { held[i] = load_loose<C>(p); });
   }
   template <class O>
   __device__ inline void load_edge(Feed<C, kAlong, kT, kThreads, 1>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
-    f.edge(o, first, k, k_end, [&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
+    f.edge(o, first, k, k_end,
+           [&](int i, int, const char* p, int valid, uint64_t room) {
+             held[i] = kAlong ? load_within<C>(p, valid, room) : load_upto<C>(p, valid);
+           });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -709,18 +738,35 @@ __device__ inline Sums<C> multiply(const u32x4& b, const u32x4& a, Sums<C> acc) 
   }
 }
 
+// The first column of a tile.  An epilogue with kFit moves the last tile of a
+// kDown operand back to end where the matrix ends, so that its loads need no
+// bound; what it then shares with the tile before has the same bits in both.
+template <class E, class = void>
+struct Fits : std::false_type {};
+template <class E>
+struct Fits<E, std::void_t<decltype(E::kFit)>> : std::true_type {};
+
+template <class E, bool kAlong, int kT>
+__device__ inline uint64_t first_column(uint64_t n0, uint64_t n) {
+  if constexpr (!kAlong && Fits<E>::value) return n >= kT && n0 + kT > n ? n - kT : n0;
+  return n0;
+}
+
 // Any sizes, strides and alignments of a 16-bit type: kBM x kBN tiles by 4
 // waves in a square, 64 k at a time, two LDS buffers.  The next kDeep blocks'
 // loads are in flight in registers.
 // Of a pair of weights a tile has kBN / 2 columns of each.
+// `chain` products of one size, t[0] .. t[chain - 1], are summed into one tile.
 template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
-__device__ inline void tile_body(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
+__device__ inline void tile_body(const TileArgsOf<B, E>* chained, int chain, uint32_t tile, uint32_t share, char* lds) {
+  const TileArgsOf<B, E>& t = chained[0];
   using SA = Stage<C, kAAlong, kBM, 256>;
   using SB = Stage<C, kBAlong, kBN, 256>;
   constexpr int kParts = B::kParts;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
-  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * (kBN / kParts);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM;
+  const uint64_t n0 = first_column<E, kBAlong, kBN>(static_cast<uint64_t>(at.n) * (kBN / kParts), t.e.n);
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * SA::kBlock;
@@ -740,8 +786,10 @@ __device__ inline void tile_body(const TileArgsOf<B, E>& t, uint32_t tile, uint3
   Feed<C, kAAlong, kBM, 256, 1> feed_a;
   Feed<C, kBAlong, kBN, 256, 1> feed_b;
   auto buffer = [&](uint32_t block) { return lds + (block & 1) * (SA::kBytes + SB::kBytes); };
-  walk<kDeep, 2>(
-      t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
+  for (int h = 0; h < chain; ++h) {
+   if (h) __syncthreads();  // the last block is read, as the first one's buffer may be its own
+   walk<kDeep, 2>(
+      chained[h], m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
       [&](int d, uint32_t block) {
         sa[d].store(buffer(block));
         sb[d].store(buffer(block) + SA::kBytes);
@@ -766,6 +814,7 @@ __device__ inline void tile_body(const TileArgsOf<B, E>& t, uint32_t tile, uint3
               for (int j = 0; j < kWN; ++j) acc[p][i][j] = multiply<C>(fb[p][j], fa[i], acc[p][i][j]);
         }
       });
+  }
   finish_tile<C, !(kAAlong && kBAlong)>(t.e, share, acc, m0 + wm, n0 + wn);
 }
 
@@ -853,6 +902,8 @@ struct Copier {
       last = voffset;
     }
   }
+
+  __device__ inline void shift(uint64_t bytes) { base += bytes; }
 
   // past any range, and with any offset added still below 2^32
   static constexpr uint32_t kNowhere = 0x80000000u;
@@ -1041,12 +1092,13 @@ struct SplitStage {
   u32x4 held[kChunks][2];
 
   __device__ inline void load(Feed<F32, kAlong, kT, 256, 2>& f) {
-    f.next([&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
+    f.next([&](int i, int q, const char* p, int, uint64_t) { held[i][q] = load_loose<F32>(p); });
   }
   template <class O>
   __device__ inline void load_edge(Feed<F32, kAlong, kT, 256, 2>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
-    f.edge(o, first, k, k_end, [&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
+    f.edge(o, first, k, k_end,
+           [&](int i, int q, const char* p, int valid, uint64_t) { held[i][q] = load_upto<F32>(p, valid); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -1077,13 +1129,15 @@ __device__ inline float value_at(const Operand& o, uint64_t i, uint64_t k, uint6
 // stores while the other multiplies.  kDeep blocks' loads are in flight, as in
 // linear_tile.
 template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
-__device__ inline void split_body(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
+__device__ inline void split_body(const TileArgsOf<B, E>* chained, int chain, uint32_t tile, uint32_t share, char* lds) {
+  const TileArgsOf<B, E>& t = chained[0];
   using SA = SplitStage<kAAlong, kBM>;
   using SB = SplitStage<kBAlong, kBN>;
   constexpr int kParts = B::kParts;
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
-  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM, n0 = static_cast<uint64_t>(at.n) * (kBN / kParts);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM;
+  const uint64_t n0 = first_column<E, kBAlong, kBN>(static_cast<uint64_t>(at.n) * (kBN / kParts), t.e.n);
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * 64;
@@ -1102,8 +1156,10 @@ __device__ inline void split_body(const TileArgsOf<B, E>& t, uint32_t tile, uint
   SB sb[kDeep];
   Feed<F32, kAAlong, kBM, 256, 2> feed_a;
   Feed<F32, kBAlong, kBN, 256, 2> feed_b;
-  walk<kDeep, 1>(
-      t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
+  for (int h = 0; h < chain; ++h) {
+   if (h) __syncthreads();
+   walk<kDeep, 1>(
+      chained[h], m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
       [&](int d, uint32_t) {
         sa[d].store(lds);
         sb[d].store(lds + SA::kBytes);
@@ -1136,6 +1192,7 @@ __device__ inline void split_body(const TileArgsOf<B, E>& t, uint32_t tile, uint
           }
         }
       });
+  }
 
   bool odd = false;
 #pragma unroll
@@ -1154,14 +1211,15 @@ __device__ inline void split_body(const TileArgsOf<B, E>& t, uint32_t tile, uint
       for (int i = 0; i < kWM; ++i)
 #pragma unroll
         for (int j = 0; j < kWN; ++j) acc[p][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < chain; ++h)
     for (uint64_t k = k_first; k < k_end; k += 4) {
       float a[kWM], b[kParts][kWN];
 #pragma unroll
-      for (int i = 0; i < kWM; ++i) a[i] = value_at<kAAlong>(t.a, m0 + wm + 16 * i + r, k + g, k_end);
+      for (int i = 0; i < kWM; ++i) a[i] = value_at<kAAlong>(chained[h].a, m0 + wm + 16 * i + r, k + g, k_end);
 #pragma unroll
       for (int p = 0; p < kParts; ++p)
 #pragma unroll
-        for (int j = 0; j < kWN; ++j) b[p][j] = value_at<kBAlong>(t.b.part(p), n0 + wn + 16 * j + r, k + g, k_end);
+        for (int j = 0; j < kWN; ++j) b[p][j] = value_at<kBAlong>(chained[h].b.part(p), n0 + wn + 16 * j + r, k + g, k_end);
 #pragma unroll
       for (int p = 0; p < kParts; ++p)
 #pragma unroll
@@ -1193,12 +1251,12 @@ constexpr int tile_lds() {
 }
 
 template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, class B, class E>
-__device__ inline void any_tile(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds) {
+__device__ inline void any_tile(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds, int chain = 1) {
   if constexpr (C::kElemBytes == 4)
-    split_body<kAAlong, kBAlong, kBM, kBN, 1>(t, tile, share, lds);
+    split_body<kAAlong, kBAlong, kBM, kBN, 1>(&t, chain, tile, share, lds);
   else
     // what the registers hold: 256 a lane, of which the larger tile's sums are 64
-    tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 64 ? 4 : (kAAlong && kBAlong ? 2 : 1)>(t, tile, share, lds);
+    tile_body<C, kAAlong, kBAlong, kBM, kBN, kBM == 64 ? 4 : (kAAlong && kBAlong ? 2 : 1)>(&t, chain, tile, share, lds);
 }
 
 // One product: all tiles of the first share of k, then of the next one.

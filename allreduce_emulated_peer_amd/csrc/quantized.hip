@@ -13,6 +13,7 @@
 #include "forward.hpp"
 #include "launch.hpp"
 #include "linear.hpp"
+#include "quantize.hpp"
 
 namespace {
 

@@ -303,11 +303,13 @@ def allreduce_tensors(inputs, outputs, algo: int = ALGO_AUTO, stream=None) -> No
 _torch = None
 _CODES = {}  # torch dtype -> element type code
 _raw_stream = None
+_device = None
+_fresh = None
 _outside_autograd = None
 
 
 def _need_torch():
-    global _torch, _raw_stream, _outside_autograd
+    global _torch, _raw_stream, _device, _fresh, _outside_autograd
     if _torch is None:
         import torch
 
@@ -333,6 +335,10 @@ def _need_torch():
         # the current stream's handle without a Stream object around it (2 us less), where torch has that
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        # (size, stride, dtype) on the current device: 0.8 us, torch.empty 1.6, where torch has it
+        _fresh = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or (
+            lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
         _torch = torch
     return _torch
 
@@ -623,19 +629,50 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
 
 # ---------------------------------------------------------------- the gated feed-forward block and 8-bit products
 
-def _needs_grad(*tensors):
-    return _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _apart(like, name, t):
+    """Raises for a tensor that is not of the others' type or device."""
+    _same_kind(like, name, t)
+    raise ValueError(f"{name} must be on {like.device}")
 
 
-def _pair_of_weights(like, k, gate_weight, up_weight):
-    """Both weights as matrices, after their checks."""
+def _space(query, call):
+    """_workspace on the current device, from a *_workspace function and its name."""
+    need = ctypes.c_size_t()
+    status = query(call, ctypes.byref(need))
+    if status:
+        _check(status, query.__name__)
+    size = need.value
+    return (_fresh((size,), (1,), _torch.uint8), size) if size else (None, 0)
+
+
+def _pair_of_weights(like, index, gate_weight, up_weight):
+    """(out, in) and both weights as matrices, after their checks."""
     if gate_weight.dim() != 2 or up_weight.dim() != 2:
         raise ValueError("gate_weight and up_weight must be matrices")
-    if gate_weight.shape != up_weight.shape:
+    n, k = shape = gate_weight.shape
+    if up_weight.shape != shape:
         raise ValueError("gate_weight and up_weight must have the same shape")
-    _same_kind(like, "gate_weight", gate_weight)
-    _same_kind(like, "up_weight", up_weight)
-    return _matrix("gate_weight", gate_weight, k), _matrix("up_weight", up_weight, k)
+    kind = like.dtype
+    if gate_weight.dtype is not kind or gate_weight.get_device() != index:
+        _apart(like, "gate_weight", gate_weight)
+    if up_weight.dtype is not kind or up_weight.get_device() != index:
+        _apart(like, "up_weight", up_weight)
+    return n, k, _matrix("gate_weight", gate_weight, k), _matrix("up_weight", up_weight, k)
+
+
+def _bias(like, kind, name, t, n):
+    if t.dtype is not kind:
+        raise ValueError(f"{name} must be of {kind}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    _vector(name, t, n)
+
+
+def _any_grad(tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
 
 
 def gated_linear_tensors(x, gate_weight, up_weight, gate_bias=None, up_bias=None, activation="silu",
@@ -650,41 +687,41 @@ def gated_linear_tensors(x, gate_weight, up_weight, gate_bias=None, up_bias=None
     not reach through it, as through linear_tensors.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
-    dtype = _CODES.get(x.dtype)
+    kind = x.dtype
+    dtype, act = _CODES.get(kind), ACTIVATION_CODES.get(activation)
     if dtype is None:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unsupported dtype {kind}")
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
-    gm, um = _pair_of_weights(x, k, gate_weight, up_weight)
-    for name, bias in (("gate_bias", gate_bias), ("up_bias", up_bias)):
-        if bias is not None:
-            _same_kind(x, name, bias)
-            _vector(name, bias, n)
-    if not x.is_cuda:
+    index = x.get_device()
+    n, k, gm, um = _pair_of_weights(x, index, gate_weight, up_weight)
+    if gate_bias is not None:
+        _bias(x, kind, "gate_bias", gate_bias, n)
+    if up_bias is not None:
+        _bias(x, kind, "up_bias", up_bias, n)
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
     xm = _matrix("x", x, k)
     rows = xm.shape[0]
 
     inputs = (x, gate_weight, up_weight, gate_bias, up_bias)
-    index = x.device.index
-    if stream is not None or index != torch.cuda.current_device():
+    if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: gated_linear_tensors(*inputs, activation, return_preacts))
-    if _needs_grad(*inputs):
+    if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: gated_linear_tensors(*inputs, activation, return_preacts), "gated_linear", *inputs)
-    y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
-    gate, up = (torch.empty_like(y), torch.empty_like(y)) if return_preacts else (None, None)
+    size, stride = (rows, n), (n, 1)
+    y = _fresh(size, stride, kind)
+    gate, up = (_fresh(size, stride, kind), _fresh(size, stride, kind)) if return_preacts else (None, None)
     call = GATED_LINEAR.pack(xm.data_ptr(), xm.stride(0), gm.data_ptr(), gm.stride(0), um.data_ptr(), um.stride(0),
                              _address(gate_bias), _address(up_bias), y.data_ptr(), n, _address(gate), n, _address(up), n,
-                             rows, k, n, dtype, ACTIVATION_CODES[activation])
-    space, size = _workspace(lib.mscl_gated_linear_workspace, call, x)
+                             rows, k, n, dtype, act)
+    space, size = _space(lib.mscl_gated_linear_workspace, call)
     status = lib.mscl_gated_linear(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear")
-    out = (y, gate, up) if return_preacts else (y,)
-    if x.dim() != 2:
-        out = tuple(t.view(x.shape[:-1] + (n,)) for t in out)
-    return out if return_preacts else out[0]
+    if not return_preacts:
+        return y if xm is x else y.view(x.shape[:-1] + (n,))
+    return (y, gate, up) if xm is x else tuple(t.view(x.shape[:-1] + (n,)) for t in (y, gate, up))
 
 
 def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activation="silu", need_dx=True, need_dw=True,
@@ -696,43 +733,44 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
     needed are None (need_dw: both weights', need_db: both biases').
     """
     torch, lib = _torch or _need_torch(), _lib or load()
-    dtype = _CODES.get(dy.dtype)
+    kind = dy.dtype
+    dtype, act = _CODES.get(kind), ACTIVATION_CODES.get(activation)
     if dtype is None:
-        raise ValueError(f"unsupported dtype {dy.dtype}")
-    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unsupported dtype {kind}")
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
-    wm, vm = _pair_of_weights(dy, k, gate_weight, up_weight)
+    index = dy.get_device()
+    n, k, wm, vm = _pair_of_weights(dy, index, gate_weight, up_weight)
     for name, t in (("x", x), ("gate", gate), ("up", up)):
-        _same_kind(dy, name, t)
-    if not dy.is_cuda:
+        if t.dtype is not kind or t.get_device() != index:
+            _apart(dy, name, t)
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
-    gm, xm = _matrix("dy", dy, n), _matrix("x", x, k)
-    rows = gm.shape[0]
-    if x.shape[:-1] != dy.shape[:-1]:
+    shape = dy.shape
+    if x.shape[:-1] != shape[:-1]:
         raise ValueError("dy and x must have the same rows")
-    if gate.shape != dy.shape or up.shape != dy.shape:
+    if gate.shape != shape or up.shape != shape:
         raise ValueError("gate and up must have dy's shape")
+    gm, xm = _matrix("dy", dy, n), _matrix("x", x, k)
     zm, um = _matrix("gate", gate, n), _matrix("up", up, n)
+    rows = gm.shape[0]
 
-    index = dy.device.index
-    if stream is not None or index != torch.cuda.current_device():
+    if stream is not None or index != _device():
         return _elsewhere(dy.device, stream, (dy, x, gate_weight, up_weight, gate, up),
                           lambda: gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activation,
                                                                 need_dx, need_dw, need_db))
-    like = {"dtype": dy.dtype, "device": dy.device}
-    dx = torch.empty((rows, k), **like) if need_dx else None
-    dgw, duw = (torch.empty((n, k), **like), torch.empty((n, k), **like)) if need_dw else (None, None)
-    dgb, dub = (torch.empty((n,), **like), torch.empty((n,), **like)) if need_db else (None, None)
+    dx = _fresh((rows, k), (k, 1), kind) if need_dx else None
+    dgw, duw = (_fresh((n, k), (k, 1), kind), _fresh((n, k), (k, 1), kind)) if need_dw else (None, None)
+    dgb, dub = (_fresh((n,), (1,), kind), _fresh((n,), (1,), kind)) if need_db else (None, None)
     call = GATED_LINEAR_BACKWARD.pack(
         gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), vm.data_ptr(), vm.stride(0),
         zm.data_ptr(), zm.stride(0), um.data_ptr(), um.stride(0), _address(dx), k, _address(dgw), k, _address(duw), k,
-        _address(dgb), _address(dub), rows, k, n, dtype, ACTIVATION_CODES[activation])
-    space, size = _workspace(lib.mscl_gated_linear_backward_workspace, call, dy)
+        _address(dgb), _address(dub), rows, k, n, dtype, act)
+    space, size = _space(lib.mscl_gated_linear_backward_workspace, call)
     status = lib.mscl_gated_linear_backward(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear_backward")
-    if need_dx and x.dim() != 2:
+    if need_dx and xm is not x:
         dx = dx.view(x.shape)
     return dx, dgw, duw, dgb, dub
 
@@ -751,49 +789,37 @@ def quantize_tensors(x, stream=None):
     shape = x.shape
     if not shape or shape[-1] == 0:
         raise ValueError("x must have a last dimension of at least 1")
-    if not x.is_cuda:
+    index = x.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
     width = shape[-1]
     xm = _matrix("x", x, width)
     rows = xm.shape[0]
 
-    index = x.device.index
-    if stream is not None or index != torch.cuda.current_device():
+    if stream is not None or index != _device():
         return _elsewhere(x.device, stream, (x,), lambda: quantize_tensors(x))
-    if _needs_grad(x):
+    if x.requires_grad and torch.is_grad_enabled():
         return _outside_autograd(lambda: quantize_tensors(x), "quantize", x)
-    q = torch.empty(shape, dtype=torch.int8, device=x.device)
-    scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    q, scale = _fresh((rows, width), (width, 1), torch.int8), _fresh((rows,), (1,), torch.float32)
     call = QUANTIZE.pack(xm.data_ptr(), xm.stride(0), q.data_ptr(), width, scale.data_ptr(), rows, width, dtype)
     status = lib.mscl_quantize(call, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_quantize")
-    return q, scale
+    return (q, scale) if xm is x else (q.view(shape), scale.view(shape[:-1]))
 
 
-def _int8_rows(name, q, scale, like, shape):
+def _int8_rows(like, index, name, q, scale, shape):
     """Checks of an 8-bit matrix and its scales, one for each row."""
-    if q.dtype != _torch.int8:
+    if q.dtype is not _torch.int8:
         raise ValueError(f"{name} must be of torch.int8")
-    if q.device != like.device or scale.device != like.device:
+    if q.get_device() != index or scale.get_device() != index:
         raise ValueError(f"{name} and its scales must be on {like.device}")
-    if scale.dtype != _torch.float32 or scale.shape != shape or not scale.is_contiguous():
+    if scale.dtype is not _torch.float32 or scale.shape != shape or not scale.is_contiguous():
         raise ValueError(f"{name}'s scales must be contiguous, float32 and {tuple(shape)}")
 
 
-def _result_type(dtype, tensors):
-    """The code of an 8-bit product's result type, which its biases and residual share."""
-    code = _CODES.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}")
-    for name, t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be of {dtype}")
-    return code
-
-
 def linear_quantized_tensors(x, x_scale, weight, weight_scale, bias=None, residual=None, activation="none", dtype=None,
-                        stream=None):
+                             stream=None):
     """mscl_linear_quantized on torch tensors: activation((x @ weight.T) * x_scale * weight_scale + bias) + residual.
 
     x (..., in) and weight (out, in) are int8 with in at most 131071, x_scale
@@ -803,86 +829,92 @@ def linear_quantized_tensors(x, x_scale, weight, weight_scale, bias=None, residu
     contiguous.  It has no gradient.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
-    dtype = torch.bfloat16 if dtype is None else dtype
-    code = _result_type(dtype, (("bias", bias), ("residual", residual)))
-    if activation not in ACTIVATION_CODES:
+    if dtype is None:
+        dtype = torch.bfloat16
+    code, act = _CODES.get(dtype), ACTIVATION_CODES.get(activation)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
     if weight.dim() != 2:
         raise ValueError("weight must be a matrix")
+    index = x.get_device()
     n, k = weight.shape
-    _int8_rows("x", x, x_scale, x, x.shape[:-1])
-    _int8_rows("weight", weight, weight_scale, x, (n,))
-    if not x.is_cuda:
+    leading = x.shape[:-1]
+    _int8_rows(x, index, "x", x, x_scale, leading)
+    _int8_rows(x, index, "weight", weight, weight_scale, (n,))
+    if bias is not None:
+        _bias(x, dtype, "bias", bias, n)
+    if residual is not None and residual.dtype is not dtype:
+        raise ValueError(f"residual must be of {dtype}")
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
     xm, wm = _matrix("x", x, k), _matrix("weight", weight, k)
     rows = xm.shape[0]
-    if bias is not None:
-        _vector("bias", bias, n)
-        if bias.device != x.device:
-            raise ValueError(f"bias must be on {x.device}")
     rm = None
     if residual is not None:
-        if residual.shape != x.shape[:-1] + (n,) or residual.device != x.device:
-            raise ValueError(f"residual must be {tuple(x.shape[:-1]) + (n,)} on {x.device}")
+        if residual.shape != leading + (n,) or residual.get_device() != index:
+            raise ValueError(f"residual must be {tuple(leading) + (n,)} on {x.device}")
         rm = _matrix("residual", residual, n)
 
     inputs = (x, x_scale, weight, weight_scale, bias, residual)
-    index = x.device.index
-    if stream is not None or index != torch.cuda.current_device():
+    if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: linear_quantized_tensors(*inputs, activation, dtype))
-    if _needs_grad(*inputs):
+    if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: linear_quantized_tensors(*inputs, activation, dtype), "linear_quantized", *inputs)
-    y = torch.empty((rows, n), dtype=dtype, device=x.device)
+    y = _fresh((rows, n), (n, 1), dtype)
     call = LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), wm.data_ptr(), wm.stride(0),
-                            weight_scale.data_ptr(), _address(bias), _address(rm), _row_stride(rm), y.data_ptr(), n, rows,
-                            k, n, code, ACTIVATION_CODES[activation])
-    space, size = _workspace(lib.mscl_linear_quantized_workspace, call, x)
+                                 weight_scale.data_ptr(), _address(bias), _address(rm), _row_stride(rm), y.data_ptr(), n,
+                                 rows, k, n, code, act)
+    space, size = _space(lib.mscl_linear_quantized_workspace, call)
     status = lib.mscl_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_linear_quantized")
-    return y if x.dim() == 2 else y.view(x.shape[:-1] + (n,))
+    return y if xm is x else y.view(leading + (n,))
 
 
 def gated_linear_quantized_tensors(x, x_scale, gate_weight, gate_scale, up_weight, up_scale, gate_bias=None, up_bias=None,
-                              activation="silu", dtype=None, stream=None):
+                                   activation="silu", dtype=None, stream=None):
     """mscl_gated_linear_quantized on torch tensors: gated_linear_tensors with 8-bit rows and weights.
 
-    Arguments and result are as for linear_quantized_tensors, with two weights of one
-    shape and their scales.  It has no gradient.
+    Arguments and result are as for linear_quantized_tensors, with two weights of
+    one shape and their scales.  It has no gradient.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
-    dtype = torch.bfloat16 if dtype is None else dtype
-    code = _result_type(dtype, (("gate_bias", gate_bias), ("up_bias", up_bias)))
-    if activation not in ACTIVATION_CODES:
+    if dtype is None:
+        dtype = torch.bfloat16
+    code, act = _CODES.get(dtype), ACTIVATION_CODES.get(activation)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    n, k = gate_weight.shape if gate_weight.dim() == 2 else (0, 0)
-    _int8_rows("x", x, x_scale, x, x.shape[:-1])
-    gm, um = _pair_of_weights(x, k, gate_weight, up_weight)
-    _int8_rows("gate_weight", gate_weight, gate_scale, x, (n,))
-    _int8_rows("up_weight", up_weight, up_scale, x, (n,))
-    if not x.is_cuda:
+    index = x.get_device()
+    leading = x.shape[:-1]
+    _int8_rows(x, index, "x", x, x_scale, leading)
+    n, k, gm, um = _pair_of_weights(x, index, gate_weight, up_weight)
+    _int8_rows(x, index, "gate_weight", gate_weight, gate_scale, (n,))
+    _int8_rows(x, index, "up_weight", up_weight, up_scale, (n,))
+    if gate_bias is not None:
+        _bias(x, dtype, "gate_bias", gate_bias, n)
+    if up_bias is not None:
+        _bias(x, dtype, "up_bias", up_bias, n)
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
-    for name, bias in (("gate_bias", gate_bias), ("up_bias", up_bias)):
-        if bias is not None:
-            _vector(name, bias, n)
-            if bias.device != x.device:
-                raise ValueError(f"{name} must be on {x.device}")
     xm = _matrix("x", x, k)
     rows = xm.shape[0]
 
     inputs = (x, x_scale, gate_weight, gate_scale, up_weight, up_scale, gate_bias, up_bias)
-    index = x.device.index
-    if stream is not None or index != torch.cuda.current_device():
+    if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: gated_linear_quantized_tensors(*inputs, activation, dtype))
-    if _needs_grad(*inputs):
-        return _outside_autograd(lambda: gated_linear_quantized_tensors(*inputs, activation, dtype), "gated_linear_quantized", *inputs)
-    y = torch.empty((rows, n), dtype=dtype, device=x.device)
+    if torch.is_grad_enabled() and _any_grad(inputs):
+        return _outside_autograd(lambda: gated_linear_quantized_tensors(*inputs, activation, dtype),
+                                 "gated_linear_quantized", *inputs)
+    y = _fresh((rows, n), (n, 1), dtype)
     call = GATED_LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), gm.data_ptr(), gm.stride(0),
-                                  gate_scale.data_ptr(), um.data_ptr(), um.stride(0), up_scale.data_ptr(),
-                                  _address(gate_bias), _address(up_bias), y.data_ptr(), n, rows, k, n, code,
-                                  ACTIVATION_CODES[activation])
-    space, size = _workspace(lib.mscl_gated_linear_quantized_workspace, call, x)
+                                       gate_scale.data_ptr(), um.data_ptr(), um.stride(0), up_scale.data_ptr(),
+                                       _address(gate_bias), _address(up_bias), y.data_ptr(), n, rows, k, n, code, act)
+    space, size = _space(lib.mscl_gated_linear_quantized_workspace, call)
     status = lib.mscl_gated_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear_quantized")
-    return y if x.dim() == 2 else y.view(x.shape[:-1] + (n,))
+    return y if xm is x else y.view(leading + (n,))

@@ -156,7 +156,7 @@ LARGE = [(2304, 1024, 2048, "plain"), (2100, 1040, 2000, "plain"), (2100, 1040, 
          (4097, 576, 1040, "plain")]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,k,n,form", LARGE)
 def test_large_gated_products(dtype, m, k, n, form):
     gen = torch.Generator().manual_seed(56)
@@ -171,7 +171,7 @@ def test_large_gated_products(dtype, m, k, n, form):
 
 
 # k and n large enough that the input gradient, the weights' gradients or both run by large tiles
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,k,n,form", [(2304, 4096, 512, "plain"), (300, 4096, 2304, "plain"), (2100, 4000, 2056, "columns"),
                                         (2300, 4099, 1955, "odd"), (2200, 4104, 200, "plain")])
 def test_large_gated_gradients(dtype, m, k, n, form):
@@ -187,6 +187,43 @@ def test_large_gated_gradients(dtype, m, k, n, form):
         F.assert_within(g, want, name)
     for a, b in zip(got, M.gated_linear_backward_tensors(*there, "gelu")):
         assert torch.equal(a, b)
+
+
+def test_large_binary32_products_with_infinities_nan_and_far_values():
+    """What the bfloat16 parts of a value cannot hold: the tiles with such sums are summed again in binary32."""
+    gen = torch.Generator().manual_seed(59)
+    m, k, n = 2100, 4100, 1030
+    x, wg, wu, _, _ = gated_case(gen, m, k, n, torch.float32, bias=False)
+    x[5, 3], x[7, k - 1], wu[11, 40] = math.inf, math.nan, -math.inf
+    x[9] *= 2.0 ** 108
+    x[300:, 40] = x[300:, 40].abs() + 1
+    x[:300, 40] = -x[:300, 40].abs() - 1
+    note("large binary32 product with infinities")
+    y, gate, up = M.gated_linear_tensors(x.cuda(), wg.cuda(), wu.cuda(), activation="none", return_preacts=True)
+    bad = torch.zeros(m, n, dtype=torch.bool)
+    bad[[5, 7]] = True
+    assert not bool(torch.isfinite(gate.cpu()[bad]).any()) and bool(torch.isnan(gate[7]).all())
+    assert torch.equal(up[300:, 11].cpu(), torch.full((m - 300,), -math.inf))
+    ok = [i for i in range(m) if i not in (5, 7)]
+    cols = [i for i in range(n) if i != 11]
+    c = x[ok].cuda(), wg[cols].cuda(), wu[cols].cuda()
+    _, want_gate, want_up = F.gated_linear(*c, None, None, "none")
+    F.assert_within(gate[ok][:, cols], want_gate, "gate")
+    F.assert_within(up[ok][:, cols], want_up, "up")
+
+    note("large binary32 gradients with infinities")
+    dy, z, v = (normal(gen, m, n, scale=s) for s in (1.0, 1.5, 1.0))
+    dy[5, 3], dy[7, 12] = math.inf, math.nan
+    dy[9] *= 2.0 ** 108
+    x, wg, wu, _, _ = gated_case(gen, m, k, n, torch.float32, bias=False)
+    got = M.gated_linear_backward_tensors(*[t.cuda() for t in (dy, x, wg, wu, z, v)], "none")
+    assert not bool(torch.isfinite(got[0][[5, 7]]).any()) and not bool(torch.isfinite(got[1][[3, 12]]).any())
+    c = [t.cuda() for t in (dy[ok], x, wg, wu, z[ok], v[ok])]
+    F.assert_within(got[0][ok], F.gated_linear_backward(c[0], x[ok].cuda(), *c[2:], "none")[0], "dx")
+    cols = [i for i in range(n) if i not in (3, 12)]
+    c = [t.cuda() for t in (dy[:, cols], x, wg[cols], wu[cols], z[:, cols], v[:, cols])]
+    for g, want, name in zip(got[1:], F.gated_linear_backward(*c, "none")[1:], ("dwg", "dwu", "dbg", "dbu")):
+        F.assert_within(g[cols], want, name)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
