@@ -140,6 +140,15 @@ mscl_status_t launch_forward_tile(const TileArgsOf<B, E>& t, uint32_t groups, hi
   return launched("forward_tile");
 }
 
+// Adds the shares of k at e.partial and finishes the sums.
+template <class C, class E>
+mscl_status_t join_forward(const E& e, uint32_t shares, hipStream_t stream) {
+  const uint64_t joins = ceil_div(ceil_div(e.n, OutOf<E>::V) * e.m, 256);
+  if (joins > kMostGroups) return bad("the matrices have too many tiles");
+  forward_join<C, E><<<static_cast<uint32_t>(joins), 256, 0, stream>>>(e, static_cast<int>(shares));
+  return launched("forward_join");
+}
+
 template <class C, class B, class E>
 mscl_status_t forward(const ForwardPlan& p, Operand a, B b, uint64_t k, E e, char* workspace, hipStream_t stream) {
   const uint64_t tm = ceil_div(e.m, p.tile_m), tn = ceil_div(e.n, p.outs);
@@ -181,11 +190,7 @@ mscl_status_t forward(const ForwardPlan& p, Operand a, B b, uint64_t k, E e, cha
   } else {
     st = launch_forward_tile<C, 64, 64 * B::kParts>(t, groups * p.shares, stream);
   }
-  if (st != MSCL_SUCCESS || p.shares == 1) return st;
-  const uint64_t joins = ceil_div(ceil_div(e.n, OutOf<E>::V) * e.m, 256);
-  if (joins > kMostGroups) return bad("the matrices have too many tiles");
-  forward_join<C, E><<<static_cast<uint32_t>(joins), 256, 0, stream>>>(e, static_cast<int>(p.shares));
-  return launched("forward_join");
+  return st != MSCL_SUCCESS || p.shares == 1 ? st : join_forward<C>(e, p.shares, stream);
 }
 
 }  // namespace launch

@@ -52,15 +52,47 @@ mscl_status_t split_operand(const Operand& o, char* to, hipStream_t s) {
   split_parts<<<static_cast<uint32_t>(groups), 256, 0, s>>>(a);
   return launched("split_parts");
 }
-// Whether a product of binary32 operands, m x n of `tiles` tiles of 256 x 256,
-// is large enough for its operands to be taken into parts first.
-bool by_parts(int dtype, uint64_t tiles, uint64_t k, uint64_t a_stride, uint64_t b_stride) {
+// How a product of binary32 operands in parts runs, if at all.  Its tiles of
+// 256 x 256 take 6 x 1.4 us a block of k whether or not they fill the device, so
+// k is split where they would leave much of it idle, and the shares' sums (and
+// the parts themselves, 10 bytes a value) are a pass over memory at 5 TB/s.
+// linear_tile's kind, which takes operands into parts in every tile, reaches 130
+// to 165 TFLOP/s.  Forward, us by parts and by those tiles: 1024 x 4096 -> 4096
+// 389 and 509, 2048 x 2048 -> 2048 203 and 260, 512 x 4096 -> 4096 249 and 205.
+struct PartsPlan {
+  bool on = false;
+  uint32_t blocks = 0, blocks_per_share = 0, shares = 1;
+  uint64_t partial_stride = 0;
+  size_t partial_bytes = 0;  // of one product
+};
+
+// `products` of m x n with `blocks` blocks of k each, from `values` values of
+// operands; `flops` in all.
+PartsPlan plan_parts(int dtype, uint64_t tiles, uint64_t products, uint64_t m, uint64_t n, uint64_t blocks, double values,
+                     double flops, uint64_t a_stride, uint64_t b_stride) {
+  PartsPlan p;
   const uint64_t limit = uint64_t(1) << 22;  // elements of 2 bytes within a tile's 31-bit offsets
-  return dtype == MSCL_FLOAT32 && tiles >= kCus / 2 && k >= 256 && a_stride < limit && b_stride < limit;
+  if (dtype != MSCL_FLOAT32 || a_stride >= limit || b_stride >= limit || blocks < 4 || blocks >= (1u << 24)) return p;
+  double best = flops / 160e6;  // us
+  for (uint64_t shares = 1; shares <= 8 && 4 * shares <= blocks; ++shares) {
+    const uint64_t per = ceil_div(blocks, shares);
+    if (ceil_div(blocks, per) != shares) continue;
+    double us = static_cast<double>(ceil_div(tiles * products * shares, kCus)) * per * 6 * 1.4 + values * 10 / 5e6 + 8;
+    if (shares > 1) us += 8.0 * shares * products * m * n / 5e6 + 4;
+    if (us >= best) continue;
+    best = us;
+    p.on = true;
+    p.shares = static_cast<uint32_t>(shares);
+    p.blocks_per_share = static_cast<uint32_t>(per);
+  }
+  p.blocks = static_cast<uint32_t>(blocks);
+  p.partial_stride = round_up(n, 8);
+  if (p.on && p.shares > 1) p.partial_bytes = round_up(p.shares * m * p.partial_stride * 4, 256);
+  return p;
 }
 
 struct GatedPlan {
-  bool parts = false;
+  PartsPlan parts;
   ForwardPlan tiles;
   size_t a_part = 0, b_part = 0;  // bytes of one part of x, of a weight
   size_t bytes = 0;
@@ -71,11 +103,16 @@ GatedPlan plan_gated(const mscl_gated_linear_t& c) {
   const Operand x = operand(c.x, c.x_stride, c.rows, c.in_features);
   const PairOperand w = weights_of(c);
   const uint64_t stride = packed_stride(c.in_features);
-  p.parts = by_parts(c.dtype, ceil_div(c.rows, 256) * ceil_div(c.out_features, 128), c.in_features, stride, stride);
-  if (p.parts) {
+  const double m = c.rows, k = c.in_features, n = c.out_features;
+  p.parts = plan_parts(c.dtype, ceil_div(c.rows, 256) * ceil_div(c.out_features, 128), 1, c.rows, 2 * c.out_features,
+                       ceil_div(c.in_features, 64), (m + 2 * n) * k, 4 * m * n * k, stride, stride);
+  if (p.parts.on) {
     p.a_part = part_bytes(x);
     p.b_part = part_bytes(w.half[0]);
-    p.bytes = 3 * p.a_part + 6 * p.b_part;
+    p.parts.partial_stride = 2 * round_up(c.out_features, 8);
+    if (p.parts.shares > 1)
+      p.parts.partial_bytes = round_up(p.parts.shares * c.rows * p.parts.partial_stride * 4, 256);
+    p.bytes = 3 * p.a_part + 6 * p.b_part + p.parts.partial_bytes;
     return p;
   }
   p.tiles = plan_forward(x, w.half, 2, c.rows, c.out_features, c.in_features, bytes_of(c.dtype));
@@ -83,7 +120,7 @@ GatedPlan plan_gated(const mscl_gated_linear_t& c) {
   return p;
 }
 
-mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, const Gated<F32>& e, char* ws, hipStream_t s) {
+mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, Gated<F32> e, char* ws, hipStream_t s) {
   const Operand x = operand(c.x, c.x_stride, c.rows, c.in_features);
   const PairOperand w = weights_of(c);
   char* w_at = ws + 3 * p.a_part;
@@ -91,18 +128,21 @@ mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, c
   for (int h = 0; h < 2 && st == MSCL_SUCCESS; ++h) st = split_operand(w.half[h], w_at + 3 * h * p.b_part, s);
   if (st != MSCL_SUCCESS) return st;
   const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.out_features, 128);
-  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  if (tm > kMostGroups / 8 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  if (p.parts.shares > 1) e.partial = reinterpret_cast<float*>(w_at + 6 * p.b_part);
+  e.partial_stride = p.parts.partial_stride;
   GatedPartsArgs a;
   a.parts = {parts_at(x, ws), PairOperand{{parts_at(w.half[0], w_at), parts_at(w.half[1], w_at + 3 * p.b_part)}}, e,
              round_up(c.in_features, 8), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
-  a.of = {p.a_part, p.b_part};
+  a.of = {p.a_part, p.b_part, p.parts.blocks, p.parts.blocks_per_share};
   a.a = x;
   a.b = w;
   a.k = c.in_features;
-  gated_parts_big<<<static_cast<uint32_t>(tm * tn), 512, kBigLds, s>>>(a);
-  return launched("gated_parts_big");
+  gated_parts_big<<<static_cast<uint32_t>(tm * tn * p.parts.shares), 512, kBigLds, s>>>(a);
+  st = launched("gated_parts_big");
+  return st != MSCL_SUCCESS || p.parts.shares == 1 ? st : join_forward<F32>(e, p.parts.shares, s);
 }
 
 // ------------------------------------------------------------------ backward pass
@@ -119,6 +159,7 @@ struct GatedBackwardPlan {
   size_t w_bytes = 0;    // of one weight laid out anew, or of one part of it
   // large binary32 products: bytes of one part of d and of x
   bool parts = false;
+  PartsPlan dx_parts, dw_parts;
   size_t d_part = 0, x_part = 0;
   size_t d_at = 0, sums_at = 0, parts_at = 0, dx_at = 0, dw_at = 0, bytes = 0;
 };
@@ -153,9 +194,13 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
     p.dw_big = p.dw.kind == ProductPlan::kBig;
   }
   if (c.dtype == MSCL_FLOAT32 && m && n && k) {
-    const uint64_t big_of_dw = 2 * ceil_div(n, 256) * big_n, stride = packed_stride(k);
-    p.dx_big = by_parts(c.dtype, big_m * big_n, 2 * n, d.stride, stride);
-    p.dw_big = by_parts(c.dtype, big_of_dw, m, d.stride, stride);
+    const double M = m, N = n, K = k;
+    const uint64_t stride = packed_stride(k);
+    p.dx_parts = plan_parts(c.dtype, big_m * big_n, 1, m, k, 2 * turn, 2 * N * (M + K), 4 * M * N * K, d.stride, stride);
+    p.dw_parts = plan_parts(c.dtype, ceil_div(n, 256) * big_n, 2, n, k, ceil_div(m, 64), M * (2 * N + K), 4 * M * N * K,
+                            d.stride, stride);
+    p.dx_big = p.dx_parts.on;
+    p.dw_big = p.dw_parts.on;
     p.parts = (p.dx_big && c.dx) || (p.dw_big && want_dw);
   }
   // what runs as tiles runs in one launch
@@ -178,7 +223,7 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   p.dx_at = at;
   if (c.dx && p.dx_big && e == 4) {
     p.w_bytes = part_bytes(p.w.half[0]);
-    at += 6 * p.w_bytes;
+    at += 6 * p.w_bytes + p.dx_parts.partial_bytes;
   } else if (c.dx) {
     if (p.pack_w) p.w_bytes = packed_bytes(p.w.half[0]);
     if (p.dx_big)
@@ -189,7 +234,7 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   p.dw_at = at;
   if (want_dw && p.dw_big && e == 4) {
     p.x_part = part_bytes(p.x);
-    at += 3 * p.x_part;
+    at += 3 * p.x_part + 2 * p.dw_parts.partial_bytes;
   } else if (want_dw) {
     at += p.dw_big ? p.dw.bytes() : 2 * p.dw.partial_bytes;
   }
@@ -227,6 +272,22 @@ mscl_status_t launch_gated_back(const GatedBackArgs& a, uint32_t groups, hipStre
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   gated_back<C, kBM, kBN><<<groups, 256, kLds, stream>>>(a);
   return launched("gated_back");
+}
+
+// The joins of up to three products; one of fewer than two shares has none.
+template <class C>
+mscl_status_t join_gradients(GatedJoinArgs& j, hipStream_t s) {
+  uint64_t joins = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (j.shares[i] < 2) continue;
+    const uint64_t of_it = ceil_div(ceil_div(j.e[i].n, C::V) * j.e[i].m, 256);
+    joins += of_it;
+    if (joins > kMostGroups) return bad("the matrices have too many tiles");
+    j.groups[i] = static_cast<uint32_t>(of_it);
+  }
+  if (joins == 0) return MSCL_SUCCESS;
+  gated_join<C><<<static_cast<uint32_t>(joins), 256, 0, s>>>(j);
+  return launched("gated_join");
 }
 
 FittedArgs fitted(const TileArgs& t) {
@@ -278,29 +339,36 @@ mscl_status_t dx_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
     if (st != MSCL_SUCCESS) return st;
   }
   const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.in_features, 256);
-  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
+  if (tm > kMostGroups / 8 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_dx_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
+  Epilogue e = results(c.dx, c.dx_stride, c.rows, c.in_features);
+  if (p.dx_parts.shares > 1) e.partial = reinterpret_cast<float*>(w_at + 6 * p.w_bytes);
+  e.partial_stride = p.dx_parts.partial_stride;
   GatedDxPartsArgs a;
   a.parts = {parts_at(d, ws + p.parts_at),
              PairOperand{{parts_at(p.w.half[0], w_at), parts_at(p.w.half[1], w_at + 3 * p.w_bytes)}},
-             results(c.dx, c.dx_stride, c.rows, c.in_features), static_cast<uint32_t>(p.half / 64),
-             static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
-  a.of = {p.d_part, p.w_bytes};
+             e, static_cast<uint32_t>(p.half / 64), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
+  a.of = {p.d_part, p.w_bytes, p.dx_parts.blocks, p.dx_parts.blocks_per_share};
   for (int h = 0; h < 2; ++h) a.a[h] = Operand{d.base + h * p.half * 4, d.stride, c.rows, c.out_features};
   a.b = p.w;
   a.k = c.out_features;
-  gated_dx_parts_big<<<static_cast<uint32_t>(tm * tn), 512, kBigLds, s>>>(a);
-  return launched("gated_dx_parts_big");
+  gated_dx_parts_big<<<static_cast<uint32_t>(tm * tn * p.dx_parts.shares), 512, kBigLds, s>>>(a);
+  const mscl_status_t st = launched("gated_dx_parts_big");
+  GatedJoinArgs j;
+  memset(&j, 0, sizeof j);
+  j.e[0] = e;
+  j.shares[0] = p.dx_parts.shares;
+  return st != MSCL_SUCCESS ? st : join_gradients<F32>(j, s);
 }
 
 // Both weights' gradients; d's parts are there.
 mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c, const Operand& d, char* ws,
                           hipStream_t s) {
-  const mscl_status_t st = split_operand(p.x, ws + p.dw_at, s);
+  mscl_status_t st = split_operand(p.x, ws + p.dw_at, s);
   if (st != MSCL_SUCCESS) return st;
   const uint64_t tm = ceil_div(c.out_features, 256), tn = ceil_div(c.in_features, 256);
-  if (tm > kMostGroups / 2 / tn) return bad("the matrices have too many tiles");
+  if (tm > kMostGroups / 16 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_dw_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   GatedDwPartsArgs a;
@@ -310,15 +378,25 @@ mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
     void* to = h ? c.dup_w : c.dgate_w;
     // a gradient that is not wanted has no rows
     a.e[h] = results(to, h ? c.dup_w_stride : c.dgate_w_stride, to ? c.out_features : 0, c.in_features);
+    if (p.dw_parts.shares > 1)
+      a.e[h].partial = reinterpret_cast<float*>(ws + p.dw_at + 3 * p.x_part + h * p.dw_parts.partial_bytes);
+    a.e[h].partial_stride = p.dw_parts.partial_stride;
   }
   a.b = parts_at(p.x, ws + p.dw_at);
   a.b32 = p.x;
-  a.of = {p.d_part, p.x_part};
+  a.of = {p.d_part, p.x_part, p.dw_parts.blocks, p.dw_parts.blocks_per_share};
   a.k = c.rows;
   a.tiles_m = static_cast<uint32_t>(tm);
   a.tiles_n = static_cast<uint32_t>(tn);
-  gated_dw_parts_big<<<static_cast<uint32_t>(2 * tm * tn), 512, kBigLds, s>>>(a);
-  return launched("gated_dw_parts_big");
+  gated_dw_parts_big<<<static_cast<uint32_t>(2 * tm * tn * p.dw_parts.shares), 512, kBigLds, s>>>(a);
+  if ((st = launched("gated_dw_parts_big")) != MSCL_SUCCESS) return st;
+  GatedJoinArgs j;
+  memset(&j, 0, sizeof j);
+  for (int h = 0; h < 2; ++h) {
+    j.e[h] = a.e[h];
+    j.shares[h] = p.dw_parts.shares;
+  }
+  return join_gradients<F32>(j, s);
 }
 
 // dx, both weights' gradients and the bias gradients' last sums, as far as they
@@ -382,17 +460,7 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
   else
     st = launch_gated_back<C, 64, 64>(a, static_cast<uint32_t>(groups), s);
   if (st != MSCL_SUCCESS) return st;
-  uint64_t joins = 0;
-  for (int i = 0; i < 3; ++i) {
-    if (!(i == 0 ? dx : dw) || j.shares[i] < 2) continue;
-    const uint64_t of_it = ceil_div(ceil_div(j.e[i].n, C::V) * j.e[i].m, 256);
-    joins += of_it;
-    if (joins > kMostGroups) return bad("the matrices have too many tiles");
-    j.groups[i] = static_cast<uint32_t>(of_it);
-  }
-  if (joins == 0) return MSCL_SUCCESS;
-  gated_join<C><<<static_cast<uint32_t>(joins), 256, 0, s>>>(j);
-  return launched("gated_join");
+  return join_gradients<C>(j, s);
 }
 
 }  // namespace
@@ -433,7 +501,7 @@ mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace
     e.n = c.out_features;
     e.act = c.activation;
     if constexpr (std::is_same<decltype(t), F32>::value)
-      if (p.parts) return gated_by_parts(p, c, e, bytes_at(workspace), static_cast<hipStream_t>(stream));
+      if (p.parts.on) return gated_by_parts(p, c, e, bytes_at(workspace), static_cast<hipStream_t>(stream));
     return forward<decltype(t)>(p.tiles, operand(c.x, c.x_stride, c.rows, c.in_features), weights_of(c), c.in_features, e,
                                 bytes_at(workspace), static_cast<hipStream_t>(stream));
   });

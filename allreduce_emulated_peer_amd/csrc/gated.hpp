@@ -56,27 +56,53 @@ __global__ __launch_bounds__(256) void split_parts(const SplitArgs a) {
   }
 }
 
-// The copies of an operand that lies in parts.
+// The copies of an operand that lies in parts, from block `first` of k on.
 template <class Inner>
 struct PartCopier {
   Inner in;
   uint64_t part_bytes;
   uint32_t parts;  // 2 bits for each pair
+  uint32_t first;
   __device__ inline void copy(uint32_t lds, int h, uint32_t t, int wave) const {
     const uint32_t block = t / kPairs, pair = t - block * kPairs;
     Inner from = in;
     from.shift((parts >> (2 * pair) & 3) * part_bytes);
-    from.copy(lds, h, block, wave);
+    from.copy(lds, h, first + block, wave);
   }
 };
 
+struct PartsOf {
+  uint64_t a_bytes, b_bytes;  // of one part
+  uint32_t blocks;            // of k, and of one share of it
+  uint32_t blocks_per_share;
+};
+
+// Blocks [first, first + count) of k: one share's.
+struct ShareOf {
+  uint32_t first, count;
+  __device__ inline ShareOf(const PartsOf& o, uint32_t share) {
+    first = share * o.blocks_per_share;
+    count = o.blocks - first < o.blocks_per_share ? o.blocks - first : o.blocks_per_share;
+  }
+};
+
+template <class A, class B>
+__device__ inline void take_parts(PartCopier<A>& a, PartCopier<B>& b, const PartsOf& o, const ShareOf& s) {
+  a.part_bytes = o.a_bytes;
+  b.part_bytes = o.b_bytes;
+  a.parts = kPartsOfA;
+  b.parts = kPartsOfB;
+  a.first = b.first = s.first;
+}
+
 // A wave's sums of parts to those of the values; where one of the m x n is not
-// finite, all of them again in binary32 from the `chain` products' operands
-// themselves.  What lies past the matrix may be anything and is not looked at.
-// at(p) is where quarter p begins, a_of(h) and b_of(h, p) its operands.
+// finite, all of them again in binary32 from the operands themselves.  What lies
+// past the matrix may be anything and is not looked at.  at(p) is where quarter p
+// begins, a_of(h) and b_of(h, p) its operands in the h-th run of `turn` blocks of
+// k, of which k_end exist.
 template <bool kAAlong, bool kBAlong, class At, class OfA, class OfB>
-__device__ inline void finish_parts(f32x4 (&acc)[4][4][2], uint64_t m, uint64_t n, uint64_t k_end, int chain, At&& at,
-                                    OfA&& a_of, OfB&& b_of) {
+__device__ inline void finish_parts(f32x4 (&acc)[4][4][2], uint64_t m, uint64_t n, uint64_t k_end, uint32_t turn,
+                                    const ShareOf& share, At&& at, OfA&& a_of, OfB&& b_of) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   bool odd = false;
 #pragma unroll
@@ -102,24 +128,21 @@ __device__ inline void finish_parts(f32x4 (&acc)[4][4][2], uint64_t m, uint64_t 
 #pragma unroll
       for (int y = 0; y < 2; ++y) acc[p][x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
     const Corner c = at(p);
-    for (int h = 0; h < chain; ++h)
-      for (uint64_t k = 0; k < k_end; k += 4) {
-        float a[4], b[2];
+    for (uint32_t step = 0; step < share.count * 16; ++step) {
+      const uint32_t block = share.first + step / 16, h = block / turn;
+      const uint64_t k = static_cast<uint64_t>(block % turn) * 64 + step % 16 * 4;
+      float a[4], b[2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) a[x] = value_at<kAAlong>(a_of(h), c.first + 16 * x + r, k + g, k_end);
+      for (int x = 0; x < 4; ++x) a[x] = value_at<kAAlong>(a_of(h), c.first + 16 * x + r, k + g, k_end);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) b[y] = value_at<kBAlong>(b_of(h, p), c.second + 16 * y + r, k + g, k_end);
+      for (int y = 0; y < 2; ++y) b[y] = value_at<kBAlong>(b_of(h, p), c.second + 16 * y + r, k + g, k_end);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) acc[p][x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[y], a[x], acc[p][x][y], 0, 0, 0);
-      }
+        for (int y = 0; y < 2; ++y) acc[p][x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[y], a[x], acc[p][x][y], 0, 0, 0);
+    }
   }
 }
-
-struct PartsOf {
-  uint64_t a_bytes, b_bytes;  // of one part
-};
 
 // forward_big of a pair of binary32 weights in parts; a and b are the operands
 // themselves.
@@ -136,22 +159,32 @@ __global__ __launch_bounds__(512, 2) void gated_parts_big(const GatedPartsArgs a
   const auto& t = args.parts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const TileAt at(xcd_run(blockIdx.x, t.tiles_m * t.tiles_n), t.tiles_m, t.tiles_n);
+  const uint32_t tiles = t.tiles_m * t.tiles_n, id = xcd_run(blockIdx.x, gridDim.x);
+  const TileAt at(id % tiles, t.tiles_m, t.tiles_n);
+  const ShareOf share(args.of, id / tiles);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 128;
-  const uint32_t blocks = static_cast<uint32_t>((t.k + 63) / 64);
   PartCopier<Copier<BF16, true>> ca;
   PartCopier<PairCopier<BF16>> cb;
-  ca.in.init(t.a, m0, t.k, blocks, wave);
-  cb.in.init(t.b, n0, t.k, blocks, wave);
-  ca.part_bytes = args.of.a_bytes;
-  cb.part_bytes = args.of.b_bytes;
-  ca.parts = kPartsOfA;
-  cb.parts = kPartsOfB;
+  ca.in.init(t.a, m0, t.k, args.of.blocks, wave);
+  cb.in.init(t.b, n0, t.k, args.of.blocks, wave);
+  take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, true, true>(ca, cb, kPairs * blocks, lds, wave, acc);
+  big_sums<BF16, true, true>(ca, cb, kPairs * share.count, lds, wave, acc);
   finish_parts<true, true>(
-      acc, t.e.m, t.e.n, args.k, 1, [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + wn * 32}; },
+      acc, t.e.m, t.e.n, args.k, args.of.blocks, share, [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + wn * 32}; },
       [&](int) -> const Operand& { return args.a; }, [&](int, int p) -> const Operand& { return args.b.half[p & 1]; });
+  if (t.e.partial) {
+    using G = Groups<F32, 4, 2>;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < G::kCount; ++q) {
+        float v[4];
+        G::sums(acc[p], q, v);
+        keep_share(t.e, id / tiles, G::row(m0 + (p >> 1) * 128 + wm * 64, q), G::column(n0 + wn * 32, q), p & 1, v);
+      }
+    return;
+  }
   finish_blocks<F32, 4, 2, 2>(
       t.e, [&](int b, int p) -> const f32x4(&)[4][2] { return acc[2 * b + p]; },
       [&](int b) { return Corner{m0 + b * 128 + wm * 64, n0 + wn * 32}; });
@@ -299,6 +332,21 @@ __global__ __launch_bounds__(512, 2) void gated_dx_big(const GatedDxArgs args) {
   });
 }
 
+// A gradient's sums, or those of one share of k.
+template <class At>
+__device__ inline void finish_share(const Epilogue& e, uint32_t share, const f32x4 (&acc)[4][4][2], At&& at) {
+  if (!e.partial) return finish_all<F32, true>(e, acc, at);
+  using G = Groups<F32, 4, 2>;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int q = 0; q < G::kCount; ++q) {
+      float v[4];
+      G::sums(acc[p], q, v);
+      keep_partial<F32>(e, share, G::row(at(p).first, q), G::column(at(p).second, q), v);
+    }
+}
+
 // The same of binary32 operands in parts; a[h] and b are the operands themselves.
 struct GatedDxPartsArgs {
   GatedDxArgs parts;
@@ -313,23 +361,22 @@ __global__ __launch_bounds__(512, 2) void gated_dx_parts_big(const GatedDxPartsA
   const auto& t = args.parts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const TileAt at(xcd_run(blockIdx.x, t.tiles_m * t.tiles_n), t.tiles_m, t.tiles_n);
+  const uint32_t tiles = t.tiles_m * t.tiles_n, id = xcd_run(blockIdx.x, gridDim.x);
+  const TileAt at(id % tiles, t.tiles_m, t.tiles_n);
+  const ShareOf share(args.of, id / tiles);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
   PartCopier<Copier<BF16, true>> ca;
   PartCopier<ChainCopier<BF16>> cb;
   ca.in.init(t.a, m0, t.a.cols, 2 * t.turn, wave);
   cb.in.init(t.b, n0, t.turn, wave);
-  ca.part_bytes = args.of.a_bytes;
-  cb.part_bytes = args.of.b_bytes;
-  ca.parts = kPartsOfA;
-  cb.parts = kPartsOfB;
+  take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, true, false>(ca, cb, 2 * kPairs * t.turn, lds, wave, acc);
+  big_sums<BF16, true, false>(ca, cb, kPairs * share.count, lds, wave, acc);
   auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
   finish_parts<true, false>(
-      acc, t.e.m, t.e.n, args.k, 2, corner, [&](int h) -> const Operand& { return args.a[h]; },
+      acc, t.e.m, t.e.n, args.k, t.turn, share, corner, [&](int h) -> const Operand& { return args.a[h]; },
       [&](int h, int) -> const Operand& { return args.b.half[h]; });
-  finish_all<F32, true>(t.e, acc, corner);
+  finish_share(t.e, id / tiles, acc, corner);
 }
 
 // Both weights' gradients of binary32 operands in parts.
@@ -346,24 +393,21 @@ __global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsA
   extern __shared__ __align__(16) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles;
+  const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles % 2;
   const TileAt at(id % tiles, args.tiles_m, args.tiles_n);
+  const ShareOf share(args.of, id / (2 * tiles));
   const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
-  const uint32_t blocks = static_cast<uint32_t>((args.k + 63) / 64);
   PartCopier<Copier<BF16, false>> ca, cb;
-  ca.in.init(args.a[h], m0, args.k, blocks, wave);
-  cb.in.init(args.b, n0, args.k, blocks, wave);
-  ca.part_bytes = args.of.a_bytes;
-  cb.part_bytes = args.of.b_bytes;
-  ca.parts = kPartsOfA;
-  cb.parts = kPartsOfB;
+  ca.in.init(args.a[h], m0, args.k, args.of.blocks, wave);
+  cb.in.init(args.b, n0, args.k, args.of.blocks, wave);
+  take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, false, false>(ca, cb, kPairs * blocks, lds, wave, acc);
+  big_sums<BF16, false, false>(ca, cb, kPairs * share.count, lds, wave, acc);
   auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
   finish_parts<false, false>(
-      acc, args.e[h].m, args.e[h].n, args.k, 1, corner, [&](int) -> const Operand& { return args.a32[h]; },
+      acc, args.e[h].m, args.e[h].n, args.k, args.of.blocks, share, corner, [&](int) -> const Operand& { return args.a32[h]; },
       [&](int, int) -> const Operand& { return args.b32; });
-  finish_all<F32, true>(args.e[h], acc, corner);
+  finish_share(args.e[h], id / (2 * tiles), acc, corner);
 }
 
 // A gradient's sums, whose last tile of columns ends where the matrix does.

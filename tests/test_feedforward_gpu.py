@@ -153,7 +153,7 @@ def test_gated_linear_quantized(dtype, form):
 # Large products (256 x 256 tiles): edges inside a tile, k that ends inside a block, odd and even numbers of blocks, and
 # operands that have to be laid out anew.
 LARGE = [(2304, 1024, 2048, "plain"), (2100, 1040, 2000, "plain"), (2100, 1040, 2000, "columns"), (2300, 1027, 1955, "odd"),
-         (4097, 576, 1040, "plain")]
+         (4097, 576, 1040, "plain"), (1030, 4100, 3960, "odd")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
