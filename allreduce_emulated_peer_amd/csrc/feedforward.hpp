@@ -33,6 +33,7 @@ template <class Out>
 struct Scaled : Epilogue {
   using Type = Out;
   static constexpr int kParts = 1;
+  static constexpr bool kFit = true;
   const float* row_scale;
   const float* col_scale;
   __device__ inline const float* scale_of(int) const { return col_scale; }
@@ -43,6 +44,7 @@ template <class Out>
 struct Gated {
   using Type = Out;
   static constexpr int kParts = 2;
+  static constexpr bool kFit = true;
   const char* bias[2];
   char* y;
   char* z[2];  // the sums with their biases, kept for a backward pass, or null
@@ -269,6 +271,29 @@ __global__ __launch_bounds__(512) void forward_few(const TileArgsOf<B, E> t) {
   few_body<C, kM, kN, kDeep>(t);
 }
 
+// The sums of kGroups times four neighbouring values of the shares, in their
+// order, `apart` values between one share and the next; eight shares' loads are
+// in flight together.
+template <int kGroups, class S>
+__device__ inline void add_shares(const float* at, uint64_t apart, int shares, S (&sum)[kGroups]) {
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) sum[i] = S{0, 0, 0, 0};
+  for (int first = 0; first < shares; first += 8) {
+    S held[8][kGroups];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int share = first + q < shares ? first + q : shares - 1;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) held[q][i] = *reinterpret_cast<const S*>(at + share * apart + 4 * i);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (first + q < shares)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) sum[i] += held[q][i];
+  }
+}
+
 // Adds the shares of k in their order and finishes a group of V columns.
 template <class C, class E>
 __global__ __launch_bounds__(256) void forward_join(const E e, int shares) {
@@ -279,14 +304,7 @@ __global__ __launch_bounds__(256) void forward_join(const E e, int shares) {
   Sums<C> s[E::kParts][V / 4];
 #pragma unroll
   for (int p = 0; p < E::kParts; ++p)
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) s[p][i] = Sums<C>{0, 0, 0, 0};
-  for (int share = 0; share < shares; ++share)
-#pragma unroll
-    for (int p = 0; p < E::kParts; ++p)
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i)
-        s[p][i] += *reinterpret_cast<const Sums<C>*>(partial_at(e, share, m, n, p) + 4 * i);
+    add_shares<V / 4>(partial_at(e, 0, m, n, p), e.m * e.partial_stride, shares, s[p]);
   float v[E::kParts][V];
 #pragma unroll
   for (int p = 0; p < E::kParts; ++p)

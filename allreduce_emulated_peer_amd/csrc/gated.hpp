@@ -225,15 +225,33 @@ __global__ __launch_bounds__(256) void gated_slope(const GatedSlopeArgs a) {
       constexpr int kAct = decltype(act)::value;
       constexpr bool kFull = decltype(full)::value;
       constexpr int kRows = 4;  // in flight
+      // A lane at a row's end loads the vector that ends there and moves it down,
+      // a lane behind it the row's first and drops it, so that no load hangs on a
+      // branch and all are in flight together; rows shorter than a vector are
+      // loaded element by element.
+      const bool whole = kFull || a.cols >= V;
+      const uint32_t back = kFull || valid == V ? 0 : (valid > 0 ? (V - valid) * C::kElemBytes : 16);
+      const uint64_t from = kFull || valid == V ? n : (valid > 0 ? a.cols - V : 0);
+      auto fetch = [&](const char* base, uint64_t m, uint64_t stride) {
+        if (!whole) return load_upto<C>(base + (m * stride + n) * C::kElemBytes, valid);
+        return load_loose<C>(base + (m * stride + from) * C::kElemBytes);
+      };
       for (uint64_t m0 = first + wave; m0 < end; m0 += 4 * kRows) {
         u32x4 dy[kRows], z[kRows], v[kRows];
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
           const uint64_t m = m0 + 4 * q < end ? m0 + 4 * q : end - 1;
-          const int there = kFull ? V : valid;
-          dy[q] = load_upto<C>(a.dy + (m * a.dy_stride + n) * C::kElemBytes, there);
-          z[q] = load_upto<C>(a.z + (m * a.z_stride + n) * C::kElemBytes, there);
-          v[q] = load_upto<C>(a.v + (m * a.v_stride + n) * C::kElemBytes, there);
+          dy[q] = fetch(a.dy, m, a.dy_stride);
+          z[q] = fetch(a.z, m, a.z_stride);
+          v[q] = fetch(a.v, m, a.v_stride);
+        }
+        if (!kFull && whole) {
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            dy[q] = moved_down(dy[q], back);
+            z[q] = moved_down(z[q], back);
+            v[q] = moved_down(v[q], back);
+          }
         }
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
@@ -466,7 +484,17 @@ __global__ __launch_bounds__(256) void gated_join(const GatedJoinArgs p) {
   uint32_t id = blockIdx.x;
   int i = 0;
   while (i < 2 && id >= p.groups[i]) id -= p.groups[i++];
-  join_shares<C>(p.e[i], static_cast<int>(p.shares[i]), static_cast<uint64_t>(id) * 256 + threadIdx.x);
+  const Epilogue& e = p.e[i];
+  constexpr int V = C::V;
+  const uint64_t per_row = (e.n + V - 1) / V, at = static_cast<uint64_t>(id) * 256 + threadIdx.x;
+  if (at >= per_row * e.m) return;
+  const uint64_t m = at / per_row, n = at % per_row * V;
+  f32x4 s[V / 4];
+  add_shares<V / 4>(e.partial + m * e.partial_stride + n, e.m * e.partial_stride, static_cast<int>(p.shares[i]), s);
+  float v[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) v[c] = s[c / 4][c % 4];
+  store_row<C>(e.y, e.y_stride, m, n, e.m, e.n, v);
 }
 
 }  // namespace mscl

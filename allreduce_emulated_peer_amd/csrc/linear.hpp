@@ -74,17 +74,10 @@ __device__ inline u32x4 load_upto(const char* p, int valid) {
   return v;
 }
 
-// The same where at least `room` bytes of the row lie before `p`: the vector
-// that ends with the last element, moved down, in place of a load an element.
-template <class C>
-__device__ inline u32x4 load_within(const char* p, int valid, uint64_t room) {
-  if (valid >= C::V) return load_loose<C>(p);
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (valid <= 0) return v;
-  const uint32_t back = (C::V - valid) * C::kElemBytes;
-  if (room < back) return load_partial<C>(p, 0, valid);
-  const u32x4 w = load_loose<C>(p - back);
-  const uint32_t words = back >> 2, bytes = back & 3;
+// A vector's bytes from byte `by` (0..16) on, zeros behind them.
+__device__ inline u32x4 moved_down(const u32x4& w, uint32_t by) {
+  const uint32_t words = by >> 2, bytes = by & 3;
+  u32x4 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t lo = 0, hi = 0;
@@ -557,14 +550,14 @@ struct Feed {
   // Whether all of the tile's columns exist.
   __device__ inline bool whole() const { return kAlong || cols >= kT; }
 
-  // fn(chunk, part, address, how many of the part's elements exist, bytes of the
-  // row before it) for the next whole block.
+  // fn(chunk, part, address, how many of the part's elements exist) for the
+  // next whole block.
   template <class Fn>
   __device__ inline void next(Fn&& fn) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, C::V, uint64_t(0));
+      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, C::V);
     const uint64_t by = left > 1 ? step : 0;
     if (left > 1) --left;
 #pragma unroll
@@ -587,8 +580,40 @@ struct Feed {
         valid = k + r < k_end ? static_cast<int64_t>(cols) - c * kChunk : 0;
       const int n = valid < 0 ? 0 : (valid > kChunk ? kChunk : static_cast<int>(valid));
 #pragma unroll
-      for (int q = 0; q < kParts; ++q)
-        fn(i, q, chunk(i) + q * 16, n - q * C::V, ((kAlong ? k : first) + c * kChunk + q * C::V) * e);
+      for (int q = 0; q < kParts; ++q) fn(i, q, chunk(i) + q * 16, n - q * C::V);
+    }
+  }
+
+  // Whether edge() can do without branches, of an operand whose k ends at k_all:
+  // its rows hold a vector.
+  template <class O>
+  static __device__ inline bool reaches(const O& o, uint64_t k_all) {
+    return (kAlong ? k_all : o.part(0).cols) >= C::V;
+  }
+
+  // fn(chunk, part, address, by) for such a block, each vector from inside the
+  // matrix: its wanted elements start at byte `by`, and none is wanted at 16.
+  template <class O, class Fn>
+  static __device__ inline void edge_free(const O& both, uint64_t first, uint64_t k, uint64_t k_end, Fn&& fn) {
+    constexpr int V = C::V;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      constexpr int kOfPart = kChunks / O::kParts;
+      const Operand& o = both.part(i / kOfPart);
+      const int id = (O::kParts == 1 ? i : i % kOfPart) * kThreads + threadIdx.x;
+      const int r = id / kPerRow, c = id % kPerRow;
+      const uint64_t end = kAlong ? k_end : o.cols, last = kAlong ? o.rows : k_end;
+      const uint64_t row = (kAlong ? first : k) + r;
+      const bool there = kAlong || row < last;
+      const char* line = o.base + (row < last ? row : last - 1) * o.stride * e;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        const uint64_t col = (kAlong ? k : first) + c * kChunk + q * V;
+        const uint64_t left = col < end ? end - col : 0;
+        const bool all = left >= V, some = left > 0;
+        fn(i, q, line + (all ? col : (some ? end - V : 0)) * e,
+           there ? (all ? 0u : (some ? static_cast<uint32_t>(V - left) * e : 16u)) : 16u);
+      }
     }
   }
 };
@@ -596,7 +621,9 @@ struct Feed {
 // Walks over the blocks of k of a tile: kDeep whole blocks' loads in flight,
 // then what is left one by one.  store(d, block) puts set d into the block's
 // LDS buffer, compute(block) multiplies it; kBuffers LDS buffers alternate.
-template <int kDeep, int kBuffers, class Args, class FA, class FB, class SA, class SB, class Store, class Compute>
+// kTogether: the blocks that are left are loaded without branches, kDeep at a
+// time (where the matrices' rows hold a vector).
+template <int kDeep, int kBuffers, bool kTogether, class Args, class FA, class FB, class SA, class SB, class Store, class Compute>
 __device__ inline void walk(const Args& t, uint64_t m0, uint64_t n0, uint64_t k_first, uint64_t k_end, FA& feed_a,
                             FB& feed_b, SA (&sa)[kDeep], SB (&sb)[kDeep], Store&& store, Compute&& compute) {
   constexpr int kBlock = FA::kBlock;
@@ -638,6 +665,29 @@ __device__ inline void walk(const Args& t, uint64_t m0, uint64_t n0, uint64_t k_
     }
     k += static_cast<uint64_t>(blocks) * kBlock;
   }
+  if constexpr (kTogether) {
+    if (FA::reaches(t.a, t.k) && FB::reaches(t.b, t.k)) {
+      for (; k < k_end; k += kDeep * kBlock) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+          if (k + d * kBlock < k_end) {
+            sa[d].load_free(t.a, m0, k + d * kBlock, k_end);
+            sb[d].load_free(t.b, n0, k + d * kBlock, k_end);
+          }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+          if (k + d * kBlock < k_end) {
+            sa[d].settle(t.a, m0, k + d * kBlock, k_end);
+            sb[d].settle(t.b, n0, k + d * kBlock, k_end);
+            __syncthreads();
+            store(d, 0);
+            __syncthreads();
+            compute(0);
+          }
+      }
+      return;
+    }
+  }
   for (; k < k_end; k += kBlock) {
     sa[0].load_edge(feed_a, t.a, m0, k, k_end);
     sb[0].load_edge(feed_b, t.b, n0, k, k_end);
@@ -673,15 +723,22 @@ struct Stage {
   }
 
   __device__ inline void load(Feed<C, kAlong, kT, kThreads, 1>& f) {
-    f.next([&](int i, int, const char* p, int, uint64_t) { held[i] = load_loose<C>(p); });
+    f.next([&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
   }
   template <class O>
   __device__ inline void load_edge(Feed<C, kAlong, kT, kThreads, 1>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
-    f.edge(o, first, k, k_end,
-           [&](int i, int, const char* p, int valid, uint64_t room) {
-             held[i] = kAlong ? load_within<C>(p, valid, room) : load_upto<C>(p, valid);
-           });
+    f.edge(o, first, k, k_end, [&](int i, int, const char* p, int valid) { held[i] = load_upto<C>(p, valid); });
+  }
+  // The same in two steps, so that the loads of several blocks are in flight.
+  template <class O>
+  __device__ inline void load_free(const O& o, uint64_t first, uint64_t k, uint64_t k_end) {
+    Feed<C, kAlong, kT, kThreads, 1>::edge_free(o, first, k, k_end, [&](int i, int, const char* p, uint32_t) { held[i] = load_loose<C>(p); });
+  }
+  template <class O>
+  __device__ inline void settle(const O& o, uint64_t first, uint64_t k, uint64_t k_end) {
+    Feed<C, kAlong, kT, kThreads, 1>::edge_free(
+        o, first, k, k_end, [&](int i, int, const char*, uint32_t by) { held[i] = moved_down(held[i], by); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -738,9 +795,10 @@ __device__ inline Sums<C> multiply(const u32x4& b, const u32x4& a, Sums<C> acc) 
   }
 }
 
-// The first column of a tile.  An epilogue with kFit moves the last tile of a
-// kDown operand back to end where the matrix ends, so that its loads need no
-// bound; what it then shares with the tile before has the same bits in both.
+// An epilogue with kFit has its tiles' last blocks loaded without branches, and
+// the last tile of a kDown operand moved back to end where the matrix ends, so
+// that its loads need no bound; what it then shares with the tile before has the
+// same bits in both.
 template <class E, class = void>
 struct Fits : std::false_type {};
 template <class E>
@@ -788,7 +846,7 @@ __device__ inline void tile_body(const TileArgsOf<B, E>* chained, int chain, uin
   auto buffer = [&](uint32_t block) { return lds + (block & 1) * (SA::kBytes + SB::kBytes); };
   for (int h = 0; h < chain; ++h) {
    if (h) __syncthreads();  // the last block is read, as the first one's buffer may be its own
-   walk<kDeep, 2>(
+   walk<kDeep, 2, Fits<E>::value>(
       chained[h], m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
       [&](int d, uint32_t block) {
         sa[d].store(buffer(block));
@@ -1092,13 +1150,21 @@ struct SplitStage {
   u32x4 held[kChunks][2];
 
   __device__ inline void load(Feed<F32, kAlong, kT, 256, 2>& f) {
-    f.next([&](int i, int q, const char* p, int, uint64_t) { held[i][q] = load_loose<F32>(p); });
+    f.next([&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
   }
   template <class O>
   __device__ inline void load_edge(Feed<F32, kAlong, kT, 256, 2>& f, const O& o, uint64_t first, uint64_t k,
                                    uint64_t k_end) {
-    f.edge(o, first, k, k_end,
-           [&](int i, int q, const char* p, int valid, uint64_t) { held[i][q] = load_upto<F32>(p, valid); });
+    f.edge(o, first, k, k_end, [&](int i, int q, const char* p, int valid) { held[i][q] = load_upto<F32>(p, valid); });
+  }
+  template <class O>
+  __device__ inline void load_free(const O& o, uint64_t first, uint64_t k, uint64_t k_end) {
+    Feed<F32, kAlong, kT, 256, 2>::edge_free(o, first, k, k_end, [&](int i, int q, const char* p, uint32_t) { held[i][q] = load_loose<F32>(p); });
+  }
+  template <class O>
+  __device__ inline void settle(const O& o, uint64_t first, uint64_t k, uint64_t k_end) {
+    Feed<F32, kAlong, kT, 256, 2>::edge_free(
+        o, first, k, k_end, [&](int i, int q, const char*, uint32_t by) { held[i][q] = moved_down(held[i][q], by); });
   }
   __device__ inline void store(char* lds) const {
 #pragma unroll
@@ -1158,7 +1224,7 @@ __device__ inline void split_body(const TileArgsOf<B, E>* chained, int chain, ui
   Feed<F32, kBAlong, kBN, 256, 2> feed_b;
   for (int h = 0; h < chain; ++h) {
    if (h) __syncthreads();
-   walk<kDeep, 1>(
+   walk<kDeep, 1, Fits<E>::value>(
       chained[h], m0, n0, k_first, k_end, feed_a, feed_b, sa, sb,
       [&](int d, uint32_t) {
         sa[d].store(lds);
