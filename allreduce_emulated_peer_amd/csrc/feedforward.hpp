@@ -357,7 +357,6 @@ __device__ inline PairCopier<C> copier_of(const PairOperand&) {
 // tile has 128 columns of each weight, in quarters (i, 0) and (i, 1).
 template <class C, class B, class E>
 __global__ __launch_bounds__(512, 2) void forward_big(const BigArgsOf<B, E> args) {
-  extern __shared__ __align__(16) char lds[];
   constexpr int kParts = B::kParts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -370,7 +369,7 @@ __global__ __launch_bounds__(512, 2) void forward_big(const BigArgsOf<B, E> args
   ca.init(args.a, m0, args.k, blocks, wave);
   cb.init(args.b, n0, args.k, blocks, wave);
   Sums<C> acc[4][4][2];
-  big_sums<C, true, true>(ca, cb, blocks, lds, wave, acc);
+  big_sums<C, true, true>(ca, cb, blocks, wave, acc);
   // block b is quarter b, or with a pair quarters (b, 0) and (b, 1)
   finish_blocks<C, 4, 2, 4 / kParts>(
       args.e, [&](int b, int p) -> const Sums<C>(&)[4][2] { return acc[kParts * b + p]; },

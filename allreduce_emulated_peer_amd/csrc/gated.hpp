@@ -155,7 +155,6 @@ struct GatedPartsArgs {
 };
 
 __global__ __launch_bounds__(512, 2) void gated_parts_big(const GatedPartsArgs args) {
-  extern __shared__ __align__(16) char lds[];
   const auto& t = args.parts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -169,7 +168,7 @@ __global__ __launch_bounds__(512, 2) void gated_parts_big(const GatedPartsArgs a
   cb.in.init(t.b, n0, t.k, args.of.blocks, wave);
   take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, true, true>(ca, cb, kPairs * share.count, lds, wave, acc);
+  big_sums<BF16, true, true>(ca, cb, kPairs * share.count, wave, acc);
   finish_parts<true, true>(
       acc, t.e.m, t.e.n, args.k, args.of.blocks, share, [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + wn * 32}; },
       [&](int) -> const Operand& { return args.a; }, [&](int, int p) -> const Operand& { return args.b.half[p & 1]; });
@@ -334,7 +333,6 @@ struct GatedDxArgs {
 // dx = dz wg + dv wu: one product whose k runs over both.
 template <class C>
 __global__ __launch_bounds__(512, 2) void gated_dx_big(const GatedDxArgs args) {
-  extern __shared__ __align__(16) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
@@ -344,7 +342,7 @@ __global__ __launch_bounds__(512, 2) void gated_dx_big(const GatedDxArgs args) {
   ca.init(args.a, m0, args.a.cols, 2 * args.turn, wave);
   cb.init(args.b, n0, args.turn, wave);
   f32x4 acc[4][4][2];
-  big_sums<C, true, false>(ca, cb, 2 * args.turn, lds, wave, acc);
+  big_sums<C, true, false>(ca, cb, 2 * args.turn, wave, acc);
   finish_all<C, true>(args.e, acc, [&](int p) {
     return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
   });
@@ -375,7 +373,6 @@ struct GatedDxPartsArgs {
 };
 
 __global__ __launch_bounds__(512, 2) void gated_dx_parts_big(const GatedDxPartsArgs args) {
-  extern __shared__ __align__(16) char lds[];
   const auto& t = args.parts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -389,7 +386,7 @@ __global__ __launch_bounds__(512, 2) void gated_dx_parts_big(const GatedDxPartsA
   cb.in.init(t.b, n0, t.turn, wave);
   take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, true, false>(ca, cb, kPairs * share.count, lds, wave, acc);
+  big_sums<BF16, true, false>(ca, cb, kPairs * share.count, wave, acc);
   auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
   finish_parts<true, false>(
       acc, t.e.m, t.e.n, args.k, t.turn, share, corner, [&](int h) -> const Operand& { return args.a[h]; },
@@ -408,7 +405,6 @@ struct GatedDwPartsArgs {
 };
 
 __global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsArgs args) {
-  extern __shared__ __align__(16) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles % 2;
@@ -420,7 +416,7 @@ __global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsA
   cb.in.init(args.b, n0, args.k, args.of.blocks, wave);
   take_parts(ca, cb, args.of, share);
   f32x4 acc[4][4][2];
-  big_sums<BF16, false, false>(ca, cb, kPairs * share.count, lds, wave, acc);
+  big_sums<BF16, false, false>(ca, cb, kPairs * share.count, wave, acc);
   auto corner = [&](int p) { return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32}; };
   finish_parts<false, false>(
       acc, args.e[h].m, args.e[h].n, args.k, args.of.blocks, share, corner, [&](int) -> const Operand& { return args.a32[h]; },

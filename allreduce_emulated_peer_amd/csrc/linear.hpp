@@ -977,7 +977,7 @@ struct Copier {
       const uint32_t v = t + 1 < blocks ? voffset : (t + 1 == blocks ? last : kNowhere);
       const uint32_t k = t < blocks ? t * 128 : 0;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) copy_to_lds(from, lds + (q * 8 + wave) * 1024, v + (h * 128 + q * 64) * stride + k);
+      for (int q = 0; q < 2; ++q) copy_to_lds(from, lds + (q * 8 + wave) * 1024, v + ((h * 128 + q * 64) * stride + k));
     } else {
       const uint64_t at = static_cast<uint64_t>(t) * (64 * stride);
       const __amdgpu_buffer_rsrc_t from = range(base + at, t < blocks ? left - at : 0);
@@ -990,7 +990,8 @@ struct Copier {
 
 // The sums of one tile: acc[2 i + j] is a wave's part of quarter (i, j).
 template <class C, bool kAAlong, bool kBAlong, class CA, class CB>
-__device__ inline void big_sums(const CA& ca, const CB& cb, uint32_t blocks, char* lds, int wave, Sums<C> (&acc)[4][4][2]) {
+__device__ inline void big_sums(const CA& ca, const CB& cb, uint32_t blocks, int wave, Sums<C> (&acc)[4][4][2]) {
+  extern __shared__ __align__(16) char lds[];
   using SA = Stage<C, kAAlong, 128, 512>;
   using SB = Stage<C, kBAlong, 128, 512>;
   const int wm = wave >> 2, wn = wave & 3;
@@ -1080,7 +1081,6 @@ __device__ inline void big_sums(const CA& ca, const CB& cb, uint32_t blocks, cha
 
 template <class C, bool kAAlong, bool kBAlong>
 __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
-  extern __shared__ __align__(16) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const TileAt at(xcd_run(blockIdx.x, args.tiles_m * args.tiles_n), args.tiles_m, args.tiles_n);
@@ -1092,7 +1092,7 @@ __global__ __launch_bounds__(512, 2) void linear_big(const BigArgs args) {
   ca.init(args.a, m0, args.k, blocks, wave);
   cb.init(args.b, n0, args.k, blocks, wave);
   f32x4 acc[4][4][2];
-  big_sums<C, kAAlong, kBAlong>(ca, cb, blocks, lds, wave, acc);
+  big_sums<C, kAAlong, kBAlong>(ca, cb, blocks, wave, acc);
   finish_all<C, !(kAAlong && kBAlong)>(args.e, acc, [&](int p) {
     return Corner{m0 + (p >> 1) * 128 + wm * 64, n0 + (p & 1) * 128 + wn * 32};
   });
