@@ -147,7 +147,7 @@ __device__ inline u32x4 residual_of(const Gated<Out>&, uint64_t, uint64_t) {
 
 // All of it for one group whose sums (integers as their bits) are at hand.
 template <class C, class E>
-__device__ inline void finish_one(const E& e, uint64_t m, uint64_t n, float (&v)[E::kParts][OutOf<E>::V]) {
+__device__ __forceinline__ void finish_one(const E& e, uint64_t m, uint64_t n, float (&v)[E::kParts][OutOf<E>::V]) {
   using Out = OutOf<E>;
   const float rs = row_scale_of<C>(e, m);
   const u32x4 residual = residual_of(e, m, n);
@@ -165,7 +165,7 @@ __device__ inline void finish_one(const E& e, uint64_t m, uint64_t n, float (&v)
 // A wave's blocks of tiles: kBlocks of them, block b of part p in acc(b, p), at
 // at(b).  A column's bias and scale are fetched once for all of its rows.
 template <class C, int kM, int kN, int kBlocks, class E, class Acc, class At>
-__device__ inline void finish_blocks(const E& e, Acc&& acc, At&& at) {
+__device__ __forceinline__ void finish_blocks(const E& e, Acc&& acc, At&& at) {
   using Out = OutOf<E>;
   using G = Groups<Out, kM, kN>;
   with_activation(e.act, [&](auto act) {
@@ -215,7 +215,7 @@ __device__ inline void keep_share(const E& e, uint64_t share, uint64_t m, uint64
 
 // What linear.hpp's tiles call for these epilogues.
 template <class C, bool kPlain, int kM, int kN, class E>
-__device__ inline void finish_tile(const E& e, uint64_t share, const Sums<C> (&acc)[E::kParts][kM][kN], uint64_t m0,
+__device__ __forceinline__ void finish_tile(const E& e, uint64_t share, const Sums<C> (&acc)[E::kParts][kM][kN], uint64_t m0,
                                    uint64_t n0) {
   using G = Groups<OutOf<E>, kM, kN>;
   if (e.partial) {
@@ -234,7 +234,7 @@ __device__ inline void finish_tile(const E& e, uint64_t share, const Sums<C> (&a
 }
 
 template <class C, int kM, int kN, class E, int kSize>
-__device__ inline void finish_few(const E& e, const SumOf<C> (&sums)[4][kSize], uint64_t n0) {
+__device__ __forceinline__ void finish_few(const E& e, const SumOf<C> (&sums)[4][kSize], uint64_t n0) {
   constexpr int V = OutOf<E>::V;
   constexpr int kPitch = 16 * kN + 4, kColumns = 16 * kN / E::kParts;
   for (int id = threadIdx.x; id < 16 * kM * kColumns / V; id += 512) {

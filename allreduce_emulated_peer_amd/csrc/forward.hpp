@@ -64,6 +64,42 @@ inline void share_k(ForwardPlan* p, uint64_t shares, uint64_t steps, uint64_t m,
   p->bytes = p->partial_bytes;
 }
 
+// forward_tile's tile, and the shares of k, by what a launch of them takes.  A
+// workgroup alone on its compute unit takes 4 us and, for each block of k (us,
+// from products of 8 to 128 blocks)
+//                          64 rows   128 rows
+//   8 bits                   0.285     0.69      (64 and 128 columns)
+//   pairs of 8 or 16 bits    0.43      0.69      (64 of each)
+//   pairs of binary32        1.35      2.35      (32 of each)
+// and r of them at once take 0.92 r times as long (0.75 r, binary32, whose
+// operands' splitting and products overlap).  Shares shorten the run of blocks,
+// and cost a launch and a write and a read of their sums at 4 TB/s.  us, without
+// shares and with two: 512 x 512 -> 4096 pairs of bf16 11 and 28, 1024 x 2048 ->
+// 1024 8 bits 8.9 and 15; the other way 64 x 8192 -> 4096 pairs of bf16 59 and
+// 38 (four 29), 1024 x 2048 -> 1024 pairs of binary32 82 and 70.
+inline void choose_tiles(ForwardPlan* p, uint64_t m, uint64_t n, uint64_t k, int parts, size_t e) {
+  const uint64_t steps = ceil_div(k, block_of(e));
+  double best = 0;
+  uint64_t best_shares = 1;
+  for (const int rows : {64, 128}) {
+    const int outs = e == 4 ? 64 / parts : (parts == 1 ? rows : 64);
+    const double block = e == 4 ? (rows == 64 ? 1.35 : 2.35) : (rows == 128 ? 0.69 : (parts == 1 ? 0.285 : 0.43));
+    const uint64_t tiles = ceil_div(m, rows) * ceil_div(n, outs);
+    for (const uint64_t shares : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (shares > 1 && 2 * shares > steps) break;
+      const double at_once = static_cast<double>(ceil_div(tiles * shares, kCus));
+      double us = 4 + block * ceil_div(steps, shares) * std::max(1.0, (e == 4 ? 0.75 : 0.92) * at_once);
+      if (shares > 1) us += 4 + 8.0 * shares * m * parts * n / 4e6;
+      if (best > 0 && us >= best) continue;
+      best = us;
+      best_shares = shares;
+      p->tile_m = rows;
+      p->outs = outs;
+    }
+  }
+  share_k(p, best_shares, steps, m, n, parts);
+}
+
 inline ForwardPlan plan_forward(const Operand& a, const Operand* b, int parts, uint64_t m, uint64_t n, uint64_t k, size_t e) {
   ForwardPlan p;
   const uint64_t block = 128 / e, blocks = ceil_div(k, block);
@@ -100,17 +136,7 @@ inline ForwardPlan plan_forward(const Operand& a, const Operand* b, int parts, u
     share_k(&p, shares, whole, m, n, parts);
     return p;
   }
-  const uint64_t large = ceil_div(m, 128) * ceil_div(n, 128 / parts);
-  if (e == 4) {
-    p.tile_m = 2 * large >= kCus / 2 ? 128 : 64;
-    p.outs = 64 / parts;
-  } else {
-    p.tile_m = large >= kCus ? 128 : 64;
-    p.outs = p.tile_m == 128 ? 128 / parts : 64;
-  }
-  const uint64_t steps = ceil_div(k, block_of(e));
-  const uint64_t run = std::max<uint64_t>(4, ceil_div(ceil_div(m, p.tile_m) * ceil_div(n, p.outs) * steps, 2 * kCus));
-  share_k(&p, std::min<uint64_t>(32, std::max<uint64_t>(1, steps / run)), steps, m, n, parts);
+  choose_tiles(&p, m, n, k, parts, e);
   return p;
 }
 
