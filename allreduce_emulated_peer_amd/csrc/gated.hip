@@ -56,8 +56,8 @@ mscl_status_t split_operand(const Operand& o, char* to, hipStream_t s) {
 // 256 x 256 take 6 x 1.4 us a block of k whether or not they fill the device, so
 // k is split where they would leave much of it idle, and the shares' sums (and
 // the parts themselves, 10 bytes a value) are a pass over memory at 5 TB/s.
-// linear_tile's kind, which takes operands into parts in every tile, reaches 130
-// to 165 TFLOP/s.  Forward, us by parts and by those tiles: 1024 x 4096 -> 4096
+// forward_tile, which takes operands into parts in every tile, reaches 130 to 165
+// TFLOP/s.  Forward, us by parts and by those tiles: 1024 x 4096 -> 4096
 // 389 and 509, 2048 x 2048 -> 2048 203 and 260, 512 x 4096 -> 4096 249 and 205.
 struct PartsPlan {
   bool on = false;
@@ -184,8 +184,9 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   plan_groups(m, ceil_div(p.half, 64 * (16 / e)), &p.groups, &p.rows_per_group);
   p.sums_at = at;
   if (c.dgate_bias || c.dup_bias) at = round_up(at + size_t(p.groups) * 2 * n * 4, 256);
-  // The plans go by sizes and layouts, not by which gradients are wanted: a
-  // gradient has the same bits alone.
+  // The plans go by sizes and layouts, not by which gradients are wanted, so a
+  // gradient has the same bits alone; except that the layouts of what is not given
+  // are taken as plain, where odd ones could send a large product to other tiles.
   const Operand none{nullptr, k, n, k};
   p.w = c.dx ? pair_of(c.gate_w, c.gate_w_stride, c.up_w, c.up_w_stride, n, k) : PairOperand{{none, none}};
   p.x = want_dw ? operand(c.x, c.x_stride, m, k) : Operand{nullptr, k, m, k};

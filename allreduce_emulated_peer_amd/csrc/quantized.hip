@@ -101,11 +101,18 @@ mscl_status_t mscl_quantize(const mscl_quantize_t* call, void* stream) {
   if (c.rows == 0) return MSCL_SUCCESS;
   int cus = 0;
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
-  const QuantizeArgs a{bytes_at(c.x), c.q, c.scale, c.x_stride, c.q_stride, c.rows, c.width};
-  return with_codec(c.dtype, [&](auto t) {
-    launch_quantize<decltype(t)>(a, static_cast<hipStream_t>(stream));
-    return launched("quantize_rows");
-  });
+  // a launch has fewer than 2^32 threads, up to 1024 of them a row
+  constexpr size_t kRowsOfLaunch = size_t(1) << 21;
+  for (size_t first = 0; first < c.rows && st == MSCL_SUCCESS; first += kRowsOfLaunch) {
+    const size_t rows = std::min(kRowsOfLaunch, c.rows - first);
+    const QuantizeArgs a{bytes_at(c.x) + first * c.x_stride * bytes_of(c.dtype), c.q + first * c.q_stride, c.scale + first,
+                         c.x_stride, c.q_stride, rows, c.width};
+    st = with_codec(c.dtype, [&](auto t) {
+      launch_quantize<decltype(t)>(a, static_cast<hipStream_t>(stream));
+      return launched("quantize_rows");
+    });
+  }
+  return st;
 }
 
 mscl_status_t mscl_linear_quantized_workspace(const mscl_linear_quantized_t* call, size_t* bytes) {

@@ -221,6 +221,18 @@ def test_rows_that_have_no_scale():
                 assert bool(torch.isnan(out[1:4]).all()) and not bool(out[4].any()) and not bool(torch.isnan(out[[0, 5]]).any())
 
 
+def test_more_rows_than_a_launch_takes():
+    rows, width = 2 ** 21 + 5, 9
+    note("many rows", rows, width)
+    x = torch.randn(rows, width, generator=torch.Generator(device="cuda").manual_seed(86), device="cuda").bfloat16()
+    q, scale = M.quantize_tensors(x)
+    for part in (slice(0, 3000), slice(2 ** 21 - 3000, None)):
+        want, want_scale = F.quantize(x[part].cpu())
+        assert torch.equal(q[part].cpu(), want) and torch.equal(scale[part].cpu(), want_scale)
+    values = q.float() * scale[:, None]
+    assert bool(((values - x.float()).abs() <= 0.5001 * scale[:, None]).all())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_ties_go_to_the_even_integer(dtype):
     """Sizes of 127 times a power of two, so that halves of a step are exact."""
