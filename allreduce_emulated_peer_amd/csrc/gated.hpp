@@ -441,6 +441,30 @@ __device__ inline void finish_tile(const Fitted& e, uint64_t share, const f32x4 
   finish_tile<C, kPlain>(static_cast<const Epilogue&>(e), share, acc, m0, n0);
 }
 
+// The same of a wave some of whose columns, those before `own`, are the tile
+// before's to store: element by element.  One wave of two at most a row of tiles.
+template <class C, bool kPlain, int kM, int kN>
+__device__ inline void finish_tile(const Fitted& e, uint64_t share, const f32x4 (&acc)[1][kM][kN], uint64_t m0, uint64_t n0,
+                                   uint64_t own) {
+  using G = Groups<C, kM, kN>;
+  if (n0 + 16 * kN <= own) return;
+#pragma unroll
+  for (int q = 0; q < G::kCount; ++q) {
+    const uint64_t m = G::row(m0, q), n = G::column(n0, q);
+    float v[C::V];
+    G::sums(acc[0], q, v);
+    if (m >= e.m) continue;
+#pragma unroll
+    for (int c = 0; c < C::V; ++c) {
+      if (n + c < own || n + c >= e.n) continue;
+      if (e.partial)
+        e.partial[(share * e.m + m) * e.partial_stride + n + c] = v[c];
+      else
+        reinterpret_cast<typename C::Bits*>(e.y)[m * e.y_stride + n + c] = C::narrow(v[c]);
+    }
+  }
+}
+
 // Tiles of the three products and the bias gradients' last sums in one launch:
 // small products leave the device half empty, and each launch costs 3 us on the
 // host.  515 x 1025 x 770 fp16: 20 us, 32 x 54 -> 189 bf16 8 us.

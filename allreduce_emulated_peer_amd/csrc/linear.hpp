@@ -797,8 +797,9 @@ __device__ inline Sums<C> multiply(const u32x4& b, const u32x4& a, Sums<C> acc) 
 
 // An epilogue with kFit has its tiles' last blocks loaded without branches, and
 // the last tile of a kDown operand moved back to end where the matrix ends, so
-// that its loads need no bound; what it then shares with the tile before has the
-// same bits in both.
+// that its loads need no bound.  The columns that it then shares with the tile
+// before are that tile's to store: the two may differ in their last bits, as a
+// wave of a binary32 tile sums all of its columns again where one is not finite.
 template <class E, class = void>
 struct Fits : std::false_type {};
 template <class E>
@@ -808,6 +809,17 @@ template <class E, bool kAlong, int kT>
 __device__ inline uint64_t first_column(uint64_t n0, uint64_t n) {
   if constexpr (!kAlong && Fits<E>::value) return n >= kT && n0 + kT > n ? n - kT : n0;
   return n0;
+}
+
+// What becomes of a wave's sums at (m0, n0) of a tile that may have been moved;
+// `own` is the first column that the tile stores.
+template <class C, bool kAAlong, bool kBAlong, class E, class Acc>
+__device__ __forceinline__ void finish_fitted(const E& e, uint64_t share, const Acc& acc, uint64_t m0, uint64_t n0,
+                                              uint64_t own) {
+  constexpr bool kPlain = !(kAAlong && kBAlong);
+  if constexpr (Fits<E>::value && !kBAlong)
+    if (n0 < own) return finish_tile<C, kPlain>(e, share, acc, m0, n0, own);
+  finish_tile<C, kPlain>(e, share, acc, m0, n0);
 }
 
 // Any sizes, strides and alignments of a 16-bit type: kBM x kBN tiles by 4
@@ -824,7 +836,7 @@ __device__ inline void tile_body(const TileArgsOf<B, E>* chained, int chain, uin
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM;
-  const uint64_t n0 = first_column<E, kBAlong, kBN>(static_cast<uint64_t>(at.n) * (kBN / kParts), t.e.n);
+  const uint64_t own = static_cast<uint64_t>(at.n) * (kBN / kParts), n0 = first_column<E, kBAlong, kBN>(own, t.e.n);
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * SA::kBlock;
@@ -873,7 +885,7 @@ __device__ inline void tile_body(const TileArgsOf<B, E>* chained, int chain, uin
         }
       });
   }
-  finish_tile<C, !(kAAlong && kBAlong)>(t.e, share, acc, m0 + wm, n0 + wn);
+  finish_fitted<C, kAAlong, kBAlong>(t.e, share, acc, m0 + wm, n0 + wn, own);
 }
 
 // ------------------------------------------------------------------ large products of 16-bit types
@@ -1203,7 +1215,7 @@ __device__ inline void split_body(const TileArgsOf<B, E>* chained, int chain, ui
   constexpr int kWM = kBM / 2 / 16, kWN = kBN / 2 / 16 / kParts;
   const TileAt at(tile, t.tiles_m, t.tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * kBM;
-  const uint64_t n0 = first_column<E, kBAlong, kBN>(static_cast<uint64_t>(at.n) * (kBN / kParts), t.e.n);
+  const uint64_t own = static_cast<uint64_t>(at.n) * (kBN / kParts), n0 = first_column<E, kBAlong, kBN>(own, t.e.n);
   const int wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * (kBM / 2), wn = (wave >> 1) * (kBN / 2 / kParts);
   const uint64_t k_first = static_cast<uint64_t>(share) * t.blocks_per_share * 64;
@@ -1302,7 +1314,7 @@ __device__ inline void split_body(const TileArgsOf<B, E>* chained, int chain, ui
 #pragma unroll
         for (int j = 0; j < kWN; ++j) acc[p][i][j] *= kSplitBack;
   }
-  finish_tile<F32, !(kAAlong && kBAlong)>(t.e, share, acc, m0 + wm, n0 + wn);
+  finish_fitted<F32, kAAlong, kBAlong>(t.e, share, acc, m0 + wm, n0 + wn, own);
 }
 
 // ------------------------------------------------------------------ launches of tiles
