@@ -177,6 +177,7 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   const size_t e = bytes_of(c.dtype);
   const uint64_t m = c.rows, k = c.in_features, n = c.out_features;
   const bool want_dw = c.dgate_w || c.dup_w;
+  const size_t dws = (c.dgate_w ? 1 : 0) + (c.dup_w ? 1 : 0);
   p.products = c.dx || want_dw;
   p.half = round_up(n, 128);  // whole tiles of the weights' gradients, whatever their size
   size_t at = 0;
@@ -252,9 +253,9 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   p.dw_at = at;
   if (want_dw && p.dw_big && e == 4) {
     p.x_part = part_bytes(p.x);
-    at += 3 * p.x_part + 2 * p.dw_parts.partial_bytes;
+    at += 3 * p.x_part + dws * p.dw_parts.partial_bytes;
   } else if (want_dw) {
-    at += p.dw_big ? p.dw.bytes() : 2 * p.dw.partial_bytes;
+    at += p.dw_big ? p.dw.bytes() : dws * p.dw.partial_bytes;
   }
   p.bytes = at;
   return p;
@@ -380,7 +381,7 @@ mscl_status_t dx_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
   return st != MSCL_SUCCESS ? st : join_gradients<F32>(j, s);
 }
 
-// Both weights' gradients; d's parts are there.
+// The weights' gradients that are wanted; d's parts are there.
 mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c, const Operand& d, char* ws,
                           hipStream_t s) {
   mscl_status_t st = split_operand(p.x, ws + p.dw_at, s);
@@ -390,15 +391,17 @@ mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
   const hipError_t err = allow_lds<&gated_dw_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   GatedDwPartsArgs a;
+  memset(&a, 0, sizeof a);
   for (int h = 0; h < 2; ++h) {
-    a.a[h] = Operand{ws + p.parts_at + h * p.half * 2, 2 * p.half, c.rows, round_up(c.out_features, 8)};
-    a.a32[h] = Operand{d.base + h * p.half * 4, d.stride, c.rows, c.out_features};
     void* to = h ? c.dup_w : c.dgate_w;
-    // a gradient that is not wanted has no rows
-    a.e[h] = results(to, h ? c.dup_w_stride : c.dgate_w_stride, to ? c.out_features : 0, c.in_features);
+    if (!to) continue;
+    const uint32_t i = a.count++;
+    a.a[i] = Operand{ws + p.parts_at + h * p.half * 2, 2 * p.half, c.rows, round_up(c.out_features, 8)};
+    a.a32[i] = Operand{d.base + h * p.half * 4, d.stride, c.rows, c.out_features};
+    a.e[i] = results(to, h ? c.dup_w_stride : c.dgate_w_stride, c.out_features, c.in_features);
     if (p.dw_parts.shares > 1)
-      a.e[h].partial = reinterpret_cast<float*>(ws + p.dw_at + 3 * p.x_part + h * p.dw_parts.partial_bytes);
-    a.e[h].partial_stride = p.dw_parts.partial_stride;
+      a.e[i].partial = reinterpret_cast<float*>(ws + p.dw_at + 3 * p.x_part + i * p.dw_parts.partial_bytes);
+    a.e[i].partial_stride = p.dw_parts.partial_stride;
   }
   a.b = parts_at(p.x, ws + p.dw_at);
   a.b32 = p.x;
@@ -406,13 +409,13 @@ mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
   a.k = c.rows;
   a.tiles_m = static_cast<uint32_t>(tm);
   a.tiles_n = static_cast<uint32_t>(tn);
-  gated_dw_parts_big<<<static_cast<uint32_t>(2 * tm * tn * p.dw_parts.shares), 512, kBigLds, s>>>(a);
+  gated_dw_parts_big<<<static_cast<uint32_t>(a.count * tm * tn * p.dw_parts.shares), 512, kBigLds, s>>>(a);
   if ((st = launched("gated_dw_parts_big")) != MSCL_SUCCESS) return st;
   GatedJoinArgs j;
   memset(&j, 0, sizeof j);
-  for (int h = 0; h < 2; ++h) {
-    j.e[h] = a.e[h];
-    j.shares[h] = p.dw_parts.shares;
+  for (uint32_t i = 0; i < a.count; ++i) {
+    j.e[i] = a.e[i];
+    j.shares[i] = p.dw_parts.shares;
   }
   return join_gradients<F32>(j, s);
 }
@@ -443,13 +446,11 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
     }
     void* to = h ? c.dup_w : c.dgate_w;
     const uint64_t stride = h ? c.dup_w_stride : c.dgate_w_stride;
-    if (dw) {
+    if (dw && to) {
       // whole tiles of columns: those past the last one meet only rows that are not stored
       const Operand side{d.base + h * p.half * e, d.stride, m, p.half};
-      a.dw[h] = fitted(
-          tile_args(p.dw, side, p.x, m, results(to, stride, to ? n : 0, k), ws + p.dw_at + h * p.dw.partial_bytes));
-      // a gradient that is not wanted has no rows, but takes its place in the launch
-      a.dw[h].tiles_m = static_cast<uint32_t>(ceil_div(n, p.dw.tile_m));
+      const uint32_t i = a.dw_count++;
+      a.dw[i] = fitted(tile_args(p.dw, side, p.x, m, results(to, stride, n, k), ws + p.dw_at + i * p.dw.partial_bytes));
     }
   }
   if (dx_tiles * p.dx.shares > kMostGroups / 8 || dw_tiles * p.dw.shares > kMostGroups / 8)
@@ -463,12 +464,12 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
   if (dw) {
     a.dw_tiles = static_cast<uint32_t>(dw_tiles);
     a.dw_groups = static_cast<uint32_t>(dw_tiles * p.dw.shares);
-    for (int h = 0; h < 2; ++h) {
-      j.e[1 + h] = a.dw[h].e;
-      j.shares[1 + h] = p.dw.shares;
+    for (uint32_t i = 0; i < a.dw_count; ++i) {
+      j.e[1 + i] = a.dw[i].e;
+      j.shares[1 + i] = p.dw.shares;
     }
   }
-  groups = uint64_t(a.dx_parts) * a.dx_groups + 2 * uint64_t(a.dw_groups);
+  groups = uint64_t(a.dx_parts) * a.dx_groups + uint64_t(a.dw_count) * a.dw_groups;
   a.db_blocks = static_cast<uint32_t>(std::max<uint64_t>(1, ceil_div(n, 32)));
   if (db) groups += 2 * uint64_t(a.db_blocks);
   if (groups == 0) return MSCL_SUCCESS;

@@ -399,10 +399,12 @@ __global__ __launch_bounds__(512, 2) void gated_dx_parts_big(const GatedDxPartsA
   finish_share(t.e, id / tiles, acc, corner);
 }
 
-// Both weights' gradients of binary32 operands in parts.
+// The weights' gradients, those of the two that are wanted, of binary32 operands
+// in parts.
 struct GatedDwPartsArgs {
   Operand a[2], b;    // parts of dz, dv and x
   Epilogue e[2];
+  uint32_t count;
   PartsOf of;
   Operand a32[2], b32;
   uint64_t k;
@@ -412,9 +414,9 @@ struct GatedDwPartsArgs {
 __global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsArgs args) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles % 2;
+  const uint32_t tiles = args.tiles_m * args.tiles_n, id = xcd_run(blockIdx.x, gridDim.x), h = id / tiles % args.count;
   const TileAt at(id % tiles, args.tiles_m, args.tiles_n);
-  const ShareOf share(args.of, id / (2 * tiles));
+  const ShareOf share(args.of, id / (args.count * tiles));
   const uint64_t m0 = static_cast<uint64_t>(at.m) * 256, n0 = static_cast<uint64_t>(at.n) * 256;
   PartCopier<Copier<BF16, false>> ca, cb;
   ca.in.init(args.a[h], m0, args.k, args.of.blocks, wave);
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(512, 2) void gated_dw_parts_big(const GatedDwPartsA
   finish_parts<false, false>(
       acc, args.e[h].m, args.e[h].n, args.k, args.of.blocks, share, corner, [&](int) -> const Operand& { return args.a32[h]; },
       [&](int, int) -> const Operand& { return args.b32; });
-  finish_share(args.e[h], id / (2 * tiles), acc, corner);
+  finish_share(args.e[h], id / (args.count * tiles), acc, corner);
 }
 
 // A gradient's sums, whose last tile of columns ends where the matrix does.
@@ -474,7 +476,7 @@ struct GatedBackArgs {
   FittedArgs dx[2], dw[2];
   JoinArgs db;
   uint32_t dx_tiles, dx_groups;  // groups of one of the two: tiles x shares
-  uint32_t dw_tiles, dw_groups;
+  uint32_t dw_tiles, dw_groups, dw_count;  // dw_count: of the two, those that are wanted
   uint32_t db_blocks;
   uint32_t dx_parts;  // 2; 1: both weights in one tile
 };
@@ -490,13 +492,13 @@ __global__ __launch_bounds__(256, 2) void gated_back(const GatedBackArgs p) {
     return;
   }
   id -= p.dx_parts * p.dx_groups;
-  if (id < 2 * p.dw_groups) {
-    id = xcd_run(id, 2 * p.dw_groups);
+  if (id < p.dw_count * p.dw_groups) {
+    id = xcd_run(id, p.dw_count * p.dw_groups);
     const uint32_t h = id / p.dw_groups, r = id % p.dw_groups;
     any_tile<C, false, false, kBM, kBN>(p.dw[h], r % p.dw_tiles, r / p.dw_tiles, lds);
     return;
   }
-  id -= 2 * p.dw_groups;
+  id -= p.dw_count * p.dw_groups;
   join_block<C>(p.db, id % p.db_blocks, id / p.db_blocks);
 }
 

@@ -35,3 +35,17 @@ def test_sizes_are_taken_into_parts(m, k, n, forward, dx, dw):
 def test_both_gradients_and_shares_are_covered():
     for at, least in ((3, {1, 2}), (4, {0, 1, 2, 4}), (5, {0, 1, 2})):
         assert least <= {size[at] for size in P.SIZES}
+
+
+IN_SHARES = [(*size[:3], M.FLOAT32) for size in P.SIZES if size[5] > 1]
+IN_SHARES += [(m, k, n, dtype) for m, k, n in ((2048, 260, 130), (4000, 100, 70)) for dtype in (M.FLOAT32, M.BFLOAT16)]
+
+
+@pytest.mark.parametrize("m,k,n,dtype", IN_SHARES)
+def test_a_weight_gradient_that_is_not_wanted_takes_no_share_of_the_workspace(m, k, n, dtype):
+    def need(*names):
+        return asked("gated_linear_backward", T.GATED_BACKWARD, m, k, n, dtype=dtype,
+                     **{g: 0 for g in GRADIENTS if g not in names})
+
+    both, gate, up = need("dgate_w", "dup_w"), need("dgate_w"), need("dup_w")
+    assert gate == up and both - gate >= P._shares(2, n, k) // 2  # a share of one of them at the least
