@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/mscl.h"
@@ -40,6 +41,11 @@ inline PairOperand pair_of(const void* gate, size_t gate_stride, const void* up,
   return PairOperand{{operand(gate, gate_stride, n, k), operand(up, up_stride, n, k)}};
 }
 // ------------------------------------------------------------------ forward products
+
+// Threads that add the shares of k of m x n results of `out` bytes each: 16 bytes a thread.
+inline double join_threads(uint64_t m, uint64_t n, size_t out) {
+  return 256 * std::ceil(static_cast<double>(ceil_div(n, 16 / out)) * m / 256);
+}
 
 // How the products of m rows with one weight or a pair of n x k run.
 struct ForwardPlan {
@@ -140,6 +146,13 @@ inline ForwardPlan plan_forward(const Operand& a, const Operand* b, int parts, u
   return p;
 }
 
+// Threads of the largest launch of a plan whose results take `out` bytes each.
+inline double threads_of(const ForwardPlan& p, uint64_t m, uint64_t n, size_t out) {
+  const double tiles = static_cast<double>(ceil_div(m, p.tile_m)) * ceil_div(n, p.outs);
+  const double products = p.kind == ForwardPlan::kTile ? 256 * tiles * p.shares : 512 * tiles;
+  return p.shares > 1 ? std::max(products, join_threads(m, n, out)) : products;
+}
+
 template <class C>
 mscl_status_t pack_any(Operand* o, char* to, hipStream_t stream) {
   if constexpr (C::kElemBytes == 2)
@@ -170,15 +183,14 @@ mscl_status_t launch_forward_tile(const TileArgsOf<B, E>& t, uint32_t groups, hi
 template <class C, class E>
 mscl_status_t join_forward(const E& e, uint32_t shares, hipStream_t stream) {
   const uint64_t joins = ceil_div(ceil_div(e.n, OutOf<E>::V) * e.m, 256);
-  if (joins > kMostGroups) return bad("the matrices have too many tiles");
   forward_join<C, E><<<static_cast<uint32_t>(joins), 256, 0, stream>>>(e, static_cast<int>(shares));
   return launched("forward_join");
 }
 
+// threads_of(p) have passed check_threads().
 template <class C, class B, class E>
 mscl_status_t forward(const ForwardPlan& p, Operand a, B b, uint64_t k, E e, char* workspace, hipStream_t stream) {
   const uint64_t tm = ceil_div(e.m, p.tile_m), tn = ceil_div(e.n, p.outs);
-  if (tm > kMostGroups / tn / p.shares) return bad("the matrices have too many tiles");
   const uint32_t groups = static_cast<uint32_t>(tm * tn);
   if constexpr (C::kElemBytes <= 2) {
     if (p.kind == ForwardPlan::kBig) {

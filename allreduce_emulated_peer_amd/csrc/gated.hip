@@ -120,6 +120,12 @@ GatedPlan plan_gated(const mscl_gated_linear_t& c) {
   return p;
 }
 
+double threads_of(const GatedPlan& p, const mscl_gated_linear_t& c) {
+  if (!p.parts.on) return threads_of(p.tiles, c.rows, c.out_features, bytes_of(c.dtype));
+  const double tiles = static_cast<double>(ceil_div(c.rows, 256)) * ceil_div(c.out_features, 128) * p.parts.shares;
+  return std::max(512 * tiles, join_threads(c.rows, c.out_features, 4));
+}
+
 mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, Gated<F32> e, char* ws, hipStream_t s) {
   const Operand x = operand(c.x, c.x_stride, c.rows, c.in_features);
   const PairOperand w = weights_of(c);
@@ -128,7 +134,6 @@ mscl_status_t gated_by_parts(const GatedPlan& p, const mscl_gated_linear_t& c, G
   for (int h = 0; h < 2 && st == MSCL_SUCCESS; ++h) st = split_operand(w.half[h], w_at + 3 * h * p.b_part, s);
   if (st != MSCL_SUCCESS) return st;
   const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.out_features, 128);
-  if (tm > kMostGroups / 8 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   if (p.parts.shares > 1) e.partial = reinterpret_cast<float*>(w_at + 6 * p.b_part);
@@ -261,6 +266,37 @@ GatedBackwardPlan plan_gated_backward(const mscl_gated_linear_backward_t& c) {
   return p;
 }
 
+// Threads of the largest launch of a backward call.
+double threads_of(const GatedBackwardPlan& p, const mscl_gated_linear_backward_t& c) {
+  const size_t e = bytes_of(c.dtype);
+  const uint64_t m = c.rows, k = c.in_features, n = c.out_features;
+  const double dws = (c.dgate_w ? 1 : 0) + (c.dup_w ? 1 : 0), across = ceil_div(k, 256);
+  double tiles = 0, joins = 0;
+  double most = 256.0 * ceil_div(p.half, 64 * (16 / e));  // the slopes
+  if (c.dx && p.dx_big) {
+    most = std::max(most, 512 * across * ceil_div(m, 256) * p.dx_parts.shares);
+    if (p.dx_parts.shares > 1) joins += join_threads(m, k, e);
+  } else if (c.dx) {
+    tiles += static_cast<double>(ceil_div(m, p.dx.tile_m)) * ceil_div(k, p.dx.tile_n) * p.dx.shares * (p.dx.shares > 1 ? 2 : 1);
+    if (p.dx.shares > 1) joins += join_threads(m, k, e);
+  }
+  if (dws && p.dw_big) {
+    most = std::max(most, 512 * across * ceil_div(n, 256) * p.dw_parts.shares * dws);
+    if (p.dw_parts.shares > 1) joins += dws * join_threads(n, k, e);
+  } else if (dws) {
+    tiles += static_cast<double>(ceil_div(n, p.dx.tile_m)) * ceil_div(k, p.dx.tile_n) * p.dw.shares * dws;
+    if (p.dw.shares > 1) joins += dws * join_threads(n, k, e);
+  }
+  if (c.dgate_bias || c.dup_bias) {
+    const double of_biases = static_cast<double>(ceil_div(n, 32));
+    if (tiles > 0)
+      tiles += 2 * of_biases;
+    else
+      most = std::max(most, 256 * of_biases);
+  }
+  return std::max({most, 256 * tiles, joins});
+}
+
 mscl_status_t check_gated_backward(const mscl_gated_linear_backward_t* c, Spans& s) {
   if (!c) return bad("call is null");
   mscl_status_t st = check_kinds(c->dtype, c->activation);
@@ -301,7 +337,6 @@ mscl_status_t join_gradients(GatedJoinArgs& j, hipStream_t s) {
     if (j.shares[i] < 2) continue;
     const uint64_t of_it = ceil_div(ceil_div(j.e[i].n, C::V) * j.e[i].m, 256);
     joins += of_it;
-    if (joins > kMostGroups) return bad("the matrices have too many tiles");
     j.groups[i] = static_cast<uint32_t>(of_it);
   }
   if (joins == 0) return MSCL_SUCCESS;
@@ -341,7 +376,6 @@ mscl_status_t dx_by_large_tiles(const GatedBackwardPlan& p, const Operand& d, co
     if (st != MSCL_SUCCESS) return st;
   }
   const uint64_t tm = ceil_div(e.m, 256), tn = ceil_div(e.n, 256);
-  if (tm > kMostGroups / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_dx_big<C>>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   const GatedDxArgs a{d, w, e, static_cast<uint32_t>(p.half / 64), static_cast<uint32_t>(tm), static_cast<uint32_t>(tn)};
@@ -358,7 +392,6 @@ mscl_status_t dx_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
     if (st != MSCL_SUCCESS) return st;
   }
   const uint64_t tm = ceil_div(c.rows, 256), tn = ceil_div(c.in_features, 256);
-  if (tm > kMostGroups / 8 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_dx_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   Epilogue e = results(c.dx, c.dx_stride, c.rows, c.in_features);
@@ -387,7 +420,6 @@ mscl_status_t dw_by_parts(const GatedBackwardPlan& p, const mscl_gated_linear_ba
   mscl_status_t st = split_operand(p.x, ws + p.dw_at, s);
   if (st != MSCL_SUCCESS) return st;
   const uint64_t tm = ceil_div(c.out_features, 256), tn = ceil_div(c.in_features, 256);
-  if (tm > kMostGroups / 16 / tn) return bad("the matrices have too many tiles");
   const hipError_t err = allow_lds<&gated_dw_parts_big>(kBigLds);
   if (err != hipSuccess) return failed_hip(err, "hipFuncSetAttribute");
   GatedDwPartsArgs a;
@@ -453,8 +485,6 @@ mscl_status_t back_by_tiles(const GatedBackwardPlan& p, const mscl_gated_linear_
       a.dw[i] = fitted(tile_args(p.dw, side, p.x, m, results(to, stride, n, k), ws + p.dw_at + i * p.dw.partial_bytes));
     }
   }
-  if (dx_tiles * p.dx.shares > kMostGroups / 8 || dw_tiles * p.dw.shares > kMostGroups / 8)
-    return bad("the matrices have too many tiles");
   if (dx) {
     a.dx_tiles = static_cast<uint32_t>(dx_tiles);
     a.dx_groups = static_cast<uint32_t>(dx_tiles * p.dx.shares);
@@ -491,8 +521,11 @@ mscl_status_t mscl_gated_linear_workspace(const mscl_gated_linear_t* call, size_
   Spans spans;
   const mscl_status_t st = check_gated(call, spans);
   if (st != MSCL_SUCCESS) return st;
-  *bytes = call->rows && call->out_features ? plan_gated(*call).bytes : 0;
-  return MSCL_SUCCESS;
+  *bytes = 0;
+  if (call->rows == 0 || call->out_features == 0) return MSCL_SUCCESS;
+  const GatedPlan p = plan_gated(*call);
+  *bytes = p.bytes;
+  return check_threads(threads_of(p, *call));
 }
 
 mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace, size_t workspace_bytes, void* stream) {
@@ -502,6 +535,7 @@ mscl_status_t mscl_gated_linear(const mscl_gated_linear_t* call, void* workspace
   const mscl_gated_linear_t& c = *call;
   if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
   const GatedPlan p = plan_gated(c);
+  if ((st = check_threads(threads_of(p, c))) != MSCL_SUCCESS) return st;
   if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
   int cus = 0;
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;
@@ -531,8 +565,9 @@ mscl_status_t mscl_gated_linear_backward_workspace(const mscl_gated_linear_backw
   Spans spans;
   const mscl_status_t st = check_gated_backward(call, spans);
   if (st != MSCL_SUCCESS) return st;
-  *bytes = plan_gated_backward(*call).bytes;
-  return MSCL_SUCCESS;
+  const GatedBackwardPlan p = plan_gated_backward(*call);
+  *bytes = p.bytes;
+  return check_threads(threads_of(p, *call));
 }
 
 mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* call, void* workspace,
@@ -542,6 +577,7 @@ mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* cal
   if (st != MSCL_SUCCESS) return st;
   const mscl_gated_linear_backward_t& c = *call;
   const GatedBackwardPlan p = plan_gated_backward(c);
+  if ((st = check_threads(threads_of(p, c))) != MSCL_SUCCESS) return st;
   if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
   const bool dx = c.dx && c.rows && c.in_features;
   const bool dw = (c.dgate_w || c.dup_w) && c.out_features && c.in_features;
@@ -568,7 +604,6 @@ mscl_status_t mscl_gated_linear_backward(const mscl_gated_linear_backward_t* cal
   g.rows_per_group = p.rows_per_group;
   g.act = c.activation;
   const uint64_t blocks = ceil_div(p.half, 64 * (16 / e));
-  if (blocks > kMostGroups) return bad("the matrices have too many tiles");
   if (blocks) {
     st = with_codec(c.dtype, [&](auto t) {
       gated_slope<decltype(t)><<<dim3(static_cast<uint32_t>(blocks), p.groups), 256, 0, s>>>(g);

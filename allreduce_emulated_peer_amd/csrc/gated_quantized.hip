@@ -55,8 +55,11 @@ mscl_status_t mscl_gated_linear_quantized_workspace(const mscl_gated_linear_quan
   Spans spans;
   const mscl_status_t st = check_gated_int8(call, spans);
   if (st != MSCL_SUCCESS) return st;
-  *bytes = call->rows && call->out_features ? plan_gated_int8(*call).bytes : 0;
-  return MSCL_SUCCESS;
+  *bytes = 0;
+  if (call->rows == 0 || call->out_features == 0) return MSCL_SUCCESS;
+  const ForwardPlan p = plan_gated_int8(*call);
+  *bytes = p.bytes;
+  return check_threads(threads_of(p, call->rows, call->out_features, bytes_of(call->dtype)));
 }
 
 mscl_status_t mscl_gated_linear_quantized(const mscl_gated_linear_quantized_t* call, void* workspace, size_t workspace_bytes,
@@ -67,6 +70,7 @@ mscl_status_t mscl_gated_linear_quantized(const mscl_gated_linear_quantized_t* c
   const mscl_gated_linear_quantized_t& c = *call;
   if (c.rows == 0 || c.out_features == 0) return MSCL_SUCCESS;
   const ForwardPlan p = plan_gated_int8(c);
+  if ((st = check_threads(threads_of(p, c.rows, c.out_features, bytes_of(c.dtype)))) != MSCL_SUCCESS) return st;
   if ((st = spans.check_workspace(workspace, workspace_bytes, p.bytes)) != MSCL_SUCCESS) return st;
   int cus = 0;
   if ((st = current_device(&cus)) != MSCL_SUCCESS) return st;

@@ -600,6 +600,9 @@ mscl_status_t mscl_layer_norm_backward_workspace(const mscl_layer_norm_backward_
  * The gated feed-forward block of a tensor-parallel layer, and the 8-bit
  * integer products by which such layers are served.  What is said above of
  * the operators' matrices, sums, streams, workspaces and errors holds here too.
+ * rows, in_features and out_features are at most 2^31 - 1, and one launch of a
+ * product is to hold all of its tiles: sizes that need 2^32 threads or more (one row by 2^27 outputs, 2^38
+ * results of large matrices) are INVALID_ARGUMENT, to the workspace function too.
  */
 typedef struct {
   const void* x;         /* [rows][in_features] */
