@@ -323,7 +323,7 @@ def _need_torch():
 
             @staticmethod
             def backward(ctx, *grads):
-                if "quantize" in ctx.name:
+                if "quantize" in ctx.name or "backward" in ctx.name:
                     raise RuntimeError(f"{ctx.name}_tensors has no gradient: call it under torch.no_grad() or detach what "
                                        "it takes or returns")
                 raise RuntimeError(f"{ctx.name}_tensors is not part of autograd's graph: run {ctx.name}_backward_tensors, and "
@@ -730,7 +730,9 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
 
     dy is the gradient of y (..., out); gate and up are what
     gated_linear_tensors returned with return_preacts.  Gradients that are not
-    needed are None (need_dw: both weights', need_db: both biases').
+    needed are None (need_dw: both weights', need_db: both biases').  There is no
+    second derivative: where an input requires a gradient, so do the results, and
+    a backward pass through them raises.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
     kind = dy.dtype
@@ -755,10 +757,13 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
     zm, um = _matrix("gate", gate, n), _matrix("up", up, n)
     rows = gm.shape[0]
 
+    inputs = (dy, x, gate_weight, up_weight, gate, up)
     if stream is not None or index != _device():
-        return _elsewhere(dy.device, stream, (dy, x, gate_weight, up_weight, gate, up),
-                          lambda: gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activation,
-                                                                need_dx, need_dw, need_db))
+        return _elsewhere(dy.device, stream, inputs,
+                          lambda: gated_linear_backward_tensors(*inputs, activation, need_dx, need_dw, need_db))
+    if torch.is_grad_enabled() and _any_grad(inputs):
+        return _outside_autograd(lambda: gated_linear_backward_tensors(*inputs, activation, need_dx, need_dw, need_db),
+                                 "gated_linear_backward", *inputs)
     dx = _fresh((rows, k), (k, 1), kind) if need_dx else None
     dgw, duw = (_fresh((n, k), (k, 1), kind), _fresh((n, k), (k, 1), kind)) if need_dw else (None, None)
     dgb, dub = (_fresh((n,), (1,), kind), _fresh((n,), (1,), kind)) if need_db else (None, None)
