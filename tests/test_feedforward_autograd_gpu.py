@@ -73,3 +73,51 @@ def test_a_function_of_ones_own_has_a_first_derivative_and_no_second():
     dx, = torch.autograd.grad(Gated.apply(x, wg, wu).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="no gradient"):
         dx.square().sum().backward()
+
+
+def _calls():
+    """name -> (call, its inputs), each with all optional inputs."""
+    dy, x, wg, wu, z, v = tensors()
+    b, r = dy[0].clone(), dy.clone()
+    q, s = M.quantize_tensors(x)
+    (qg, sg), (qu, su) = M.quantize_tensors(wg), M.quantize_tensors(wu)
+    g = x[0].clone()
+    y, mean, rstd = M.layer_norm_tensors(x, g, return_stats=True)
+    t = torch.float32
+    return {
+        "gated_linear": (lambda x, wg, wu, bg, bu, **k: M.gated_linear_tensors(x, wg, wu, bg, bu, **k), (x, wg, wu, b, b)),
+        "gated_linear_backward": (lambda *a, **k: M.gated_linear_backward_tensors(*a, **k)[0], (dy, x, wg, wu, z, v)),
+        "quantize": (lambda x, **k: M.quantize_tensors(x, **k)[1], (x,)),
+        "linear_quantized": (lambda s, sw, b, r, **k: M.linear_quantized_tensors(q, s, qg, sw, b, r, dtype=t, **k), (s, sg, b, r)),
+        "gated_linear_quantized": (lambda s, sg, su, bg, bu, **k: M.gated_linear_quantized_tensors(
+            q, s, qg, sg, qu, su, bg, bu, dtype=t, **k), (s, sg, su, b, b)),
+        "linear": (lambda *a, **k: M.linear_tensors(*a, **k), (x, wg, b, r)),
+        "linear_backward": (lambda dy, x, w, z, **k: M.linear_backward_tensors(dy, x, w, z, "gelu", **k)[0], (dy, x, wg, z)),
+        "layer_norm": (lambda *a, **k: M.layer_norm_tensors(*a, **k), (x, g, g)),
+        "layer_norm_backward": (lambda *a, **k: M.layer_norm_backward_tensors(*a, **k)[0], (x, y, mean, rstd, g)),
+    }
+
+
+@pytest.mark.parametrize("name", ["gated_linear", "gated_linear_backward", "quantize", "linear_quantized",
+                                  "gated_linear_quantized", "linear", "linear_backward", "layer_norm", "layer_norm_backward"])
+def test_a_forward_mode_tangent_is_not_lost_unseen(name):
+    call, args = _calls()[name]
+    note("forward-mode tangent", name)
+    want = call(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.autograd.forward_ad.dual_level():
+        for which in range(len(args)):
+            some = list(args)
+            some[which] = torch.autograd.forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+            for more in ({}, {"stream": side}):
+                with pytest.raises(RuntimeError, match=f"^{name}_tensors has no forward-mode derivative"):
+                    call(*some, **more)
+            with torch.no_grad(), pytest.raises(RuntimeError, match="forward-mode"):
+                call(*some)
+        # tensors without a tangent go through inside of a dual level too
+        assert torch.equal(call(*args), want)
+    assert torch.equal(call(*args), want)
+    if name != "quantize":
+        with pytest.raises(RuntimeError):
+            torch.func.jvp(lambda a: call(a, *args[1:]), (args[0],), (torch.ones_like(args[0]),))
