@@ -304,13 +304,13 @@ _torch = None
 _CODES = {}  # torch dtype -> element type code
 _raw_stream = None
 _device = None
-_fresh = None
+_allocator = None
 _outside_autograd = None
 _forward_ad = None
 
 
 def _need_torch():
-    global _torch, _raw_stream, _device, _fresh, _outside_autograd, _forward_ad
+    global _torch, _raw_stream, _device, _allocator, _outside_autograd, _forward_ad
     if _torch is None:
         import torch
 
@@ -338,11 +338,29 @@ def _need_torch():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        # (size, stride, dtype) on the current device: 0.8 us, torch.empty 1.6, where torch has it
-        _fresh = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or (
-            lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
+        _allocator = _allocators(torch)
         _torch = torch
     return _torch
+
+
+def _allocators(torch):
+    """What gives a call its allocator: (size, stride, dtype) -> a new tensor on the current device.
+
+    torch's entry past its dispatcher takes 0.75 us where torch.empty_strided takes
+    1.25; it is used where torch has it and nothing would miss the allocation: no
+    dispatch or function mode that watches, no filling of fresh memory.
+    """
+    quick = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+    dispatching = getattr(torch._C, "_len_torch_dispatch_stack", None)
+    calling = getattr(torch._C, "_len_torch_function_stack", None)
+    filling = torch.are_deterministic_algorithms_enabled
+
+    def seen(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+    if quick is None or dispatching is None or calling is None:
+        return lambda: seen
+    return lambda: seen if dispatching() or calling() or filling() else quick
 
 
 def _same_kind(like, name, t):
@@ -651,14 +669,14 @@ def _apart(like, name, t):
     raise ValueError(f"{name} must be on {like.device}")
 
 
-def _space(query, call):
-    """_workspace on the current device, from a *_workspace function and its name."""
+def _space(query, call, fresh):
+    """_workspace on the current device, from a *_workspace function and an allocator."""
     need = ctypes.c_size_t()
     status = query(call, ctypes.byref(need))
     if status:
         _check(status, query.__name__)
     size = need.value
-    return (_fresh((size,), (1,), _torch.uint8), size) if size else (None, 0)
+    return (fresh((size,), (1,), _torch.uint8), size) if size else (None, 0)
 
 
 def _pair_of_weights(like, index, gate_weight, up_weight):
@@ -726,13 +744,13 @@ def gated_linear_tensors(x, gate_weight, up_weight, gate_bias=None, up_bias=None
         return _elsewhere(x.device, stream, inputs, lambda: gated_linear_tensors(*inputs, activation, return_preacts))
     if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: gated_linear_tensors(*inputs, activation, return_preacts), "gated_linear", *inputs)
-    size, stride = (rows, n), (n, 1)
-    y = _fresh(size, stride, kind)
-    gate, up = (_fresh(size, stride, kind), _fresh(size, stride, kind)) if return_preacts else (None, None)
+    size, stride, fresh = (rows, n), (n, 1), _allocator()
+    y = fresh(size, stride, kind)
+    gate, up = (fresh(size, stride, kind), fresh(size, stride, kind)) if return_preacts else (None, None)
     call = GATED_LINEAR.pack(xm.data_ptr(), xm.stride(0), gm.data_ptr(), gm.stride(0), um.data_ptr(), um.stride(0),
                              _address(gate_bias), _address(up_bias), y.data_ptr(), n, _address(gate), n, _address(up), n,
                              rows, k, n, dtype, act)
-    space, size = _space(lib.mscl_gated_linear_workspace, call)
+    space, size = _space(lib.mscl_gated_linear_workspace, call, fresh)
     status = lib.mscl_gated_linear(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear")
@@ -782,14 +800,15 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
     if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: gated_linear_backward_tensors(*inputs, activation, need_dx, need_dw, need_db),
                                  "gated_linear_backward", *inputs)
-    dx = _fresh((rows, k), (k, 1), kind) if need_dx else None
-    dgw, duw = (_fresh((n, k), (k, 1), kind), _fresh((n, k), (k, 1), kind)) if need_dw else (None, None)
-    dgb, dub = (_fresh((n,), (1,), kind), _fresh((n,), (1,), kind)) if need_db else (None, None)
+    fresh = _allocator()
+    dx = fresh((rows, k), (k, 1), kind) if need_dx else None
+    dgw, duw = (fresh((n, k), (k, 1), kind), fresh((n, k), (k, 1), kind)) if need_dw else (None, None)
+    dgb, dub = (fresh((n,), (1,), kind), fresh((n,), (1,), kind)) if need_db else (None, None)
     call = GATED_LINEAR_BACKWARD.pack(
         gm.data_ptr(), gm.stride(0), xm.data_ptr(), xm.stride(0), wm.data_ptr(), wm.stride(0), vm.data_ptr(), vm.stride(0),
         zm.data_ptr(), zm.stride(0), um.data_ptr(), um.stride(0), _address(dx), k, _address(dgw), k, _address(duw), k,
         _address(dgb), _address(dub), rows, k, n, dtype, act)
-    space, size = _space(lib.mscl_gated_linear_backward_workspace, call)
+    space, size = _space(lib.mscl_gated_linear_backward_workspace, call, fresh)
     status = lib.mscl_gated_linear_backward(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear_backward")
@@ -824,7 +843,8 @@ def quantize_tensors(x, stream=None):
         return _elsewhere(x.device, stream, (x,), lambda: quantize_tensors(x))
     if x.requires_grad and torch.is_grad_enabled():
         return _outside_autograd(lambda: quantize_tensors(x), "quantize", x)
-    q, scale = _fresh((rows, width), (width, 1), torch.int8), _fresh((rows,), (1,), torch.float32)
+    fresh = _allocator()
+    q, scale = fresh((rows, width), (width, 1), torch.int8), fresh((rows,), (1,), torch.float32)
     call = QUANTIZE.pack(xm.data_ptr(), xm.stride(0), q.data_ptr(), width, scale.data_ptr(), rows, width, dtype)
     status = lib.mscl_quantize(call, _raw_stream(index) or None)
     if status:
@@ -887,11 +907,12 @@ def linear_quantized_tensors(x, x_scale, weight, weight_scale, bias=None, residu
         return _elsewhere(x.device, stream, inputs, lambda: linear_quantized_tensors(*inputs, activation, dtype))
     if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: linear_quantized_tensors(*inputs, activation, dtype), "linear_quantized", *inputs)
-    y = _fresh((rows, n), (n, 1), dtype)
+    fresh = _allocator()
+    y = fresh((rows, n), (n, 1), dtype)
     call = LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), wm.data_ptr(), wm.stride(0),
                                  weight_scale.data_ptr(), _address(bias), _address(rm), _row_stride(rm), y.data_ptr(), n,
                                  rows, k, n, code, act)
-    space, size = _space(lib.mscl_linear_quantized_workspace, call)
+    space, size = _space(lib.mscl_linear_quantized_workspace, call, fresh)
     status = lib.mscl_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_linear_quantized")
@@ -935,11 +956,12 @@ def gated_linear_quantized_tensors(x, x_scale, gate_weight, gate_scale, up_weigh
     if torch.is_grad_enabled() and _any_grad(inputs):
         return _outside_autograd(lambda: gated_linear_quantized_tensors(*inputs, activation, dtype),
                                  "gated_linear_quantized", *inputs)
-    y = _fresh((rows, n), (n, 1), dtype)
+    fresh = _allocator()
+    y = fresh((rows, n), (n, 1), dtype)
     call = GATED_LINEAR_QUANTIZED.pack(xm.data_ptr(), xm.stride(0), x_scale.data_ptr(), gm.data_ptr(), gm.stride(0),
                                        gate_scale.data_ptr(), um.data_ptr(), um.stride(0), up_scale.data_ptr(),
                                        _address(gate_bias), _address(up_bias), y.data_ptr(), n, rows, k, n, code, act)
-    space, size = _space(lib.mscl_gated_linear_quantized_workspace, call)
+    space, size = _space(lib.mscl_gated_linear_quantized_workspace, call, fresh)
     status = lib.mscl_gated_linear_quantized(call, _address(space), size, _raw_stream(index) or None)
     if status:
         _check(status, "mscl_gated_linear_quantized")
