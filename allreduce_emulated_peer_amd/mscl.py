@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import types
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmscl.so")
@@ -306,11 +307,11 @@ _raw_stream = None
 _device = None
 _allocator = None
 _outside_autograd = None
-_forward_ad = None
+_dual = None  # its _current_level is below 0 outside of every dual level of forward-mode derivatives
 
 
 def _need_torch():
-    global _torch, _raw_stream, _device, _allocator, _outside_autograd, _forward_ad
+    global _torch, _raw_stream, _device, _allocator, _outside_autograd, _dual
     if _torch is None:
         import torch
 
@@ -331,7 +332,9 @@ def _need_torch():
                                    "call it under torch.no_grad() or detach what it takes or returns")
 
         _outside_autograd = OutsideAutograd.apply
-        _forward_ad = torch.autograd.forward_ad
+        _dual = torch.autograd.forward_ad
+        if not hasattr(_dual, "_current_level"):
+            _dual = types.SimpleNamespace(_current_level=0)  # look at each tensor
 
         _CODES.update({torch.float32: FLOAT32, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16})
         # the current stream's handle without a Stream object around it (2 us less), where torch has that
@@ -395,11 +398,8 @@ def _vector(name, t, n):
 
 def _refuse_tangents(name, tensors):
     """Raises for a tensor with a forward-mode tangent, which would be lost; unlike requires_grad, no_grad() hides none."""
-    # outside of every dual level (where torch says so) there are none: 0.1 us, a look at each tensor 3
-    if getattr(_forward_ad, "_current_level", 0) < 0:
-        return
     for t in tensors:
-        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+        if t is not None and _torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{name}_tensors has no forward-mode derivative: take the primal of what it is given")
 
 
@@ -472,7 +472,8 @@ def linear_tensors(x, weight, bias=None, residual=None, activation="none", retur
             raise ValueError(f"residual must be {tuple(x.shape[:-1]) + (n,)}")
         rm = _matrix("residual", residual, n)
 
-    _refuse_tangents("linear", (x, weight, bias, residual))
+    if _dual._current_level >= 0:
+        _refuse_tangents("linear", (x, weight, bias, residual))
     index = x.device.index
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(x.device, stream, (x, weight, bias, residual),
@@ -532,7 +533,8 @@ def linear_backward_tensors(dy, x, weight, preact=None, activation="none", need_
             raise ValueError("preact must have dy's shape")
         zm = _matrix("preact", preact, n)
 
-    _refuse_tangents("linear_backward", (dy, x, weight, preact))
+    if _dual._current_level >= 0:
+        _refuse_tangents("linear_backward", (dy, x, weight, preact))
     index = dy.device.index
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(dy.device, stream, (dy, x, weight, preact),
@@ -591,7 +593,8 @@ def layer_norm_tensors(x, weight=None, bias=None, eps=1e-5, return_stats=False, 
     xm = _matrix("x", x, width)
     rows = xm.shape[0]
 
-    _refuse_tangents("layer_norm", (x, weight, bias))
+    if _dual._current_level >= 0:
+        _refuse_tangents("layer_norm", (x, weight, bias))
     index = x.device.index
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(x.device, stream, (x, weight, bias),
@@ -641,7 +644,8 @@ def layer_norm_backward_tensors(dy, x, mean, rstd, weight=None, need_dx=True, ne
     gm, xm = _matrix("dy", dy, width), _matrix("x", x, width)
     rows = gm.shape[0]
 
-    _refuse_tangents("layer_norm_backward", (dy, x, mean, rstd, weight))
+    if _dual._current_level >= 0:
+        _refuse_tangents("layer_norm_backward", (dy, x, mean, rstd, weight))
     index = dy.device.index
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(dy.device, stream, (dy, x, mean, rstd, weight),
@@ -739,7 +743,8 @@ def gated_linear_tensors(x, gate_weight, up_weight, gate_bias=None, up_bias=None
     rows = xm.shape[0]
 
     inputs = (x, gate_weight, up_weight, gate_bias, up_bias)
-    _refuse_tangents("gated_linear", inputs)
+    if _dual._current_level >= 0:
+        _refuse_tangents("gated_linear", inputs)
     if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: gated_linear_tensors(*inputs, activation, return_preacts))
     if torch.is_grad_enabled() and _any_grad(inputs):
@@ -793,7 +798,8 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
     rows = gm.shape[0]
 
     inputs = (dy, x, gate_weight, up_weight, gate, up)
-    _refuse_tangents("gated_linear_backward", inputs)
+    if _dual._current_level >= 0:
+        _refuse_tangents("gated_linear_backward", inputs)
     if stream is not None or index != _device():
         return _elsewhere(dy.device, stream, inputs,
                           lambda: gated_linear_backward_tensors(*inputs, activation, need_dx, need_dw, need_db))
@@ -838,7 +844,8 @@ def quantize_tensors(x, stream=None):
     xm = _matrix("x", x, width)
     rows = xm.shape[0]
 
-    _refuse_tangents("quantize", (x,))
+    if _dual._current_level >= 0:
+        _refuse_tangents("quantize", (x,))
     if stream is not None or index != _device():
         return _elsewhere(x.device, stream, (x,), lambda: quantize_tensors(x))
     if x.requires_grad and torch.is_grad_enabled():
@@ -902,7 +909,8 @@ def linear_quantized_tensors(x, x_scale, weight, weight_scale, bias=None, residu
         rm = _matrix("residual", residual, n)
 
     inputs = (x, x_scale, weight, weight_scale, bias, residual)
-    _refuse_tangents("linear_quantized", inputs)
+    if _dual._current_level >= 0:
+        _refuse_tangents("linear_quantized", inputs)
     if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: linear_quantized_tensors(*inputs, activation, dtype))
     if torch.is_grad_enabled() and _any_grad(inputs):
@@ -950,7 +958,8 @@ def gated_linear_quantized_tensors(x, x_scale, gate_weight, gate_scale, up_weigh
     rows = xm.shape[0]
 
     inputs = (x, x_scale, gate_weight, gate_scale, up_weight, up_scale, gate_bias, up_bias)
-    _refuse_tangents("gated_linear_quantized", inputs)
+    if _dual._current_level >= 0:
+        _refuse_tangents("gated_linear_quantized", inputs)
     if stream is not None or index != _device():
         return _elsewhere(x.device, stream, inputs, lambda: gated_linear_quantized_tensors(*inputs, activation, dtype))
     if torch.is_grad_enabled() and _any_grad(inputs):
