@@ -356,7 +356,7 @@ def _allocators(torch):
     quick = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
     dispatching = getattr(torch._C, "_len_torch_dispatch_stack", None)
     calling = getattr(torch._C, "_len_torch_function_stack", None)
-    filling = torch.are_deterministic_algorithms_enabled
+    filling = getattr(torch._C, "_get_deterministic_algorithms", torch.are_deterministic_algorithms_enabled)
 
     def seen(size, stride, dtype):
         return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
@@ -772,7 +772,9 @@ def gated_linear_backward_tensors(dy, x, gate_weight, up_weight, gate, up, activ
     gated_linear_tensors returned with return_preacts.  Gradients that are not
     needed are None (need_dw: both weights', need_db: both biases').  There is no
     second derivative: where an input requires a gradient, so do the results, and
-    a backward pass through them raises.
+    a backward pass through them raises.  The gradients of both products are
+    rounded to dy's dtype on the way to dx and the weights': in float16 scale dy
+    where they may be below 2^-14.
     """
     torch, lib = _torch or _need_torch(), _lib or load()
     kind = dy.dtype

@@ -666,7 +666,9 @@ typedef struct {
  *   dgate_bias and dup_bias = the columns' sums of dg and du.
  * dg and du are rounded to the element type before the matrix products, as
  * the matrix units take that type (the biases' gradients are summed from the
- * unrounded values): a binary16 value above 65504 becomes infinite.  At gate =
+ * unrounded values): a binary16 value above 65504 becomes infinite, one of at
+ * most 2^-25 becomes 0 and one below 2^-14 keeps fewer bits, so that small binary16
+ * gradients reach dx and the weights only if dy is scaled, as a loss is.  At gate =
  * 0 the slope of RELU is 0.  rows 0: the weights' and biases' gradients are 0;
  * out_features 0: dx is 0.
  */
