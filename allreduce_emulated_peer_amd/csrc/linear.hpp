@@ -822,19 +822,23 @@ __device__ __forceinline__ void finish_fitted(const E& e, uint64_t share, const 
   finish_tile<C, kPlain>(e, share, acc, m0, n0);
 }
 
-// A chain of one product is a constant and no loop: around a loop the compiler adds
-// up the LDS addresses in every block again (1001 x 2047 -> 1537 fp32 57.2 us
-// against 55.6, gradients of 515 x 1025 x 770 fp16 22.8 against 22.2).
-using Single = std::integral_constant<int, 1>;
+// Whether a tile's walk over its blocks is a loop over a chain of products.  With
+// one around it the compiler keeps fewer LDS addresses in registers and adds them
+// up in every block again.  That costs the linear layer's tiles 3% (1001 x 2047 ->
+// 1537 fp32 57.2 us against 55.6, gradients of 515 x 1025 x 770 fp16 22.8 against
+// 22.2) and saves those with kFit registers that they lack (1024 x 2048 -> 1024
+// pairs of bf16 17.5 us, 215 registers; without the loop 20.7, 256 and scratch).
+template <class E>
+constexpr bool kChains = Fits<E>::value;
 
 // Any sizes, strides and alignments of a 16-bit type: kBM x kBN tiles by 4
 // waves in a square, 64 k at a time, two LDS buffers.  The next kDeep blocks'
 // loads are in flight in registers.
 // Of a pair of weights a tile has kBN / 2 columns of each.
 // `chain` products of one size, chained[0] .. chained[chain - 1], are summed into
-// one tile.
-template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E, class Chain>
-__device__ inline void tile_body(const TileArgsOf<B, E>* chained, Chain chain, uint32_t tile, uint32_t share, char* lds) {
+// one tile; more than one only where kChains.
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
+__device__ inline void tile_body(const TileArgsOf<B, E>* chained, int chain, uint32_t tile, uint32_t share, char* lds) {
   const TileArgsOf<B, E>& t = chained[0];
   using SA = Stage<C, kAAlong, kBM, 256>;
   using SB = Stage<C, kBAlong, kBN, 256>;
@@ -886,7 +890,7 @@ __device__ inline void tile_body(const TileArgsOf<B, E>* chained, Chain chain, u
           for (int j = 0; j < kWN; ++j) acc[p][i][j] = multiply<C>(fb[p][j], fa[i], acc[p][i][j]);
     }
   };
-  if constexpr (std::is_same<Chain, Single>::value) {
+  if constexpr (!kChains<E>) {
     walk<kDeep, 2, Fits<E>::value>(t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb, store, compute);
   } else {
     for (int h = 0; h < chain; ++h) {
@@ -1215,8 +1219,8 @@ __device__ inline float value_at(const Operand& o, uint64_t i, uint64_t k, uint6
 // three planes of it let two workgroups share a compute unit: one splits and
 // stores while the other multiplies.  kDeep blocks' loads are in flight, as in
 // linear_tile.
-template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E, class Chain>
-__device__ inline void split_body(const TileArgsOf<B, E>* chained, Chain chain, uint32_t tile, uint32_t share, char* lds) {
+template <bool kAAlong, bool kBAlong, int kBM, int kBN, int kDeep, class B, class E>
+__device__ inline void split_body(const TileArgsOf<B, E>* chained, int chain, uint32_t tile, uint32_t share, char* lds) {
   const TileArgsOf<B, E>& t = chained[0];
   using SA = SplitStage<kAAlong, kBM>;
   using SB = SplitStage<kBAlong, kBN>;
@@ -1275,7 +1279,7 @@ __device__ inline void split_body(const TileArgsOf<B, E>* chained, Chain chain, 
       }
     }
   };
-  if constexpr (std::is_same<Chain, Single>::value) {
+  if constexpr (!kChains<E>) {
     walk<kDeep, 1, Fits<E>::value>(t, m0, n0, k_first, k_end, feed_a, feed_b, sa, sb, store, compute);
   } else {
     for (int h = 0; h < chain; ++h) {
@@ -1340,8 +1344,8 @@ constexpr int tile_lds() {
     return 2 * (Stage<C, kAAlong, kBM, 256>::kBytes + Stage<C, kBAlong, kBN, 256>::kBytes);
 }
 
-template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, class B, class E, class Chain = Single>
-__device__ inline void any_tile(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds, Chain chain = {}) {
+template <class C, bool kAAlong, bool kBAlong, int kBM, int kBN, class B, class E>
+__device__ inline void any_tile(const TileArgsOf<B, E>& t, uint32_t tile, uint32_t share, char* lds, int chain = 1) {
   if constexpr (C::kElemBytes == 4)
     split_body<kAAlong, kBAlong, kBM, kBN, 1>(&t, chain, tile, share, lds);
   else
