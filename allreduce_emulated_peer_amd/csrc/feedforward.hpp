@@ -259,8 +259,8 @@ __device__ __forceinline__ void finish_few(const E& e, const SumOf<C> (&sums)[4]
 
 // ------------------------------------------------------------------ forward kernels
 
-// Any sizes, strides and alignments.  1024 x 2048 -> 1024 8 bits 8.8 us, pairs of
-// bf16 19; 1001 x 2047 -> 1537 at odd addresses 20 us (8 bits), pairs of binary32
+// Any sizes, strides and alignments.  1024 x 2048 -> 1024 8 bits 9.1 us, pairs of
+// bf16 17.5; 1001 x 2047 -> 1537 at odd addresses 20 us (8 bits), pairs of binary32
 // 97 us (131 TFLOP/s), where splitting and multiplying share the time.
 template <class C, int kBM, int kBN, class B, class E>
 __global__ __launch_bounds__(256, 2) void forward_tile(const TileArgsOf<B, E> t) {
@@ -362,9 +362,9 @@ __device__ inline PairCopier<C> copier_of(const PairOperand&) {
 // linear.hpp's 256 x 256 tiles with these operands and epilogues.  Of a pair a
 // tile has 128 columns of each weight, in quarters (i, 0) and (i, 1).  What
 // bounds it is the matrix units: 8192 x 8192 -> 4096 pairs of bf16 with both sums
-// kept 735 to 770 us (1430 to 1500 TFLOP/s, MFMA busy 79% of the cycles), of 8
-// bits 370 to 390 us (2.8 to 3.0 POP/s); 8 bits 8192 x 4096 -> 8192 with a
-// residual 241 to 248 us, where stores and residual take a fifth.
+// kept 735 to 780 us (1410 to 1500 TFLOP/s, MFMA busy 79% of the cycles), of 8
+// bits 370 to 400 us (2.75 to 3.0 POP/s); 8 bits 8192 x 4096 -> 8192 with a
+// residual 241 to 252 us, where stores and residual take a fifth.
 template <class C, class B, class E>
 __global__ __launch_bounds__(512, 2) void forward_big(const BigArgsOf<B, E> args) {
   constexpr int kParts = B::kParts;

@@ -58,7 +58,7 @@ mscl_status_t split_operand(const Operand& o, char* to, hipStream_t s) {
 // the parts themselves, 10 bytes a value) are a pass over memory at 5 TB/s.
 // forward_tile, which takes operands into parts in every tile, reaches 130 to 165
 // TFLOP/s.  Forward, us by parts and by those tiles: 1024 x 4096 -> 4096
-// 389 and 509, 2048 x 2048 -> 2048 203 and 260, 512 x 4096 -> 4096 249 and 205.
+// 376 and 509, 2048 x 2048 -> 2048 203 and 260, 512 x 4096 -> 4096 249 and 205.
 struct PartsPlan {
   bool on = false;
   uint32_t blocks = 0, blocks_per_share = 0, shares = 1;

@@ -154,8 +154,8 @@ struct GatedPartsArgs {
   uint64_t k;
 };
 
-// 4096 x 4096 -> 4096: 1186 us with the parts (232 TFLOP/s; a binary32 library
-// product 153).
+// 4096 x 4096 -> 4096: 1190 to 1215 us with the parts (226 to 232 TFLOP/s; a
+// binary32 library product 153).
 __global__ __launch_bounds__(512, 2) void gated_parts_big(const GatedPartsArgs args) {
   const auto& t = args.parts;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -334,8 +334,8 @@ struct GatedDxArgs {
 };
 
 // dx = dz wg + dv wu: one product whose k runs over both, so that no sums are
-// written and read again in between.  8192 x 8192 x 4096 bf16: 746 to 773 us
-// (1420 to 1470 TFLOP/s), bounded as linear_big.
+// written and read again in between.  8192 x 8192 x 4096 bf16: 746 to 777 us
+// (1415 to 1470 TFLOP/s), bounded as linear_big.
 template <class C>
 __global__ __launch_bounds__(512, 2) void gated_dx_big(const GatedDxArgs args) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
