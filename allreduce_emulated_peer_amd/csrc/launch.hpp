@@ -178,9 +178,10 @@ inline uint64_t round_up(uint64_t a, uint64_t b) { return ceil_div(a, b) * b; }
 // Grids are 32-bit; sizes beyond them are refused, not cut.
 constexpr uint64_t kMostGroups = 0x7fffffffu;
 
-// Nor has a launch 2^32 threads or more.  A plan that needs one is refused where
-// it is made, by the workspace query too; `threads` (not always whole in 64 bits)
-// are those of its largest launch.
+// Nor has a launch 2^32 threads or more.  The gated block and the 8-bit products
+// refuse a plan that needs one where it is made, by the workspace query too (the
+// linear layer and layer norm return HIP's error at the launch); `threads` (not
+// always whole in 64 bits) are those of its largest launch.
 inline mscl_status_t check_threads(double threads) {
   return threads < 4294967296.0 ? MSCL_SUCCESS : bad("the matrices have too many tiles for a launch");
 }
